@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librecis.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-SOURCES = ["table.hip", "lookup.hip", "fwd_bwd.hip", "maint.hip"]
+SOURCES = ["table.hip", "lookup.hip", "fwd_bwd.hip", "maint.hip", "embed.hip", "norm.hip", "attn.hip"]
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
     # packed fp32 instructions stay off: hipcc must not form v_pk_* fp32 ops

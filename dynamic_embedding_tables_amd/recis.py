@@ -55,6 +55,9 @@ EXPORTED_SYMBOLS = (
     "recis_writeback", "recis_idmap_export", "recis_idmap_import", "recis_idmap_key_ages", "recis_idmap_sketch",
     "recis_idmap_stats", "recis_get_error",
     "recis_status_string", "recis_profile_kernel",
+    "recis_embed_fwd", "recis_embed_bwd_workspace_bytes", "recis_embed_bwd",
+    "recis_layernorm_fwd", "recis_layernorm_bwd_workspace_bytes", "recis_layernorm_bwd",
+    "recis_cross_attn_workspace_bytes", "recis_cross_attn_fwd", "recis_cross_attn_bwd",
 )
 
 
@@ -96,6 +99,16 @@ class recis_table_stats(C.Structure):
                 ("bytes", C.c_int64), ("probationary_keys", C.c_int64), ("claim_attempts", C.c_int64),
                 ("claim_failures", C.c_int64), ("hbm_rows", C.c_int64),
                 ("lookup_pairs", C.c_int64), ("hot_keys", C.c_int64)]
+
+
+class recis_attn_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("q_len", C.c_int32), ("kv_len", C.c_int32),
+                ("q_heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("scale", C.c_float),
+                ("q_strides", C.c_int64 * 3), ("k_strides", C.c_int64 * 3), ("v_strides", C.c_int64 * 3),
+                ("o_strides", C.c_int64 * 3), ("do_strides", C.c_int64 * 3), ("dq_strides", C.c_int64 * 3),
+                ("dk_strides", C.c_int64 * 3), ("dv_strides", C.c_int64 * 3),
+                ("kv_lens", C.c_void_p), ("kv_offsets", C.c_void_p), ("kv_rows", C.c_int64),
+                ("kv_mask", C.c_void_p), ("mask_stride", C.c_int64), ("error", C.c_void_p)]
 
 
 class RecisError(RuntimeError):
@@ -143,6 +156,19 @@ def load_library() -> C.CDLL:
     L.recis_idmap_stats.argtypes = [p, C.POINTER(recis_table_stats), p]
     L.recis_get_error.argtypes = [p, p]
     L.recis_profile_kernel.argtypes = [p, C.c_char_p, p, p]
+    f32 = C.c_float
+    L.recis_embed_fwd.argtypes = [p, i64, p, i32, i64, i32, i64, f32, p, i64, p, p]
+    L.recis_embed_bwd_workspace_bytes.argtypes = [i64, i64, i32]
+    L.recis_embed_bwd.argtypes = [p, i64, p, i32, i64, i64, i32, f32, p, i32, i64, p, i64, p, p]
+    L.recis_layernorm_fwd.argtypes = [p, i32, i64, i64, i32, p, p, i32, f32, p, i64, p, p, p]
+    L.recis_layernorm_bwd_workspace_bytes.argtypes = [i64, i32]
+    L.recis_layernorm_bwd.argtypes = [p, i64, p, i64, i32, i64, i32, p, p, p, i32, p, i64, p, p, p, i64, p]
+    L.recis_cross_attn_workspace_bytes.argtypes = [p, i32]  # p first: a recis_attn_desc by reference
+    L.recis_cross_attn_fwd.argtypes = [p, p, p, p, p, p, p, i64, p]
+    L.recis_cross_attn_bwd.argtypes = [p, p, p, p, p, p, p, p, p, p, p, i64, p]
+    for name in ("recis_embed_bwd_workspace_bytes", "recis_layernorm_bwd_workspace_bytes",
+                 "recis_cross_attn_workspace_bytes"):
+        getattr(L, name).restype = i64
     L.recis_status_string.argtypes = [i32]
     L.recis_status_string.restype = C.c_char_p
     for name in ("recis_idmap_create", "recis_idmap_destroy", "recis_idmap_insert_find",
@@ -150,7 +176,9 @@ def load_library() -> C.CDLL:
                  "recis_lookup_pool_fwd",
                  "recis_pool_bwd_update", "recis_pool_bwd_update_noalloc",
                  "recis_writeback", "recis_idmap_export", "recis_idmap_import", "recis_idmap_key_ages",
-                 "recis_idmap_sketch", "recis_idmap_stats", "recis_get_error"):
+                 "recis_idmap_sketch", "recis_idmap_stats", "recis_get_error",
+                 "recis_embed_fwd", "recis_embed_bwd", "recis_layernorm_fwd", "recis_layernorm_bwd",
+                 "recis_cross_attn_fwd", "recis_cross_attn_bwd"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -331,6 +359,63 @@ def recis_idmap_stats(h, stream=None) -> recis_table_stats:
 
 def recis_get_error(h, stream=None) -> int:
     return int(load_library().recis_get_error(h, _stream(stream)))
+
+
+# Sequence operators: pointers and sizes as in the header.  ``sequence`` has
+# the forms that take tensors, check them and allocate what a call returns.
+def recis_embed_fwd(tokens, n: int, weight, dtype: int, rows: int, dim: int, weight_stride: int, scale: float,
+                    out, out_stride: int, error=None, stream=None):
+    _check(load_library().recis_embed_fwd(_ptr(tokens), n, _ptr(weight), dtype, rows, dim, weight_stride, scale,
+                                          _ptr(out), out_stride, _ptr(error), _stream(stream)), "recis_embed_fwd")
+
+
+def recis_embed_bwd_workspace_bytes(n: int, rows: int, dim: int) -> int:
+    return int(load_library().recis_embed_bwd_workspace_bytes(n, rows, dim))
+
+
+def recis_embed_bwd(tokens, n: int, grad_out, grad_dtype: int, grad_stride: int, rows: int, dim: int, scale: float,
+                    grad_weight, weight_dtype: int, weight_stride: int, workspace, workspace_bytes: int,
+                    error=None, stream=None):
+    _check(load_library().recis_embed_bwd(_ptr(tokens), n, _ptr(grad_out), grad_dtype, grad_stride, rows, dim, scale,
+                                          _ptr(grad_weight), weight_dtype, weight_stride, _ptr(workspace),
+                                          workspace_bytes, _ptr(error), _stream(stream)), "recis_embed_bwd")
+
+
+def recis_layernorm_fwd(x, dtype: int, x_stride: int, m: int, dim: int, weight, bias, weight_dtype: int, eps: float,
+                        y, y_stride: int, mean=None, rstd=None, stream=None):
+    _check(load_library().recis_layernorm_fwd(_ptr(x), dtype, x_stride, m, dim, _ptr(weight), _ptr(bias),
+                                              weight_dtype, eps, _ptr(y), y_stride, _ptr(mean), _ptr(rstd),
+                                              _stream(stream)), "recis_layernorm_fwd")
+
+
+def recis_layernorm_bwd_workspace_bytes(m: int, dim: int) -> int:
+    return int(load_library().recis_layernorm_bwd_workspace_bytes(m, dim))
+
+
+def recis_layernorm_bwd(grad_y, grad_stride: int, x, x_stride: int, dtype: int, m: int, dim: int, mean, rstd, weight,
+                        weight_dtype: int, grad_x, grad_x_stride: int, grad_weight, grad_bias, workspace,
+                        workspace_bytes: int, stream=None):
+    _check(load_library().recis_layernorm_bwd(_ptr(grad_y), grad_stride, _ptr(x), x_stride, dtype, m, dim, _ptr(mean),
+                                              _ptr(rstd), _ptr(weight), weight_dtype, _ptr(grad_x), grad_x_stride,
+                                              _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace), workspace_bytes,
+                                              _stream(stream)), "recis_layernorm_bwd")
+
+
+def recis_cross_attn_workspace_bytes(desc: recis_attn_desc, backward: bool) -> int:
+    return int(load_library().recis_cross_attn_workspace_bytes(C.byref(desc), 1 if backward else 0))
+
+
+def recis_cross_attn_fwd(desc: recis_attn_desc, q, k, v, out, lse, workspace, workspace_bytes: int, stream=None):
+    _check(load_library().recis_cross_attn_fwd(C.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                               _ptr(workspace), workspace_bytes, _stream(stream)),
+           "recis_cross_attn_fwd")
+
+
+def recis_cross_attn_bwd(desc: recis_attn_desc, grad_out, q, k, v, out, lse, grad_q, grad_k, grad_v, workspace,
+                         workspace_bytes: int, stream=None):
+    _check(load_library().recis_cross_attn_bwd(C.byref(desc), _ptr(grad_out), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                               _ptr(lse), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(workspace),
+                                               workspace_bytes, _stream(stream)), "recis_cross_attn_bwd")
 
 
 # --------------------------------------------------------- conveniences

@@ -472,6 +472,122 @@ const char* recis_status_string(recis_status st);
  * INVALID_ARG for a NULL table, or a name with NULL events. */
 recis_status recis_profile_kernel(recis_table* t, const char* kernel, hipEvent_t start, hipEvent_t stop);
 
+/* ------------------------------------------------------------ sequence operators
+ * What reads and trains the rows that the table gathers (page "RecIS: Sparse
+ * to Dense, A Unified Training Framework for Recommendation Models", abstract:
+ * one framework for the sparse and the dense part): a token embedding for
+ * the small fixed vocabularies beside the hashed ids, layer norm, and cross
+ * attention to a history in the CSR form of the lookup.  The pages give no
+ * formula for them; each is stated at its declaration.
+ *
+ * Conventions, besides those above: these calls own no memory and keep no
+ * state.  Tensors are rows of contiguous elements, strides are in elements,
+ * rows may not overlap in a tensor that is written.  A workspace is device
+ * memory, 256-byte aligned, of at least the bytes the matching *_bytes call
+ * returns for the same sizes (that call returns -1 for sizes the operator
+ * refuses), and needs no clearing.  Nothing is allocated and nothing waits, so the calls may
+ * be captured into a graph.  `error`: a device word, 4-byte aligned, or NULL;
+ * a fault found on the GPU sets bit 1 << RECIS_ERR_* in it (the caller clears
+ * it), the data concerned is then unspecified and nothing is read or written
+ * out of bounds.  Results do not depend on timing: equal inputs give equal
+ * bits. */
+
+/* Token embedding: out[i] = scale * weight[tokens[i]], rounded once to dtype;
+ * a negative token is padding and gives zeros.  tokens device [n]; weight
+ * device [rows] rows of dim elements; out device [n] rows of dim elements, in
+ * the weight's dtype.  A token >= rows gives zeros and records
+ * RECIS_ERR_KEY_RANGE.  n <= 2^31 - 4096, rows <= 2^30, dim <= 65536 (else
+ * UNSUPPORTED).  Passage: page "RecIS: Sparse to Dense, A Unified Training
+ * Framework for Recommendation Models", abstract (sparse and dense trained together). */
+recis_status recis_embed_fwd(const int64_t* tokens, int64_t n, const void* weight, int32_t dtype, int64_t rows,
+                             int32_t dim, int64_t weight_stride, float scale, void* out, int64_t out_stride,
+                             uint32_t* error, hipStream_t s);
+
+/* Its gradient: grad_weight[v] = scale * sum of grad_out[i] over tokens[i] = v,
+ * every row written (zeros where no token fell), summed in float32 in the
+ * order of the tokens sorted by value, equal tokens by place, and rounded once to
+ * weight_dtype.  Tokens outside [0, rows) add nothing; one >= rows records
+ * RECIS_ERR_KEY_RANGE.  Limits as above. */
+int64_t recis_embed_bwd_workspace_bytes(int64_t n, int64_t rows, int32_t dim);
+recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_out, int32_t grad_dtype,
+                             int64_t grad_stride, int64_t rows, int32_t dim, float scale, void* grad_weight,
+                             int32_t weight_dtype, int64_t weight_stride, void* workspace, int64_t workspace_bytes,
+                             uint32_t* error, hipStream_t s);
+
+/* Layer norm over the dim elements of each of m rows: y = (x - mean) * rstd *
+ * weight + bias with mean = sum x / dim, rstd = 1 / sqrt(sum (x - mean)^2 / dim
+ * + eps), all in float32, y rounded once to dtype.  weight, bias: device [dim]
+ * in weight_dtype, or NULL (1 and 0).  mean, rstd: device float32 [m], both or
+ * neither.  y may be x.  dim <= 16384 (else UNSUPPORTED).  Passage: as
+ * recis_embed_fwd. */
+recis_status recis_layernorm_fwd(const void* x, int32_t dtype, int64_t x_stride, int64_t m, int32_t dim,
+                                 const void* weight, const void* bias, int32_t weight_dtype, float eps, void* y,
+                                 int64_t y_stride, float* mean, float* rstd, hipStream_t s);
+
+/* Its backward pass, from the forward's mean and rstd.  With g = grad_y and xh
+ * = (x - mean) * rstd: grad_x = rstd * (g w - sum(g w) / dim - xh sum(g w xh) /
+ * dim) in dtype (grad_x may be grad_y or x); grad_weight = sum over rows of g
+ * xh and grad_bias = sum over rows of g, in weight_dtype, either may be NULL
+ * (with both NULL no workspace is needed).  m = 0 gives zero sums. */
+int64_t recis_layernorm_bwd_workspace_bytes(int64_t m, int32_t dim);
+recis_status recis_layernorm_bwd(const void* grad_y, int64_t grad_stride, const void* x, int64_t x_stride,
+                                 int32_t dtype, int64_t m, int32_t dim, const float* mean, const float* rstd,
+                                 const void* weight, int32_t weight_dtype, void* grad_x, int64_t grad_x_stride,
+                                 void* grad_weight, void* grad_bias, void* workspace, int64_t workspace_bytes,
+                                 hipStream_t s);
+
+/* Cross attention's sizes, layouts and masks.  Strides are those of (batch
+ * entry, position, head); the head vectors' elements are contiguous. */
+typedef struct {
+  int32_t dtype;              /* of q, k, v, out and every gradient */
+  int32_t batch;
+  int32_t q_len;              /* queries a batch entry */
+  int32_t kv_len;             /* keys a batch entry; packed: the most any entry has */
+  int32_t q_heads;            /* a multiple of kv_heads: query head i reads key head */
+  int32_t kv_heads;           /*   i / (q_heads / kv_heads) */
+  int32_t head_dim;           /* 1 .. 128 (else UNSUPPORTED) */
+  float scale;                /* of the scores, > 0 */
+  int64_t q_strides[3];
+  int64_t k_strides[3];       /* packed: the batch stride is not read */
+  int64_t v_strides[3];
+  int64_t o_strides[3];
+  int64_t do_strides[3];      /* backward only, as are the rest */
+  int64_t dq_strides[3];
+  int64_t dk_strides[3];
+  int64_t dv_strides[3];
+  const int32_t* kv_lens;     /* device [batch]: padded keys, entry b has kv_lens[b] of kv_len; or NULL: all */
+  const int32_t* kv_offsets;  /* device [batch + 1]: packed keys, entry b has rows kv_offsets[b] ..
+                                 kv_offsets[b + 1] - 1 of k and v; excludes kv_lens */
+  int64_t kv_rows;            /* packed: rows of k and v */
+  const uint8_t* kv_mask;     /* device: 0 leaves a key out; [batch, kv_len], or [kv_rows] when
+                                 packed; or NULL */
+  int64_t mask_stride;        /* of a batch entry in kv_mask (padded) */
+  uint32_t* error;            /* a length or offset out of range records RECIS_ERR_INVALID_ARG;
+                                 its entry is then taken as empty */
+} recis_attn_desc;
+
+/* Device bytes of the forward's (backward 0) or the backward's workspace; 0:
+ * none needed.  Depends on the sizes alone, not on pointers or strides. */
+int64_t recis_cross_attn_workspace_bytes(const recis_attn_desc* desc, int32_t backward);
+
+/* out = softmax(scale q k^T) v over the keys of the entry that count; lse
+ * (device float32 [batch, q_len, q_heads], may be NULL) receives the log of
+ * the sum of exponentials.  An entry without a key that counts gives out 0 and
+ * lse -infinity.  What k and v hold at keys that do not count is not looked
+ * at, be it NaN.  Statistics and sums are float32; with bfloat16 the softmax
+ * weights are rounded to bfloat16 before they meet v.  Passage: as
+ * recis_embed_fwd. */
+recis_status recis_cross_attn_fwd(const recis_attn_desc* desc, const void* q, const void* k, const void* v, void* out,
+                                  float* lse, void* workspace, int64_t workspace_bytes, hipStream_t s);
+
+/* Gradients of q, k and v from the forward's out and lse.  Keys that do not
+ * count get zeros (packed rows before the first entry and after the last
+ * among them); the gradients of a shared key head are summed over its query
+ * heads.  With batch 0 nothing is written. */
+recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_out, const void* q, const void* k,
+                                  const void* v, const void* out, const float* lse, void* grad_q, void* grad_k,
+                                  void* grad_v, void* workspace, int64_t workspace_bytes, hipStream_t s);
+
 #ifdef __cplusplus
 }
 #endif
