@@ -74,115 +74,148 @@ void launch_fwd(const int64_t* tokens, int64_t n, const void* w, int64_t rows, i
 // ------------------------------------------------------------- sorted tokens
 // Least-significant-digit radix sort of (token, place), stable.  Tokens that
 // take no gradient (negative, or beyond the table) get the key `rows` and end
-// up behind every row.  Per pass: a histogram of each tile's digits, the
-// tiles' exclusive offsets, and a scatter that ranks the keys of a tile in
-// order: the wave's lanes with the same digit find each other by ballots, the
-// four waves of a block follow each other through per-wave counters in LDS.
-constexpr int kDigitBits = 8;
-constexpr int kDigits = 1 << kDigitBits;
+// up behind every row.  Digits of up to 11 bits: one pass for tables of 2047
+// rows, two up to 4M rows.  Per pass: a histogram of each tile's digits, where
+// each tile's share of a digit begins, and a scatter that ranks the keys of a
+// tile in order: the wave's lanes with the same digit find each other by
+// ballots, the waves of a block follow each other through counters in LDS.
+constexpr int kMaxDigitBits = 11;
+constexpr int kMaxDigits = 1 << kMaxDigitBits;
 constexpr int kWaves = kThreads / 64;
-constexpr int kSortPerThread = 16;
-constexpr int kSortTile = kThreads * kSortPerThread;  // 4096
+
+// A key and its place travel as one 8-byte word: half the scattered writes.
+struct __align__(8) Keyed {
+  unsigned key, place;
+};
 
 template <bool FIRST>
-__device__ __forceinline__ unsigned sort_key(const long long* tokens, const unsigned* keys, long long i,
-                                             unsigned rows, unsigned* error) {
+__device__ __forceinline__ Keyed sort_key(const long long* tokens, const Keyed* in, long long i, unsigned rows,
+                                          unsigned* error) {
   if constexpr (FIRST) {
     const long long t = tokens[i];
     if (t >= (long long)rows && error) atomicOr(error, kErrKeyRange);
-    return t < 0 || t >= (long long)rows ? rows : (unsigned)t;
+    return Keyed{t < 0 || t >= (long long)rows ? rows : (unsigned)t, (unsigned)i};
   } else {
-    return keys[i];
+    return in[i];
   }
 }
 
-template <bool FIRST>
-__global__ __launch_bounds__(kThreads) void k_sort_hist(const long long* __restrict__ tokens,
-                                                        const unsigned* __restrict__ keys, long long n, unsigned rows,
-                                                        int shift, unsigned* __restrict__ hist, unsigned* error) {
-  __shared__ unsigned h[kDigits];
-  h[threadIdx.x] = 0;
+struct SortArgs {
+  const long long* tokens;
+  const Keyed* in;
+  Keyed* out;
+  long long n;
+  unsigned rows;
+  int shift, digits, tiles;
+  unsigned* hist;    // [tiles][digits] counts, exclusive offsets after k_sort_scan
+  unsigned* totals;  // [digits], written by k_sort_scan
+  unsigned* error;
+};
+
+// PER keys a thread, PER * kThreads a tile.
+template <bool FIRST, int PER>
+__global__ __launch_bounds__(kThreads) void k_sort_hist(SortArgs a) {
+  __shared__ unsigned h[kMaxDigits];
+  for (int d = threadIdx.x; d < a.digits; d += kThreads) h[d] = 0;
   __syncthreads();
-  const long long base = (long long)blockIdx.x * kSortTile;
+  const long long base = (long long)blockIdx.x * PER * kThreads;
 #pragma unroll
-  for (int j = 0; j < kSortPerThread; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const long long i = base + j * kThreads + threadIdx.x;
-    if (i < n) atomicAdd(&h[(sort_key<FIRST>(tokens, keys, i, rows, error) >> shift) & (kDigits - 1)], 1u);
+    if (i < a.n) atomicAdd(&h[(sort_key<FIRST>(a.tokens, a.in, i, a.rows, a.error).key >> a.shift) & (a.digits - 1)], 1u);
   }
   __syncthreads();
-  hist[(long long)blockIdx.x * kDigits + threadIdx.x] = h[threadIdx.x];
+  for (int d = threadIdx.x; d < a.digits; d += kThreads) a.hist[(long long)blockIdx.x * a.digits + d] = h[d];
 }
 
-// One block a digit: its counts over the tiles become exclusive offsets, its
-// total goes to totals[digit].
-__global__ __launch_bounds__(kThreads) void k_sort_scan(unsigned* __restrict__ hist, int tiles,
-                                                        unsigned* __restrict__ totals) {
-  __shared__ unsigned part[kThreads];
-  const int d = blockIdx.x;
+// 16 digits a block, the tiles in 16 consecutive ranges: counts become
+// exclusive offsets over the tiles, a digit's total goes to totals[digit].
+constexpr int kScanDigits = 16, kScanParts = kThreads / kScanDigits;
+__global__ __launch_bounds__(kThreads) void k_sort_scan(SortArgs a) {
+  __shared__ unsigned part[kScanParts][kScanDigits];
+  const int c = threadIdx.x % kScanDigits, p = threadIdx.x / kScanDigits;
+  const int d = blockIdx.x * kScanDigits + c;
+  const int per = (a.tiles + kScanParts - 1) / kScanParts;
+  const int t0 = p * per, t1 = std::min(a.tiles, t0 + per);
+  unsigned sum = 0;
+  if (d < a.digits)
+#pragma unroll 8
+    for (int t = t0; t < t1; ++t) sum += a.hist[(long long)t * a.digits + d];
+  part[p][c] = sum;
+  __syncthreads();
+  if (d >= a.digits) return;
   unsigned run = 0;
-  for (int t0 = 0; t0 < tiles; t0 += kThreads) {
-    const int t = t0 + (int)threadIdx.x;
-    const unsigned c = t < tiles ? hist[(long long)t * kDigits + d] : 0u;
-    part[threadIdx.x] = c;
-    __syncthreads();
-    for (int o = 1; o < kThreads; o <<= 1) {
-      const unsigned x = (int)threadIdx.x >= o ? part[threadIdx.x - o] : 0u;
-      __syncthreads();
-      part[threadIdx.x] += x;
-      __syncthreads();
-    }
-    if (t < tiles) hist[(long long)t * kDigits + d] = run + part[threadIdx.x] - c;
-    run += part[kThreads - 1];
-    __syncthreads();
+  for (int k = 0; k < p; ++k) run += part[k][c];
+  if (p == kScanParts - 1) a.totals[d] = run + sum;
+#pragma unroll 8
+  for (int t = t0; t < t1; ++t) {
+    const unsigned x = a.hist[(long long)t * a.digits + d];
+    a.hist[(long long)t * a.digits + d] = run;
+    run += x;
   }
-  if (threadIdx.x == 0) totals[d] = run;
 }
 
-template <bool FIRST>
-__global__ __launch_bounds__(kThreads) void k_sort_scatter(const long long* __restrict__ tokens,
-                                                           const unsigned* __restrict__ keys,
-                                                           const unsigned* __restrict__ places, long long n,
-                                                           unsigned rows, int shift, const unsigned* __restrict__ hist,
-                                                           const unsigned* __restrict__ totals,
-                                                           unsigned* __restrict__ keys_out,
-                                                           unsigned* __restrict__ places_out) {
-  __shared__ unsigned cnt[kWaves][kDigits];
-  __shared__ unsigned scan[kThreads];
+// SCANNED: hist and totals are k_sort_scan's; otherwise hist holds the counts
+// of a few tiles and every block adds them up itself (a launch less).
+template <bool FIRST, int PER, bool SCANNED>
+__global__ __launch_bounds__(kThreads) void k_sort_scatter(SortArgs a) {
+  __shared__ unsigned cnt[kWaves][kMaxDigits];
+  __shared__ unsigned wave_sum[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // each wave owns PER * 64 consecutive keys, 64 at a time
+  const long long base = (long long)blockIdx.x * PER * kThreads + wave * (PER * 64);
+  Keyed key[PER];
+  unsigned rank[PER];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) cnt[w][threadIdx.x] = 0;
-  // where each digit's keys begin
-  const unsigned total = totals[threadIdx.x];
-  scan[threadIdx.x] = total;
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {
-    const unsigned x = (int)threadIdx.x >= o ? scan[threadIdx.x - o] : 0u;
-    __syncthreads();
-    scan[threadIdx.x] += x;
-    __syncthreads();
-  }
-  const unsigned begin = scan[threadIdx.x] - total + hist[(long long)blockIdx.x * kDigits + threadIdx.x];
-  __syncthreads();
-
-  // each wave owns kSortTile / kWaves consecutive keys, 64 at a time
-  const long long base = (long long)blockIdx.x * kSortTile + wave * (kSortTile / kWaves);
-  unsigned key[kSortPerThread], place[kSortPerThread], rank[kSortPerThread];
-#pragma unroll
-  for (int j = 0; j < kSortPerThread; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const long long i = base + j * 64 + lane;
-    const bool in = i < n;
-    key[j] = in ? sort_key<FIRST>(tokens, keys, i, rows, nullptr) : 0u;
-    place[j] = in ? (FIRST ? (unsigned)i : places[i]) : 0u;
+    key[j] = i < a.n ? sort_key<FIRST>(a.tokens, a.in, i, a.rows, nullptr) : Keyed{0u, 0u};
   }
+  // where the tile's share of each digit begins: thread t has digits
+  // t * per_thread and the next ones
+  const int per_thread = (a.digits + kThreads - 1) / kThreads;
+  unsigned begin[kMaxDigits / kThreads];
+  unsigned mine = 0;
 #pragma unroll
-  for (int j = 0; j < kSortPerThread; ++j) {
-    const bool in = base + j * 64 + lane < n;
-    const unsigned d = (key[j] >> shift) & (kDigits - 1);
+  for (int k = 0; k < kMaxDigits / kThreads; ++k) {
+    const int d = threadIdx.x * per_thread + k;
+    unsigned before = 0, total = 0;
+    if (k < per_thread && d < a.digits) {
+      if constexpr (SCANNED) {
+        total = a.totals[d];
+        before = a.hist[(long long)blockIdx.x * a.digits + d];
+      } else {
+#pragma unroll 8
+        for (int t = 0; t < a.tiles; ++t) {
+          const unsigned x = a.hist[(long long)t * a.digits + d];
+          total += x;
+          if (t < (int)blockIdx.x) before += x;
+        }
+      }
+      for (int w = 0; w < kWaves; ++w) cnt[w][d] = 0;
+    }
+    begin[k] = mine + before;
+    mine += total;
+  }
+  unsigned incl = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const unsigned x = __shfl_up(incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 63) wave_sum[wave] = incl;
+  __syncthreads();
+  unsigned first = incl - mine;
+  for (int w = 0; w < wave; ++w) first += wave_sum[w];
+
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool in = base + j * 64 + lane < a.n;
+    const unsigned d = (key[j].key >> a.shift) & (a.digits - 1);
     unsigned long long same = __ballot(in);
-#pragma unroll
-    for (int b = 0; b < kDigitBits; ++b) {
-      const unsigned long long set = __ballot((d >> b) & 1u);
-      same &= (d >> b) & 1u ? set : ~set;
+    for (int b = 1; b < a.digits; b <<= 1) {
+      const unsigned long long set = __ballot((d & b) != 0);
+      same &= d & b ? set : ~set;
     }
     rank[j] = 0;
     if (in) {
@@ -195,20 +228,24 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(const long long* __re
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   __syncthreads();
-  unsigned run = begin;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const unsigned c = cnt[w][threadIdx.x];
-    cnt[w][threadIdx.x] = run;
-    run += c;
+  for (int k = 0; k < kMaxDigits / kThreads; ++k) {
+    const int d = threadIdx.x * per_thread + k;
+    if (k >= per_thread || d >= a.digits) continue;
+    unsigned run = first + begin[k];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const unsigned c = cnt[w][d];
+      cnt[w][d] = run;
+      run += c;
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kSortPerThread; ++j) {
-    if (base + j * 64 + lane < n) {
-      const unsigned to = cnt[wave][(key[j] >> shift) & (kDigits - 1)] + rank[j];
-      keys_out[to] = key[j];
-      places_out[to] = place[j];
+  for (int j = 0; j < PER; ++j) {
+    if (base + j * 64 + lane < a.n) {
+      const unsigned to = cnt[wave][(key[j].key >> a.shift) & (a.digits - 1)] + rank[j];
+      a.out[to] = key[j];
     }
   }
 }
@@ -221,9 +258,10 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(const long long* __re
 // untouched rows makes one group longer than another.  A row that spans
 // groups of a block is joined in LDS, in order; one that spans blocks leaves a
 // float32 part per block for k_embed_join.
+constexpr int kMaxUnits = 2048;  // units a block
+
 struct SumArgs {
-  const unsigned* tok;    // [n] sorted keys
-  const unsigned* place;  // [n] their places in the call
+  const Keyed* tok;  // [n] sorted tokens with their places in the call
   long long n, rows;
   const void* grad;
   long long grad_stride;
@@ -231,6 +269,7 @@ struct SumArgs {
   long long out_stride;
   float scale;
   int dim, quantum;
+  int lane_bits;  // 2^lane_bits lanes a row; blockIdx.y counts tiles of 2^lane_bits * V columns
   // per block: the row it starts in, whether that row has earlier tokens, and
   // the parts it leaves: `head` ends the first row, `tail` belongs to the row
   // the next block starts in
@@ -241,44 +280,77 @@ struct SumArgs {
 };
 
 // Tokens consumed when the merge has made d steps (a token t goes before the
-// end of row r iff t <= r).
-__device__ __forceinline__ long long merge_tokens(const unsigned* tok, long long n, long long rows, long long d) {
-  long long lo = d > rows ? d - rows : 0, hi = d < n ? d : n;
+// end of row r iff t <= r): 64 probes a round.
+__device__ __forceinline__ long long merge_tokens(const SumArgs& a, long long d, int lane) {
+  long long lo = d > a.rows ? d - a.rows : 0, hi = d < a.n ? d : a.n;
   while (lo < hi) {
-    const long long mid = (lo + hi) >> 1;
-    if ((long long)tok[mid] <= d - 1 - mid)
-      lo = mid + 1;
-    else
-      hi = mid;
+    const long long step = (hi - lo + 63) >> 6;
+    const long long at = lo + (lane + 1) * step - 1;
+    const bool before = at < hi && (long long)a.tok[at].key <= d - 1 - at;
+    lo += __popcll(__ballot(before)) * step;
+    hi = std::min(hi, lo + step - 1);
   }
   return lo;
 }
 
-// TG: gradient type, TW: type of the result, V elements an access, L lanes a
-// row (a block covers L * V columns; blockIdx.y counts column tiles).
-template <typename TG, typename TW, int V, int L>
+// TG: gradient type, TW: type of the result, V elements an access.
+template <typename TG, typename TW, int V>
 __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
-  constexpr int kGroups = kThreads / L;
   constexpr int kBatch = 8;
-  constexpr int C = L * V;
-  __shared__ float head[kGroups][C];
-  __shared__ float tail[kGroups][C];
-  __shared__ int first[kGroups + 1];
-  __shared__ int begun[kGroups];
-  const int g = threadIdx.x / L, lane = threadIdx.x % L;
+  __shared__ Keyed slice[kMaxUnits];   // the block's tokens; later the groups' tails
+  __shared__ float head[kThreads * V];  // [groups][columns]
+  __shared__ long long ends[2];
+  __shared__ unsigned short starts[kThreads + 1];  // tokens before each group
+  static_assert(sizeof(slice) >= sizeof(head), "tails fit the slice");
+  const int lanes = 1 << a.lane_bits, groups = kThreads >> a.lane_bits, C = lanes * V;
+  const int g = threadIdx.x >> a.lane_bits, lane = threadIdx.x & (lanes - 1);
   const int col = blockIdx.y * C + lane * V;
   const bool live = col < a.dim;
   const TG* grad = static_cast<const TG*>(a.grad);
   TW* out = static_cast<TW*>(a.out);
 
   const long long total = a.n + a.rows;
-  const long long d0 = std::min(total, ((long long)blockIdx.x * kGroups + g) * a.quantum);
-  const long long d1 = std::min(total, d0 + a.quantum);
-  const long long i0 = merge_tokens(a.tok, a.n, a.rows, d0), i1 = merge_tokens(a.tok, a.n, a.rows, d1);
-  int row = (int)(d0 - i0);
-  const int row_end = (int)(d1 - i1);
-  const int row_first = row;
-  const bool began = i0 > 0 && (long long)a.tok[i0 - 1] == row;
+  const int units = groups * a.quantum;
+  const long long d0 = (long long)blockIdx.x * units;
+  const int wave = threadIdx.x >> 6;
+  if (wave < 2) {
+    const long long i = merge_tokens(a, std::min(total, d0 + wave * units), threadIdx.x & 63);
+    if ((threadIdx.x & 63) == 0) ends[wave] = i;
+  }
+  __syncthreads();
+  const long long first = ends[0];
+  const int count = (int)(ends[1] - first);
+  const int block_row = (int)(d0 - first);
+  for (int i = threadIdx.x; i < count; i += kThreads) {
+    slice[i] = a.tok[first + i];
+  }
+  __syncthreads();
+  // the same search inside the block, on what is left of the merge
+  if (threadIdx.x == 0) starts[groups] = (unsigned short)count;
+  if (threadIdx.x < groups) {
+    const int d = (int)std::min(total - d0, (long long)threadIdx.x * a.quantum);
+    int lo = d - std::min(d, (int)std::min<long long>(a.rows - block_row, units)), hi = std::min(d, count);
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if ((int)slice[mid].key - block_row <= d - 1 - mid)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    starts[threadIdx.x] = (unsigned short)lo;
+  }
+  __syncthreads();
+  auto row_of = [&](int k) {  // the row group k starts in
+    return block_row + (int)std::min(total - d0, (long long)k * a.quantum) - (int)starts[k];
+  };
+  auto has_tokens = [&](int k) {  // whether that row has tokens before the group
+    const int i = starts[k];
+    return i > 0 ? (int)slice[i - 1].key == row_of(k) : first > 0 && (int)a.tok[first - 1].key == row_of(k);
+  };
+  const int i0 = starts[g], i1 = starts[g + 1];
+  const int row_first = row_of(g), row_end = row_of(g + 1);
+  const bool began = has_tokens(g);
+  int row = row_first;
 
   float acc[V];
 #pragma unroll
@@ -287,7 +359,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
     if (live) {
       if (row == row_first && began) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) head[g][lane * V + i] = acc[i];
+        for (int i = 0; i < V; ++i) head[g * C + lane * V + i] = acc[i];
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] *= a.scale;
@@ -298,120 +370,168 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     ++row;
   };
-  for (long long i = i0; i < i1; i += kBatch) {
-    unsigned t[kBatch];
-    float x[kBatch][V];
+  // the next batch's gradient rows are on their way while one is added up
+  Vec<TG, V> x[kBatch], ahead[kBatch];
+  auto fetch = [&](int i, Vec<TG, V>(&to)[kBatch]) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const bool in = i + b < i1;
-      t[b] = in ? a.tok[i + b] : (unsigned)a.rows;
-      if (live && t[b] < (unsigned)a.rows) {
-        load_f32<TG, V>(grad + (long long)a.place[i + b] * a.grad_stride + col, x[b]);
-      } else {
+      if (live && i + b < i1 && slice[i + b].key < (unsigned)a.rows)
+        to[b] = *reinterpret_cast<const Vec<TG, V>*>(grad + (long long)slice[i + b].place * a.grad_stride + col);
+    }
+  };
+  fetch(i0, x);
+  for (int i = i0; i < i1; i += kBatch) {
+    fetch(i + kBatch, ahead);
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[b][k] = 0.f;
+    for (int b = 0; b < kBatch; ++b) {
+      const unsigned t = i + b < i1 ? slice[i + b].key : (unsigned)a.rows;
+      if (t < (unsigned)a.rows) {
+        while (row < (int)t) finish_row();
+        if (live) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[k] += (float)x[b].e[k];
+        }
       }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (t[b] < (unsigned)a.rows) {
-        while (row < (int)t[b]) finish_row();
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += x[b][k];
-      }
-    }
+    for (int b = 0; b < kBatch; ++b) x[b] = ahead[b];
   }
   while (row < row_end) finish_row();
-#pragma unroll
-  for (int i = 0; i < V; ++i) tail[g][lane * V + i] = acc[i];
-  if (lane == 0) {
-    first[g] = row_first;
-    begun[g] = began;
-    if (g == kGroups - 1) first[kGroups] = row_end;
-  }
-  __syncthreads();
   // join the rows that span groups: thread c carries column c through the
   // groups in order
+  const int rows_of = threadIdx.x < groups ? row_of(threadIdx.x) : 0;
+  const int begun_of = threadIdx.x < groups ? has_tokens(threadIdx.x) : 0;
+  const int last_row = row_of(groups);
+  __shared__ int group_row[kThreads + 1];
+  __shared__ unsigned char group_began[kThreads];
+  if (threadIdx.x < groups) {
+    group_row[threadIdx.x] = rows_of;
+    group_began[threadIdx.x] = begun_of;
+  }
+  if (threadIdx.x == 0) group_row[groups] = last_row;
+  __syncthreads();  // the slice is free from here on
+  float* tail = reinterpret_cast<float*>(slice);
+#pragma unroll
+  for (int i = 0; i < V; ++i) tail[g * C + lane * V + i] = acc[i];
+  __syncthreads();
   for (int c = threadIdx.x; c < C; c += kThreads) {
     const int column = blockIdx.y * C + c;
     if (column >= a.dim) break;
     float run = 0.f;
-    bool open = begun[0];  // the row in `run` has tokens before this block
-    for (int k = 0; k < kGroups; ++k) {
-      const int r = first[k];
-      if (first[k + 1] > r) {  // the group ends row r
+    bool open = group_began[0];  // the row in `run` has tokens before this block
+    for (int k = 0; k < groups; ++k) {
+      const int r = group_row[k];
+      if (group_row[k + 1] > r) {  // the group ends row r
         if (open) {
-          a.head[(long long)blockIdx.x * a.dim + column] = run + head[k][c];
-        } else if (begun[k]) {
-          out[(long long)r * a.out_stride + column] = (TW)((run + head[k][c]) * a.scale);
+          a.head[(long long)blockIdx.x * a.dim + column] = run + head[k * C + c];
+        } else if (group_began[k]) {
+          out[(long long)r * a.out_stride + column] = (TW)((run + head[k * C + c]) * a.scale);
         }
-        run = tail[k][c];
+        run = tail[k * C + c];
         open = false;
       } else {
-        run += tail[k][c];
+        run += tail[k * C + c];
       }
     }
     a.tail[(long long)blockIdx.x * a.dim + column] = run;
   }
   if (threadIdx.x == 0 && blockIdx.y == 0) {
-    a.first_row[blockIdx.x] = first[0];
-    a.began[blockIdx.x] = begun[0];
-    if (blockIdx.x == gridDim.x - 1) a.first_row[gridDim.x] = first[kGroups];
+    a.first_row[blockIdx.x] = group_row[0];
+    a.began[blockIdx.x] = group_began[0];
+    if (blockIdx.x == gridDim.x - 1) a.first_row[gridDim.x] = last_row;
   }
 }
 
 // Rows that span blocks of k_embed_sum: the block that ends the row adds the
-// tails of the blocks before it that the row runs through, in order.
-template <typename TW>
+// tails of the blocks before it that the row runs through.  The tails are
+// taken in kJoinParts consecutive ranges at a time, joined in order.
+constexpr int kJoinLanes = 32, kJoinParts = kThreads / kJoinLanes;
+template <typename TW, int V>
 __global__ __launch_bounds__(kThreads) void k_embed_join(SumArgs a) {
+  __shared__ float part[kJoinParts][kJoinLanes * V];
   const int b = blockIdx.x;
-  const int r = a.first_row[b];
-  if (!a.began[b] || a.first_row[b + 1] == r) return;
-  int k = b - 1;  // the first block with tokens of the row
-  while (k > 0 && a.first_row[k] == r && a.began[k]) --k;
-  for (int c = threadIdx.x; c < a.dim; c += kThreads) {
-    float sum = 0.f;
-    for (int j = k; j < b; ++j) sum += a.tail[(long long)j * a.dim + c];
-    sum += a.head[(long long)b * a.dim + c];
-    static_cast<TW*>(a.out)[(long long)r * a.out_stride + c] = (TW)(sum * a.scale);
+  const int r = a.first_row[b], next = a.first_row[b + 1], began = a.began[b];
+  if (!began || next == r) return;
+  // the first block with tokens of the row: every block after it starts in
+  // the row, which has begun by then (64 blocks a step)
+  int k = b;
+  const int lane = threadIdx.x & 63;
+  for (;;) {
+    const int at = k - lane;
+    const bool inside = at > 0 && a.first_row[at] == r && a.began[at];
+    const unsigned long long out_of_it = ~__ballot(inside);
+    const int steps = out_of_it ? __ffsll(out_of_it) - 1 : 64;
+    k -= steps;
+    if (steps < 64) break;
+  }
+  const int l = threadIdx.x % kJoinLanes, p = threadIdx.x / kJoinLanes;
+  const int per = (b - k + kJoinParts - 1) / kJoinParts;
+  const int j0 = std::min(b, k + p * per), j1 = std::min(b, j0 + per);
+  for (int c0 = 0; c0 < a.dim; c0 += kJoinLanes * V) {
+    const int c = c0 + l * V;
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    if (c < a.dim) {
+#pragma unroll 8
+      for (int j = j0; j < j1; ++j) {
+        float x[V];
+        load_f32<float, V>(a.tail + (long long)j * a.dim + c, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += x[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[p][l * V + i] = sum[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kJoinLanes * V && c0 + i < a.dim; i += kThreads) {
+      float x = part[0][i];
+#pragma unroll
+      for (int q = 1; q < kJoinParts; ++q) x += part[q][i];
+      x += a.head[(long long)b * a.dim + c0 + i];
+      static_cast<TW*>(a.out)[(long long)r * a.out_stride + c0 + i] = (TW)(x * a.scale);
+    }
+    __syncthreads();
   }
 }
 
 // ----------------------------------------------------------- sizes, launches
 struct BwdPlan {
-  int bits, passes, tiles;
-  int v, lanes, groups, quantum, col_tiles;
+  int passes, digit_bits, per, tiles;
+  bool scanned;
+  int lane_bits, quantum, col_tiles;
   int64_t blocks;
   // byte offsets in the workspace
-  int64_t keys[2], places[2], hist, totals, first_row, began, head, tail, bytes;
+  int64_t sorted[2], hist, totals, first_row, began, head, tail, bytes;
 };
 
 BwdPlan bwd_plan(int64_t n, int64_t rows, int dim, int v) {
   BwdPlan p;
-  p.bits = 1;
-  while ((rows >> p.bits) != 0) ++p.bits;  // keys 0 .. rows
-  p.passes = (p.bits + kDigitBits - 1) / kDigitBits;
-  p.tiles = (int)((n + kSortTile - 1) / kSortTile);
-  p.v = v;
-  p.lanes = 8;
-  while (p.lanes < 64 && p.lanes * v < dim) p.lanes *= 2;
-  p.groups = kThreads / p.lanes;
-  p.col_tiles = (dim + p.lanes * v - 1) / (p.lanes * v);
+  int bits = 1;
+  while ((rows >> bits) != 0) ++bits;  // keys 0 .. rows
+  p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
+  p.digit_bits = (bits + p.passes - 1) / p.passes;
+  const int digits = 1 << p.digit_bits;
+  p.per = n <= (1 << 18) ? 4 : 16;
+  p.tiles = (int)((n + p.per * kThreads - 1) / (p.per * kThreads));
+  p.scanned = p.tiles > 64;
+  p.lane_bits = 0;
+  while (p.lane_bits < 6 && (v << p.lane_bits) < dim) ++p.lane_bits;
+  const int groups = kThreads >> p.lane_bits, columns = v << p.lane_bits;
+  p.col_tiles = (dim + columns - 1) / columns;
   const int64_t units = n + rows;
-  p.quantum = (int)std::min<int64_t>(128, std::max<int64_t>(8, units / ((int64_t)p.groups * 1024)));
-  p.blocks = (units + (int64_t)p.groups * p.quantum - 1) / ((int64_t)p.groups * p.quantum);
+  const int64_t most = std::min(128, kMaxUnits / groups);
+  p.quantum = (int)std::min<int64_t>(most, std::max<int64_t>(4, units / ((int64_t)groups * 1024)));
+  p.blocks = (units + (int64_t)groups * p.quantum - 1) / ((int64_t)groups * p.quantum);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
     at += round_up(bytes, 256);
     return o;
   };
-  for (int k = 0; k < 2; ++k) {
-    p.keys[k] = take(4 * n);
-    p.places[k] = take(4 * n);
-  }
-  p.hist = take(4ll * kDigits * p.tiles);
-  p.totals = take(4ll * kDigits);
+  for (int k = 0; k < 2; ++k) p.sorted[k] = take(8 * n);
+  p.hist = take(4ll * digits * p.tiles);
+  p.totals = take(4ll * digits);
   p.first_row = take(4 * (p.blocks + 1));
   p.began = take(4 * p.blocks);
   p.head = take(4 * p.blocks * dim);
@@ -420,29 +540,36 @@ BwdPlan bwd_plan(int64_t n, int64_t rows, int dim, int v) {
   return p;
 }
 
-template <typename TG, typename TW, int V>
-void launch_sum_v(const BwdPlan& p, const SumArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)p.blocks, (unsigned)p.col_tiles), block(kThreads);
-  switch (p.lanes) {
-    case 8: hipLaunchKernelGGL((k_embed_sum<TG, TW, V, 8>), grid, block, 0, s, a); break;
-    case 16: hipLaunchKernelGGL((k_embed_sum<TG, TW, V, 16>), grid, block, 0, s, a); break;
-    case 32: hipLaunchKernelGGL((k_embed_sum<TG, TW, V, 32>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_embed_sum<TG, TW, V, 64>), grid, block, 0, s, a); break;
+template <bool FIRST, int PER>
+void launch_sort(const BwdPlan& p, const SortArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)p.tiles), block(kThreads);
+  hipLaunchKernelGGL((k_sort_hist<FIRST, PER>), grid, block, 0, s, a);
+  if (p.scanned) {
+    hipLaunchKernelGGL(k_sort_scan, dim3((a.digits + kScanDigits - 1) / kScanDigits), block, 0, s, a);
+    hipLaunchKernelGGL((k_sort_scatter<FIRST, PER, true>), grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_sort_scatter<FIRST, PER, false>), grid, block, 0, s, a);
   }
 }
 
 template <typename TG, typename TW>
-void launch_sum(const BwdPlan& p, const SumArgs& a, hipStream_t s) {
-  if (p.v == 4)
-    launch_sum_v<TG, TW, 4>(p, a, s);
-  else if (p.v == 2)
-    launch_sum_v<TG, TW, 2>(p, a, s);
+void launch_sum(const BwdPlan& p, int v, const SumArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)p.blocks, (unsigned)p.col_tiles), block(kThreads);
+  switch (v) {
+    case 8:
+      if constexpr (sizeof(TG) == 2) hipLaunchKernelGGL((k_embed_sum<TG, TW, 8>), grid, block, 0, s, a);
+      break;
+    case 4: hipLaunchKernelGGL((k_embed_sum<TG, TW, 4>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((k_embed_sum<TG, TW, 2>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((k_embed_sum<TG, TW, 1>), grid, block, 0, s, a); break;
+  }
+  if (a.dim % 4 == 0)
+    hipLaunchKernelGGL((k_embed_join<TW, 4>), dim3((unsigned)p.blocks), block, 0, s, a);
   else
-    launch_sum_v<TG, TW, 1>(p, a, s);
-  hipLaunchKernelGGL((k_embed_join<TW>), dim3((unsigned)p.blocks), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_embed_join<TW, 1>), dim3((unsigned)p.blocks), block, 0, s, a);
 }
 
-constexpr int64_t kMaxTokens = (1ll << 31) - kSortTile;
+constexpr int64_t kMaxTokens = (1ll << 31) - 4096;
 constexpr int64_t kMaxVocab = 1ll << 30;
 constexpr int kMaxDim = 1 << 16;
 
@@ -481,7 +608,7 @@ recis_status recis_embed_fwd(const int64_t* tokens, int64_t n, const void* weigh
 int64_t recis_embed_bwd_workspace_bytes(int64_t n, int64_t rows, int32_t dim) {
   if (n < 0 || rows < 1 || dim < 1 || n > kMaxTokens || rows > kMaxVocab || dim > kMaxDim) return -1;
   int64_t most = 0;
-  for (int v : {1, 2, 4}) most = std::max(most, bwd_plan(n, rows, dim, v).bytes);
+  for (int v : {1, 2, 4, 8}) most = std::max(most, bwd_plan(n, rows, dim, v).bytes);
   return most;
 }
 
@@ -498,43 +625,37 @@ recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_
       !aligned_to(grad_weight, ws) || !aligned_to(error, 4))
     return RECIS_ERR_INVALID_ARG;
   // one access width for both sides: the gradients' and the result's rows
-  const int v = std::min(4, std::min(access_width(gs, dim, {grad_out}, {grad_stride}),
-                                     access_width(ws, dim, {grad_weight}, {weight_stride})));
+  // (a bfloat16 side may ask for eight elements, a float32 one for four; the
+  // float32 result of a bfloat16 gradient is then written in two accesses)
+  const int gv = access_width(gs, dim, {grad_out}, {grad_stride});
+  const int wv = access_width(ws, dim, {grad_weight}, {weight_stride});
+  const int v = gv == 8 && wv == 4 && ws == 4 ? 8 : std::min(gv, wv);
   const BwdPlan p = bwd_plan(n, rows, dim, v);
   if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.bytes) return RECIS_ERR_INVALID_ARG;
   if (p.blocks > (1ll << 31) - 1) return RECIS_ERR_UNSUPPORTED;
   char* w = static_cast<char*>(workspace);
-  unsigned* hist = reinterpret_cast<unsigned*>(w + p.hist);
-  unsigned* totals = reinterpret_cast<unsigned*>(w + p.totals);
-  const long long* tok = reinterpret_cast<const long long*>(tokens);
+  SortArgs o;
+  o.tokens = reinterpret_cast<const long long*>(tokens);
+  o.n = n;
+  o.rows = (unsigned)rows;
+  o.digits = 1 << p.digit_bits;
+  o.tiles = p.tiles;
+  o.hist = reinterpret_cast<unsigned*>(w + p.hist);
+  o.totals = reinterpret_cast<unsigned*>(w + p.totals);
+  o.error = error;
   int cur = 0;
-  if (n > 0) {
-    for (int pass = 0; pass < p.passes; ++pass) {
-      const unsigned* kin = reinterpret_cast<const unsigned*>(w + p.keys[cur]);
-      const unsigned* pin = reinterpret_cast<const unsigned*>(w + p.places[cur]);
-      unsigned* kout = reinterpret_cast<unsigned*>(w + p.keys[cur ^ 1]);
-      unsigned* pout = reinterpret_cast<unsigned*>(w + p.places[cur ^ 1]);
-      const int shift = pass * kDigitBits;
-      const dim3 grid((unsigned)p.tiles), block(kThreads);
-      if (pass == 0)
-        hipLaunchKernelGGL((k_sort_hist<true>), grid, block, 0, s, tok, kin, (long long)n, (unsigned)rows, shift, hist,
-                           error);
-      else
-        hipLaunchKernelGGL((k_sort_hist<false>), grid, block, 0, s, tok, kin, (long long)n, (unsigned)rows, shift,
-                           hist, error);
-      hipLaunchKernelGGL(k_sort_scan, dim3(kDigits), block, 0, s, hist, p.tiles, totals);
-      if (pass == 0)
-        hipLaunchKernelGGL((k_sort_scatter<true>), grid, block, 0, s, tok, kin, pin, (long long)n, (unsigned)rows,
-                           shift, hist, totals, kout, pout);
-      else
-        hipLaunchKernelGGL((k_sort_scatter<false>), grid, block, 0, s, tok, kin, pin, (long long)n, (unsigned)rows,
-                           shift, hist, totals, kout, pout);
-      cur ^= 1;
-    }
+  for (int pass = 0; n > 0 && pass < p.passes; ++pass) {
+    o.in = reinterpret_cast<const Keyed*>(w + p.sorted[cur]);
+    o.out = reinterpret_cast<Keyed*>(w + p.sorted[cur ^ 1]);
+    o.shift = pass * p.digit_bits;
+    if (p.per == 4)
+      pass == 0 ? launch_sort<true, 4>(p, o, s) : launch_sort<false, 4>(p, o, s);
+    else
+      pass == 0 ? launch_sort<true, 16>(p, o, s) : launch_sort<false, 16>(p, o, s);
+    cur ^= 1;
   }
   SumArgs a;
-  a.tok = reinterpret_cast<const unsigned*>(w + p.keys[cur]);
-  a.place = reinterpret_cast<const unsigned*>(w + p.places[cur]);
+  a.tok = reinterpret_cast<const Keyed*>(w + p.sorted[cur]);
   a.n = n;
   a.rows = rows;
   a.grad = grad_out;
@@ -544,19 +665,20 @@ recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_
   a.scale = scale;
   a.dim = dim;
   a.quantum = p.quantum;
+  a.lane_bits = p.lane_bits;
   a.first_row = reinterpret_cast<int*>(w + p.first_row);
   a.began = reinterpret_cast<int*>(w + p.began);
   a.head = reinterpret_cast<float*>(w + p.head);
   a.tail = reinterpret_cast<float*>(w + p.tail);
   const bool gb = grad_dtype == RECIS_DTYPE_BF16, wb = weight_dtype == RECIS_DTYPE_BF16;
   if (gb && wb)
-    launch_sum<__bf16, __bf16>(p, a, s);
+    launch_sum<__bf16, __bf16>(p, v, a, s);
   else if (gb)
-    launch_sum<__bf16, float>(p, a, s);
+    launch_sum<__bf16, float>(p, v, a, s);
   else if (wb)
-    launch_sum<float, __bf16>(p, a, s);
+    launch_sum<float, __bf16>(p, v, a, s);
   else
-    launch_sum<float, float>(p, a, s);
+    launch_sum<float, float>(p, v, a, s);
   return launch_status();
 }
 

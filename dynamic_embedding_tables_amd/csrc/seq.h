@@ -24,13 +24,18 @@ __device__ __forceinline__ void load_f32(const T* p, float (&v)[V]) {
   for (int i = 0; i < V; ++i) v[i] = (float)x.e[i];
 }
 
-// One rounding, to nearest with ties to even, where T is bfloat16.
+// One rounding, to nearest with ties to even, where T is bfloat16; 16 bytes a
+// store at most.
 template <typename T, int V>
 __device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
-  Vec<T, V> x;
+  constexpr int W = V * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
 #pragma unroll
-  for (int i = 0; i < V; ++i) x.e[i] = (T)v[i];
-  *reinterpret_cast<Vec<T, V>*>(p) = x;
+  for (int j = 0; j < V; j += W) {
+    Vec<T, W> x;
+#pragma unroll
+    for (int i = 0; i < W; ++i) x.e[i] = (T)v[j + i];
+    *reinterpret_cast<Vec<T, W>*>(p + j) = x;
+  }
 }
 
 // Widest access, in elements of `size` bytes, that the pointers, the row
