@@ -29,13 +29,15 @@
 namespace recis {
 namespace {
 
+constexpr int kMaxHeadDim = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
   const void *q, *k, *v, *o, *dout;
   void *out, *dq, *dk, *dv;
-  float *lse, *delta;
+  float* lse;
+  f32x2* stats;  // [batch * kv_heads][rows], from k_attn_bwd_q to k_attn_bwd_kv
   const int *kv_offsets, *kv_lens;
   const unsigned char* kv_mask;
   long long mask_stride, kv_rows;
@@ -43,11 +45,16 @@ struct AttnArgs {
   int batch, q_len, kv_len, q_heads, kv_heads, group, head_dim;
   int rows;                // q_len * group
   int row_tiles, key_tiles;
-  int splits, split_keys;  // forward: key ranges of a row tile, joined by k_attn_join
+  int dies;                    // pairs of (batch entry, key head) side by side in the grid
+  int splits, split_keys;      // forward: key ranges of a row tile, joined by k_attn_join
+  int q_splits, q_split_keys;  // dQ: the same, joined by k_attn_join_q
   float scale;
-  float *part_o, *part_ml;  // [batch * kv_heads][splits][rows][head_dim], [..][2]
+  float *part_o, *part_ml;     // [batch * kv_heads][splits][rows][head_dim], [..][2]
   unsigned* error;
 };
+
+// The wave's number, known to be the same in all its lanes.
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // ---------------------------------------------------------------- fragments
 template <typename T>
@@ -72,6 +79,35 @@ __device__ __forceinline__ f32x4 mma(f32x8 a, f32x8 b, f32x4 c) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
   return c;
+}
+
+// Four zeros that stay in registers: a product that starts from them needs no
+// moves (the compiler would clear its accumulator each time).
+__device__ __forceinline__ f32x4 zeros() {
+  f32x4 z{0.f, 0.f, 0.f, 0.f};
+  asm volatile("" : "+v"(z));
+  return z;
+}
+
+// LDS reads stay on their side of this point (everything else may cross): a
+// product's operands are all asked for before the first one is needed, where
+// the compiler, short of registers, would ask for two and wait, and so on.
+__device__ __forceinline__ void reads_before() { __builtin_amdgcn_sched_barrier(0x47F); }
+
+// The larger / the sum of a lane's value and those of the lanes 16, 32 and 48
+// away, by register swaps (no LDS access).
+template <typename F>
+__device__ __forceinline__ float across_groups(float x, F f) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float group_max(float x) {
+  return across_groups(x, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float group_add(float x) {
+  return across_groups(x, [](float a, float b) { return a + b; });
 }
 
 template <typename T>
@@ -113,14 +149,33 @@ __device__ __forceinline__ void store4(T* row, int d0, int dim, f32x4 x) {
   }
 }
 
-// LDS tile rows are padded by 16 bytes: 16 lanes reading one column of 16
-// rows then fall on distinct banks.
+// LDS tiles.  A bfloat16 tile is read by rows (8 lanes at a time take 16 bytes
+// of one column of 8 rows) and by columns (16 lanes take 32 bytes of 4 rows).
+// Both fall on distinct banks when the 16-byte chunks of a row are exchanged
+// by a number that differs over any 8 rows, and in its upper bits over any
+// aligned 4; padding the rows instead left the column reads two to a bank
+// (half of the backward's LDS time).  Float32 rows are padded by 16 bytes.
 template <typename T, int DP>
-constexpr int kLd = DP + 16 / (int)sizeof(T);
+constexpr int kLd = DP + (sizeof(T) == 2 ? 0 : 4);
+
+template <int DP>
+__device__ __forceinline__ int exchange(int row) {
+  if constexpr (DP == 32)  // two rows to the 128 bytes of all banks
+    return ((row >> 1 & 1) << 1) | (row >> 2 & 1);
+  else
+    return ((row & 3) << 1) | (row >> 2 & 1);
+}
+
+// Offset of 8 elements of a tile's row.
+template <typename T, int DP>
+__device__ __forceinline__ int chunk_at(int row, int chunk) {
+  return row * kLd<T, DP> + (sizeof(T) == 2 ? chunk ^ exchange<DP>(row) : chunk) * 8;
+}
 
 template <typename T, int DP>
 __device__ __forceinline__ Frag<T> read_rows(const T* tile, int row0, int c0, int lane) {
-  return *reinterpret_cast<const Frag<T>*>(tile + (row0 + (lane & 15)) * kLd<T, DP> + c0 + (lane >> 4) * 8);
+  return *reinterpret_cast<const Frag<T>*>(tile + row0 * kLd<T, DP> +
+                                           chunk_at<T, DP>(lane & 15, c0 / 8 + (lane >> 4)));
 }
 
 // Column c0 + lane % 16 of 32 rows, in the slot order of pack().
@@ -128,7 +183,9 @@ template <int DP>
 __device__ __forceinline__ bf16x8 read_cols(const __bf16* tile, int row0, int c0, int lane) {
   typedef short s16x4 __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const __bf16* p = tile + (row0 + (lane >> 4) * 4 + ((lane & 15) >> 2)) * kLd<__bf16, DP> + c0 + (lane & 3) * 4;
+  const int row = (lane >> 4) * 4 + ((lane & 15) >> 2);
+  const __bf16* p =
+      tile + row0 * kLd<__bf16, DP> + chunk_at<__bf16, DP>(row, c0 / 8 + ((lane & 3) >> 1)) + (lane & 1) * 4;
   // within 16 lanes: lane i names 4 columns of row i / 4, and receives column i of the 4 rows
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * kLd<__bf16, DP>));
@@ -183,12 +240,14 @@ __device__ __forceinline__ unsigned long long key_bits(const AttnArgs& a, const 
   return __ballot(in);
 }
 
-// Consecutive blocks go to the eight dies in turn; the blocks of one (batch
-// entry, key head) are given to the same die, so its keys stay in one L2.
-constexpr int kDies = 8;
+// Consecutive blocks go to the eight dies in turn.  With many (batch entry, key
+// head) pairs the blocks of one are given to the same die, so its keys stay in
+// one L2; with few, that would leave dies idle (9 entries of 0 to 1499 keys,
+// 2 heads: 31 us against 21), and a pair's blocks go to every die.
+constexpr int kDies = 8, kPairsForDies = 128;
 __device__ __forceinline__ bool place(const AttnArgs& a, int per, int* b, int* h, int* t) {
-  const int slot = blockIdx.x / kDies;
-  const int bh = (slot / per) * kDies + blockIdx.x % kDies;
+  const int slot = blockIdx.x / a.dies;
+  const int bh = (slot / per) * a.dies + blockIdx.x % a.dies;
   *t = slot % per;
   *b = bh / a.kv_heads;
   *h = bh % a.kv_heads;
@@ -206,29 +265,54 @@ __device__ __forceinline__ long long stat_at(const AttnArgs& a, int b, int h, in
   return ((long long)b * a.q_len + q) * a.q_heads + h * a.group + g;
 }
 
+// 8 elements at a base that every lane shares plus the lane's own byte offset
+// (one 32-bit register of address for all of a thread's loads).
+template <typename T>
+__device__ __forceinline__ Frag<T> load_at(const T* base, unsigned bytes) {
+  return *reinterpret_cast<const Frag<T>*>(reinterpret_cast<const char*>(base) + bytes);
+}
+
 // A tile of R rows x DP held in registers on its way to LDS.
 template <typename T, int DP, int R, bool ALN>
 struct Stage {
   static constexpr int kChunks = R * (DP / 8);
   static constexpr int kPer = (kChunks + kThreads - 1) / kThreads;
+  static constexpr int kStep = kThreads / (DP / 8);  // rows between a thread's chunks
   Frag<T> f[kPer];
+  const T* base;
+  int row, d0;
+  unsigned at;
+  __device__ __forceinline__ void start(const T* from, long long stride, int first) {
+    row = threadIdx.x / (DP / 8);
+    d0 = (threadIdx.x % (DP / 8)) * 8;
+    at = (unsigned)((row * stride + d0) * (long long)sizeof(T));  // ALN: fits (rows_aligned)
+    base = from + (long long)first * stride;
+  }
   // rows whose bit is clear are zero, whatever memory holds there
-  __device__ __forceinline__ void load(const T* base, long long stride, int first, unsigned long long bits, int dim) {
+  __device__ __forceinline__ void load(long long stride, unsigned long long bits, int dim) {
+    const bool all = ALN && dim == DP && bits == ~0ull && kChunks % kThreads == 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      const int r = c / (DP / 8), d0 = (c % (DP / 8)) * 8;
-      const bool in = (kChunks % kThreads == 0 || c < kChunks) && ((bits >> r) & 1);
-      f[i] = load8<T, ALN>(base + (long long)(first + r) * stride, d0, dim, in);
+      const T* from = base + (long long)(i * kStep) * stride;
+      const int r = row + i * kStep;
+      const bool in = r < R && ((bits >> (r & 63)) & 1);
+      if (all) {
+        f[i] = load_at<T>(from, at);
+      } else if constexpr (ALN) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[i][k] = (T)0.f;
+        if (in && d0 < dim) f[i] = load_at<T>(from, at);
+      } else {
+        f[i] = load8<T, ALN>(from + (long long)row * stride, d0, dim, in);
+      }
     }
+    base += (long long)R * stride;
   }
   __device__ __forceinline__ void store(T* tile) const {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      if (kChunks % kThreads == 0 || c < kChunks)
-        *reinterpret_cast<Frag<T>*>(tile + (c / (DP / 8)) * kLd<T, DP> + (c % (DP / 8)) * 8) = f[i];
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (kChunks % kThreads == 0 || row + i * kStep < R)
+        *reinterpret_cast<Frag<T>*>(tile + chunk_at<T, DP>(row + i * kStep, d0 / 8)) = f[i];
   }
 };
 
@@ -237,16 +321,21 @@ constexpr int kAttnWaves = kThreads / 64;
 
 // ------------------------------------------------------------------ forward
 // A wave holds QT tiles of 16 queries; the block walks the keys 64 at a time,
-// staged in LDS for its four waves, the next tile's loads in flight meanwhile.
+// staged in LDS for its four waves in two buffers (one barrier a tile), the
+// next tile's loads in flight meanwhile.  The running maximum that the weights
+// are taken relative to is raised only once a score exceeds it by 2^kSlack in
+// weight: the sum and the output stay exact relative to it, far from float32's
+// range, and most tiles need no rescaling of the output.
+constexpr float kSlack = 8.f;
 template <typename T, int DP, int QT, bool ALN>
-__global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void k_attn_fwd(AttnArgs a) {
   constexpr int KK = DP / 32, DT = DP / 16, NT = kBlockKeys / 16;
-  __shared__ __attribute__((aligned(16))) T tk[kBlockKeys * kLd<T, DP>];
-  __shared__ __attribute__((aligned(16))) T tv[kBlockKeys * kLd<T, DP>];
+  constexpr int kTile = kBlockKeys * kLd<T, DP>;
+  __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, t;
   if (!place(a, a.row_tiles * a.splits, &b, &h, &t)) return;
   const int split = t % a.splits, tile = t / a.splits;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_of();
   const Span sp = kv_span(a, b);
   const int key0 = split * a.split_keys;
   const int key1 = std::min(sp.len, key0 + a.split_keys);
@@ -263,45 +352,59 @@ __global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
     for (int c = 0; c < KK; ++c) q[j][c] = load8<T, ALN>(p, c * 32 + (lane >> 4) * 8, a.head_dim, in);
   }
   f32x4 o[QT][DT];
-  float m[QT], l[QT];
+  // maximum, the same in log2 of the weight (0 before the first key), how far a
+  // score may go before both are raised, sum
+  float m[QT], ref[QT], most[QT], l[QT];
 #pragma unroll
   for (int j = 0; j < QT; ++j) {
-    m[j] = -INFINITY;
-    l[j] = 0.f;
+    m[j] = most[j] = -INFINITY;
+    ref[j] = l[j] = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   const float c2 = a.scale * kLog2e;
+  const f32x4 zero = zeros();
   Stage<T, DP, kBlockKeys, ALN> sk, sv;
   unsigned long long bits = 0;
   if (key0 < key1) {
+    sk.start(kb, a.ks[1], key0);
+    sv.start(vb, a.vs[1], key0);
     bits = key_bits(a, sp, b, key0, lane);
-    sk.load(kb, a.ks[1], key0, bits, a.head_dim);
-    sv.load(vb, a.vs[1], key0, bits, a.head_dim);
+    sk.load(a.ks[1], bits, a.head_dim);
+    sv.load(a.vs[1], bits, a.head_dim);
   }
-  for (int first = key0; first < key1; first += kBlockKeys) {
-    __syncthreads();
+  int buffer = 0;
+  for (int first = key0; first < key1; first += kBlockKeys, buffer ^= 1) {
+    T* tk = tiles + buffer * 2 * kTile;
+    T* tv = tk + kTile;
     sk.store(tk);
     sv.store(tv);
     __syncthreads();
     const unsigned long long now = bits;
     if (first + kBlockKeys < key1) {
       bits = key_bits(a, sp, b, first + kBlockKeys, lane);
-      sk.load(kb, a.ks[1], first + kBlockKeys, bits, a.head_dim);
-      sv.load(vb, a.vs[1], first + kBlockKeys, bits, a.head_dim);
+      sk.load(a.ks[1], bits, a.head_dim);
+      sv.load(a.vs[1], bits, a.head_dim);
     }
     if (now == 0) continue;
     f32x4 s[NT][QT];
+    // as many operands ahead as 32 registers hold
+    constexpr int kAhead = std::max(1, std::min(NT, 16 * 4 / (KK * (int)sizeof(Frag<T>))));
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n0 = 0; n0 < NT; n0 += kAhead) {
+      Frag<T> f[kAhead][KK];
 #pragma unroll
-      for (int j = 0; j < QT; ++j) s[n][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < kAhead; ++n)
 #pragma unroll
-      for (int c = 0; c < KK; ++c) {
-        const Frag<T> f = read_rows<T, DP>(tk, n * 16, c * 32, lane);
+        for (int c = 0; c < KK; ++c) f[n][c] = read_rows<T, DP>(tk, (n0 + n) * 16, c * 32, lane);
+      reads_before();
+      // a sum's next product is issued as late as it can be
 #pragma unroll
-        for (int j = 0; j < QT; ++j) s[n][j] = mma(f, q[j][c], s[n][j]);
-      }
+      for (int c = 0; c < KK; ++c)
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n)
+#pragma unroll
+          for (int j = 0; j < QT; ++j) s[n0 + n][j] = mma(f[n][c], q[j][c], c == 0 ? zero : s[n0 + n][j]);
     }
     if (now != ~0ull) {
 #pragma unroll
@@ -312,30 +415,40 @@ __global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
             for (int j = 0; j < QT; ++j) s[n][j][i] = -INFINITY;
     }
+    float top[QT];
+    bool raise = false;
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
-      float top = m[j];
+      top[j] = s[0][j][0];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[n][j][i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float ref = top == -INFINITY ? 0.f : top * c2;
-      const float alpha = __builtin_amdgcn_exp2f(m[j] * c2 - ref);
-      m[j] = top;
-      float sum = 0.f;
+        for (int i = 0; i < 4; ++i) top[j] = fmaxf(top[j], s[n][j][i]);
+      top[j] = group_max(top[j]);
+      raise |= top[j] * c2 > most[j];
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        const float to = fmaxf(m[j], top[j]);
+        ref[j] = to == -INFINITY ? 0.f : to * c2;
+        const float alpha = __builtin_amdgcn_exp2f(m[j] * c2 - ref[j]);
+        m[j] = to;
+        most[j] = to == -INFINITY ? -INFINITY : ref[j] + kSlack;
+        l[j] *= alpha;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[j][d] *= alpha;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < QT; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[n][j][i] = __builtin_amdgcn_exp2f(s[n][j][i] * c2 - ref);
-          sum += s[n][j][i];
+          s[n][j][i] = __builtin_amdgcn_exp2f(s[n][j][i] * c2 - ref[j]);
+          l[j] += s[n][j][i];
         }
-      l[j] = l[j] * alpha + sum;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[j][d] *= alpha;
-    }
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
       Frag<T> p[QT];
@@ -352,8 +465,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
   for (int j = 0; j < QT; ++j) {
     const int r = row0 + j * 16;
-    l[j] += __shfl_xor(l[j], 16);
-    l[j] += __shfl_xor(l[j], 32);
+    l[j] = group_add(l[j]);
     if (r >= a.rows) continue;
     if (a.splits > 1) {
       const long long at = (((long long)b * a.kv_heads + h) * a.splits + split) * a.rows + r;
@@ -375,58 +487,253 @@ __global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
   }
 }
 
-// Joins the key ranges of a row: one wave a row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
-  const long long id = (long long)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (id >= (long long)a.batch * a.kv_heads * a.rows) return;
-  const int r = (int)(id % a.rows);
-  const long long bh = id / a.rows;
-  const int h = (int)(bh % a.kv_heads), b = (int)(bh / a.kv_heads);
-  const long long at = bh * a.splits * a.rows + r;
-  float top = -INFINITY;
-  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.part_ml[2 * (at + (long long)s * a.rows)]);
+// Few rows (16 at most: single queries, and their heads): the block's waves
+// take turns of 32 keys and meet once, at the end.  Keys go from memory into
+// the product's operand directly, values through LDS of the wave's own, so no
+// wave waits for another while the keys stream.
+constexpr int kFewRows = 16, kFewKeys = 32;
+
+template <typename T, int DP, bool ALN>
+__global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
+  constexpr int KK = DP / 32, DT = DP / 16, kPer = DP / 16;  // chunks of values a lane
+  constexpr int kTile = kFewKeys * kLd<T, DP>;
+  __shared__ __attribute__((aligned(128))) T tiles[kAttnWaves * kTile];
+  __shared__ float refs[kAttnWaves][kFewRows], sums[kAttnWaves][kFewRows];
+  static_assert(kTile * (int)sizeof(T) >= kFewRows * DP * 4, "a wave's output fits its tile");
+  int b, h, split;
+  if (!place(a, a.splits, &b, &h, &split)) return;
+  const int lane = threadIdx.x & 63, wave = wave_of();
+  const Span sp = kv_span(a, b);
+  const int key0 = split * a.split_keys;
+  const int key1 = std::min(sp.len, key0 + a.split_keys);
+  const T* kb = kv_base<T>(a.k, a.ks, a, sp, b, h);
+  const T* vb = kv_base<T>(a.v, a.vs, a, sp, b, h);
+  const float c2 = a.scale * kLog2e;
+  const f32x4 zero = zeros();
+  Frag<T> q[KK];
+  {
+    const int r = lane & 15;
+    const bool in = r < a.rows;
+    const T* p = static_cast<const T*>(a.q) + (in ? row_at(a, a.qs, b, h, r) : 0);
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float o[2] = {0.f, 0.f}, l = 0.f;  // head_dim <= 128
-  for (int s = 0; s < a.splits; ++s) {
-    const long long p = at + (long long)s * a.rows;
-    const float w = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ref);
-    if (w == 0.f) continue;
-    l += w * a.part_ml[2 * p + 1];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 64 * i < a.head_dim) o[i] += w * a.part_o[p * a.head_dim + lane + 64 * i];
+    for (int c = 0; c < KK; ++c) q[c] = load8<T, ALN>(p, c * 32 + (lane >> 4) * 8, a.head_dim, in);
   }
+  Frag<T> kf[2][KK], vf[kPer];
+  // a lane's place in the operand of 16 keys, and in 64 chunks of values
+  const int kr = lane & 15, kd = (lane >> 4) * 8, vr = lane / (DP / 8), vd = (lane % (DP / 8)) * 8;
+  constexpr int kRows = 64 / (DP / 8);
+  const unsigned k_at = (unsigned)((kr * a.ks[1] + kd) * (long long)sizeof(T));  // ALN: fits (rows_aligned)
+  const unsigned v_at = (unsigned)((vr * a.vs[1] + vd) * (long long)sizeof(T));
+  auto fetch = [&](int first, unsigned bits) {
+    const T* kp = kb + (long long)first * a.ks[1];
+    const T* vp = vb + (long long)first * a.vs[1];
+    if (ALN && a.head_dim == DP && bits == ~0u) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < KK; ++c) kf[u][c] = load_at<T>(kp + u * 16 * a.ks[1] + c * 32, k_at);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) vf[i] = load_at<T>(vp + (long long)(i * kRows) * a.vs[1], v_at);
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < KK; ++c)
+        kf[u][c] = load8<T, ALN>(kp + (long long)(u * 16 + kr) * a.ks[1], c * 32 + kd, a.head_dim,
+                                 (bits >> (u * 16 + kr)) & 1);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      vf[i] = load8<T, ALN>(vp + (long long)(i * kRows + vr) * a.vs[1], vd, a.head_dim, (bits >> (i * kRows + vr)) & 1);
+  };
+  f32x4 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = zero;
+  float m = -INFINITY, ref = 0.f, most = -INFINITY, l = 0.f;
+  T* tv = tiles + wave * kTile;
+  constexpr int kStep = kFewKeys * kAttnWaves;
+  unsigned bits = 0;
+  int first = key0 + wave * kFewKeys;
+  if (first < key1) {
+    bits = (unsigned)key_bits(a, sp, b, first, lane);
+    fetch(first, bits);
+  }
+  for (; first < key1; first += kStep) {
+    const unsigned now = bits;
+    f32x4 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u] = zero;
+#pragma unroll
+      for (int c = 0; c < KK; ++c) s[u] = mma(kf[u][c], q[c], s[u]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int c = i * 64 + lane;
+      *reinterpret_cast<Frag<T>*>(tv + chunk_at<T, DP>(c / (DP / 8), c % (DP / 8))) = vf[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are executed in order
+    if (first + kStep < key1) {
+      bits = (unsigned)key_bits(a, sp, b, first + kStep, lane);
+      fetch(first + kStep, bits);
+    }
+    if (now != ~0u) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((now >> (u * 16 + (lane >> 4) * 4 + i)) & 1)) s[u][i] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][i]);
+    top = group_max(top);
+    if (__any(top * c2 > most)) {
+      const float to = fmaxf(m, top);
+      ref = to == -INFINITY ? 0.f : to * c2;
+      const float alpha = __builtin_amdgcn_exp2f(m * c2 - ref);
+      m = to;
+      most = to == -INFINITY ? -INFINITY : ref + kSlack;
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= alpha;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[u][i] = __builtin_amdgcn_exp2f(s[u][i] * c2 - ref);
+        l += s[u][i];
+      }
+    const Frag<T> p = pack<T>(s[0], s[1]);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = mma(read_cols<DP>(tv, 0, d * 16, lane), p, o[d]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  l = group_add(l);
+  float* mine = reinterpret_cast<float*>(tv);  // [row][DP]
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+    *reinterpret_cast<f32x4*>(mine + (lane & 15) * DP + d * 16 + (lane >> 4) * 4) = o[d];
+  if (lane < 16) {
+    refs[wave][lane] = m * c2;
+    sums[wave][lane] = l;
+  }
+  __syncthreads();
+  // 16 threads a row, DT elements each
+  const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * DT;
+  if (r >= a.rows) return;
+  float top = refs[0][r];
+#pragma unroll
+  for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, refs[w][r]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, out[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) out[i] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kAttnWaves; ++w) {
+    const float weight = __builtin_amdgcn_exp2f(refs[w][r] - base);
+    sum += weight * sums[w][r];
+    const float* from = reinterpret_cast<const float*>(tiles + w * kTile) + r * DP + d0;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) out[i] += weight * from[i];
+  }
+  if (a.splits > 1) {
+    const long long at = (((long long)b * a.kv_heads + h) * a.splits + split) * a.rows + r;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+      if (d0 + i < a.head_dim) a.part_o[at * a.head_dim + d0 + i] = out[i];
+    if (d0 == 0) {
+      a.part_ml[2 * at] = top;
+      a.part_ml[2 * at + 1] = sum;
+    }
+    return;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* to = static_cast<T*>(a.out) + row_at(a, a.os, b, h, r);
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+    if (d0 + i < a.head_dim) to[d0 + i] = (T)(out[i] * inv);
+  if (a.lse && d0 == 0) a.lse[stat_at(a, b, h, r)] = sum == 0.f ? -INFINITY : top * kLn2 + __logf(sum);
+}
+
+// Joins the key ranges of a row: WAVES waves a row, consecutive ranges each.
+template <typename T, int WAVES>
+__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
+  constexpr int kParts = kMaxHeadDim / 64;
+  __shared__ float part[kAttnWaves][kMaxHeadDim + 1];
+  const int lane = threadIdx.x & 63, wave = wave_of(), w = wave % WAVES;
+  const long long id = (long long)blockIdx.x * (kAttnWaves / WAVES) + wave / WAVES;
+  const bool in = id < (long long)a.batch * a.kv_heads * a.rows;
+  const int r = (int)(id % a.rows), bh = (int)(id / a.rows);
+  const int h = bh % a.kv_heads, b = bh / a.kv_heads;
+  const long long at = (long long)bh * a.splits * a.rows + r;
+  float top = -INFINITY, ref = 0.f, o[kParts] = {}, l = 0.f;
+  if (in) {
+    for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.part_ml[2 * (at + (long long)s * a.rows)]);
+    top = group_max(top);
+#pragma unroll
+    for (int k = 1; k < 16; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+    ref = top == -INFINITY ? 0.f : top;
+    const int per = (a.splits + WAVES - 1) / WAVES;
+    const int s1 = std::min(a.splits, (w + 1) * per);
+#pragma unroll 4
+    for (int s = w * per; s < s1; ++s) {
+      const long long p = at + (long long)s * a.rows;
+      const float weight = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ref);
+      l += weight * a.part_ml[2 * p + 1];
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+        if (lane + 64 * i < a.head_dim) o[i] += weight * a.part_o[p * a.head_dim + lane + 64 * i];
+    }
+  }
+  if constexpr (WAVES > 1) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) part[wave][lane + 64 * i] = o[i];
+    if (lane == 0) part[wave][kMaxHeadDim] = l;
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) {
+      l += part[wave + k][kMaxHeadDim];
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) o[i] += part[wave + k][lane + 64 * i];
+    }
+  }
+  if (!in) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* out = static_cast<T*>(a.out) + row_at(a, a.os, b, h, r);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < kParts; ++i)
     if (lane + 64 * i < a.head_dim) out[lane + 64 * i] = (T)(o[i] * inv);
   if (a.lse && lane == 0) a.lse[stat_at(a, b, h, r)] = l == 0.f ? -INFINITY : top * kLn2 + __logf(l);
 }
 
 // ----------------------------------------------------------------- backward
-// dQ (and delta, which k_attn_bwd_kv reads): the forward's walk over the keys,
-// with P from the saved L.
+// dQ, and for k_attn_bwd_kv each row's L and delta in the form it starts its
+// sums with: the forward's walk over the keys, with P from the saved L.
 template <typename T, int DP, int QT, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
   constexpr int KK = DP / 32, DT = DP / 16;
-  __shared__ __attribute__((aligned(16))) T tk[kBlockKeys * kLd<T, DP>];
-  __shared__ __attribute__((aligned(16))) T tv[kBlockKeys * kLd<T, DP>];
+  constexpr int kTile = kBlockKeys * kLd<T, DP>;
+  __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, tile;
-  if (!place(a, a.row_tiles, &b, &h, &tile)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (!place(a, a.row_tiles * a.q_splits, &b, &h, &tile)) return;
+  const int split = tile % a.q_splits;
+  tile /= a.q_splits;
+  const int lane = threadIdx.x & 63, wave = wave_of();
   const Span sp = kv_span(a, b);
   const T* kb = kv_base<T>(a.k, a.ks, a, sp, b, h);
   const T* vb = kv_base<T>(a.v, a.vs, a, sp, b, h);
   const int row0 = tile * (16 * QT * kAttnWaves) + wave * 16 * QT + (lane & 15);
   const float c2 = a.scale * kLog2e;
+  const f32x4 zero = zeros();
   Frag<T> q[QT][KK], g[QT][KK];
   f32x4 dq[QT][DT];
-  float lse2[QT], delta[QT];
+  float lse2[QT];
+  f32x4 start[QT];  // -delta
 #pragma unroll
   for (int j = 0; j < QT; ++j) {
     const int r = row0 + j * 16;
@@ -444,67 +751,90 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += (float)g[j][c][i] * (float)o[i];
     }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    delta[j] = sum;
+    sum = group_add(sum);
+    start[j] = f32x4{-sum, -sum, -sum, -sum};
     const float lse = in ? a.lse[stat_at(a, b, h, r)] : 0.f;
     lse2[j] = in && lse != -INFINITY ? lse * kLog2e : INFINITY;  // exp2(s - inf) = 0
-    if (in && lane < 16) a.delta[((long long)b * a.kv_heads + h) * a.rows + r] = sum;
+    if (in && lane < 16 && split == 0)
+      a.stats[((long long)b * a.kv_heads + h) * a.rows + r] = f32x2{sizeof(T) == 2 ? -lse2[j] / c2 : lse2[j], -sum};
 #pragma unroll
     for (int d = 0; d < DT; ++d) dq[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   Stage<T, DP, kBlockKeys, ALN> sk, sv;
   unsigned long long bits = 0;
-  if (sp.len > 0) {
-    bits = key_bits(a, sp, b, 0, lane);
-    sk.load(kb, a.ks[1], 0, bits, a.head_dim);
-    sv.load(vb, a.vs[1], 0, bits, a.head_dim);
+  const int key0 = split * a.q_split_keys;
+  const int key1 = std::min(sp.len, key0 + a.q_split_keys);
+  if (key0 < key1) {
+    sk.start(kb, a.ks[1], key0);
+    sv.start(vb, a.vs[1], key0);
+    bits = key_bits(a, sp, b, key0, lane);
+    sk.load(a.ks[1], bits, a.head_dim);
+    sv.load(a.vs[1], bits, a.head_dim);
   }
-  for (int first = 0; first < sp.len; first += kBlockKeys) {
-    __syncthreads();
+  int buffer = 0;
+  for (int first = key0; first < key1; first += kBlockKeys, buffer ^= 1) {
+    T* tk = tiles + buffer * 2 * kTile;
+    T* tv = tk + kTile;
     sk.store(tk);
     sv.store(tv);
     __syncthreads();
     const unsigned long long now = bits;
-    if (first + kBlockKeys < sp.len) {
+    if (first + kBlockKeys < key1) {
       bits = key_bits(a, sp, b, first + kBlockKeys, lane);
-      sk.load(kb, a.ks[1], first + kBlockKeys, bits, a.head_dim);
-      sv.load(vb, a.vs[1], first + kBlockKeys, bits, a.head_dim);
+      sk.load(a.ks[1], bits, a.head_dim);
+      sv.load(a.vs[1], bits, a.head_dim);
     }
     if (now == 0) continue;
 #pragma unroll
     for (int n = 0; n < kBlockKeys; n += 32) {
       f32x4 s[2][QT], dp[2][QT];
+      Frag<T> fk[2][KK], fv[2][KK];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < KK; ++c) {
+          fk[u][c] = read_rows<T, DP>(tk, n + u * 16, c * 32, lane);
+          fv[u][c] = read_rows<T, DP>(tv, n + u * 16, c * 32, lane);
+        }
+      if constexpr (sizeof(T) == 2) reads_before();
+#pragma unroll
+      for (int c = 0; c < KK; ++c)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < QT; ++j) {
+            s[u][j] = mma(fk[u][c], q[j][c], c == 0 ? zero : s[u][j]);
+            dp[u][j] = mma(fv[u][c], g[j][c], c == 0 ? start[j] : dp[u][j]);  // dP - delta, for nothing
+          }
+      Frag<T> ft[DT];  // on their way during the exponentials
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) ft[d] = read_cols<DP>(tk, n, d * 16, lane);
+        reads_before();
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int j = 0; j < QT; ++j) s[u][j] = dp[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < KK; ++c) {
-          const Frag<T> fk = read_rows<T, DP>(tk, n + u * 16, c * 32, lane);
-          const Frag<T> fv = read_rows<T, DP>(tv, n + u * 16, c * 32, lane);
+          for (int j = 0; j < QT; ++j)
+            s[u][j][i] = __builtin_amdgcn_exp2f(s[u][j][i] * c2 - lse2[j]) * dp[u][j][i];
+      }
+      if (now != ~0ull) {
 #pragma unroll
-          for (int j = 0; j < QT; ++j) {
-            s[u][j] = mma(fk, q[j][c], s[u][j]);
-            dp[u][j] = mma(fv, g[j][c], dp[u][j]);
-          }
-        }
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = (now >> (n + u * 16 + (lane >> 4) * 4 + i)) & 1;
+          for (int i = 0; i < 4; ++i)
+            if (!((now >> (n + u * 16 + (lane >> 4) * 4 + i)) & 1))
 #pragma unroll
-          for (int j = 0; j < QT; ++j) {
-            const float p = __builtin_amdgcn_exp2f(s[u][j][i] * c2 - lse2[j]);
-            s[u][j][i] = in ? p * (dp[u][j][i] - delta[j]) : 0.f;
-          }
-        }
+              for (int j = 0; j < QT; ++j) s[u][j][i] = 0.f;
       }
       Frag<T> ds[QT];
 #pragma unroll
       for (int j = 0; j < QT; ++j) ds[j] = pack<T>(s[0][j], s[1][j]);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        const Frag<T> f = read_cols<DP>(tk, n, d * 16, lane);
+        const Frag<T> f = sizeof(T) == 2 ? ft[d] : read_cols<DP>(tk, n, d * 16, lane);
 #pragma unroll
         for (int j = 0; j < QT; ++j) dq[j][d] = mma(f, ds[j], dq[j][d]);
       }
@@ -514,27 +844,111 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
   for (int j = 0; j < QT; ++j) {
     const int r = row0 + j * 16;
     if (r >= a.rows) continue;
+    if (a.q_splits > 1) {
+      const long long at = (((long long)b * a.kv_heads + h) * a.q_splits + split) * a.rows + r;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        store4<float, false>(a.part_o + at * a.head_dim, d * 16 + (lane >> 4) * 4, a.head_dim, dq[j][d]);
+      continue;
+    }
     T* out = static_cast<T*>(a.dq) + row_at(a, a.dqs, b, h, r);
 #pragma unroll
     for (int d = 0; d < DT; ++d) store4<T, ALN>(out, d * 16 + (lane >> 4) * 4, a.head_dim, dq[j][d] * a.scale);
   }
 }
 
+// Adds the key ranges' parts of dQ, in order: a wave a row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_attn_join_q(AttnArgs a) {
+  const long long id = (long long)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (id >= (long long)a.batch * a.kv_heads * a.rows) return;
+  const int r = (int)(id % a.rows), bh = (int)(id / a.rows);
+  const float* from = a.part_o + ((long long)bh * a.q_splits * a.rows + r) * a.head_dim;
+  T* out = static_cast<T*>(a.dq) + row_at(a, a.dqs, bh / a.kv_heads, bh % a.kv_heads, r);
+  for (int d = lane; d < a.head_dim; d += 64) {
+    float sum = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < a.q_splits; ++s) sum += from[(long long)s * a.rows * a.head_dim + d];
+    out[d] = (T)(sum * a.scale);
+  }
+}
+
 // dK and dV: a wave holds KT tiles of 16 keys and walks the rows, kBlockRows
 // at a time, staged in LDS.  Here the scores have rows as rows, so a lane
-// holds rows of one key.
-constexpr int kBlockRows = 32;
+// holds rows of one key.  A key that does not count spoils its own column
+// only, which is written as zero at the end.
+template <int DP>
+constexpr int kBlockRows = DP <= 64 ? 64 : 32;
+
+// Walks a thread's chunks of the folded rows of two tensors (Q and dO).
+template <typename T, int DP, bool ALN>
+struct RowStage {
+  static constexpr int R = kBlockRows<DP>;
+  static constexpr int kChunks = R * (DP / 8);
+  static constexpr int kPer = (kChunks + kThreads - 1) / kThreads;
+  static constexpr int kStep = kThreads / (DP / 8);
+  Frag<T> fq[kPer], fg[kPer];
+  const T *pq[kPer], *pg[kPer];  // of the row that comes next
+  int head[kPer];                // its head in the group
+  int row, d0;
+  __device__ __forceinline__ void start(const AttnArgs& a, int b, int h) {
+    row = threadIdx.x / (DP / 8);
+    d0 = (threadIdx.x % (DP / 8)) * 8;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = row + i * kStep;
+      head[i] = r % a.group;
+      pq[i] = static_cast<const T*>(a.q) + row_at(a, a.qs, b, h, r);
+      pg[i] = static_cast<const T*>(a.dout) + row_at(a, a.dos, b, h, r);
+    }
+  }
+  // `left` rows from the next one on exist; the others are zero
+  __device__ __forceinline__ void load(const AttnArgs& a, int left) {
+    const bool all = ALN && a.head_dim == DP && left >= R && kChunks % kThreads == 0;
+    const int dq = R / a.group, dh = R % a.group;  // R rows on
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (all) {
+        fq[i] = *reinterpret_cast<const Frag<T>*>(pq[i] + d0);
+        fg[i] = *reinterpret_cast<const Frag<T>*>(pg[i] + d0);
+      } else {
+        const bool in = row + i * kStep < std::min(left, R);
+        fq[i] = load8<T, ALN>(pq[i], d0, a.head_dim, in);
+        fg[i] = load8<T, ALN>(pg[i], d0, a.head_dim, in);
+      }
+      pq[i] += dq * a.qs[1] + dh * a.qs[2];
+      pg[i] += dq * a.dos[1] + dh * a.dos[2];
+      if (dh) {
+        head[i] += dh;
+        if (head[i] >= a.group) {
+          head[i] -= a.group;
+          pq[i] += a.qs[1] - a.group * a.qs[2];
+          pg[i] += a.dos[1] - a.group * a.dos[2];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* tq, T* tg) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (kChunks % kThreads == 0 || row + i * kStep < R) {
+        const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
+        *reinterpret_cast<Frag<T>*>(tq + at) = fq[i];
+        *reinterpret_cast<Frag<T>*>(tg + at) = fg[i];
+      }
+  }
+};
 
 template <typename T, int DP, int KT, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int KK = DP / 32, DT = DP / 16;
-  __shared__ __attribute__((aligned(16))) T tq[kBlockRows * kLd<T, DP>];
-  __shared__ __attribute__((aligned(16))) T tg[kBlockRows * kLd<T, DP>];
-  __shared__ __attribute__((aligned(16))) float tl[kBlockRows];
-  __shared__ __attribute__((aligned(16))) float td[kBlockRows];
+  constexpr int R = kBlockRows<DP>, kTile = R * kLd<T, DP>;
+  __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
+  __shared__ __attribute__((aligned(16))) float stats[2][2 * R];
   int b, h, tile;
   if (!place(a, a.key_tiles, &b, &h, &tile)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_of();
   const Span sp = kv_span(a, b);
   const int block_key = tile * (16 * KT * kAttnWaves);
   if (tile == 0 && a.kv_offsets) {  // packed rows before the first entry and after the last: zero
@@ -574,78 +988,93 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) dk[j][d] = dv[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  const long long stat0 = ((long long)b * a.kv_heads + h) * a.rows;
+  const f32x2* row_stats = a.stats + ((long long)b * a.kv_heads + h) * a.rows;
   const int rows = block_key < sp.len ? a.rows : 0;
-  constexpr int kChunks = kBlockRows * (DP / 8), kPer = (kChunks + kThreads - 1) / kThreads;
-  Frag<T> sq[kPer], sg[kPer];
-  float sl = INFINITY, sd = 0.f;
-  auto stage = [&](int first) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      const int r = first + c / (DP / 8), d0 = (c % (DP / 8)) * 8;
-      const bool ok = c < kChunks && r < rows;
-      sq[i] = load8<T, ALN>(static_cast<const T*>(a.q) + (ok ? row_at(a, a.qs, b, h, r) : 0), d0, a.head_dim, ok);
-      sg[i] = load8<T, ALN>(static_cast<const T*>(a.dout) + (ok ? row_at(a, a.dos, b, h, r) : 0), d0, a.head_dim, ok);
-    }
-    if (threadIdx.x < kBlockRows) {
-      const int r = first + threadIdx.x;
-      const float lse = r < rows ? a.lse[stat_at(a, b, h, r)] : -INFINITY;
-      sl = lse == -INFINITY ? INFINITY : lse * kLog2e;
-      sd = r < rows ? a.delta[stat0 + r] : 0.f;
-    }
-  };
-  if (rows > 0) stage(0);
-  for (int first = 0; first < rows; first += kBlockRows) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      if (c < kChunks) {
-        const int at = (c / (DP / 8)) * kLd<T, DP> + (c % (DP / 8)) * 8;
-        *reinterpret_cast<Frag<T>*>(tq + at) = sq[i];
-        *reinterpret_cast<Frag<T>*>(tg + at) = sg[i];
-      }
-    }
-    if (threadIdx.x < kBlockRows) {
-      tl[threadIdx.x] = sl;
-      td[threadIdx.x] = sd;
+  // rows that do not exist: weight 0
+  const f32x2 none{sizeof(T) == 2 ? -INFINITY : INFINITY, 0.f};
+  RowStage<T, DP, ALN> st;
+  f32x2 stat = none;
+  if (rows > 0) {
+    st.start(a, b, h);
+    st.load(a, rows);
+    if ((int)threadIdx.x < std::min(rows, R)) stat = row_stats[threadIdx.x];
+  }
+  int buffer = 0;
+  for (int first = 0; first < rows; first += R, buffer ^= 1) {
+    T* tq = tiles + buffer * 2 * kTile;
+    T* tg = tq + kTile;
+    float* tl = stats[buffer];
+    float* td = tl + R;
+    st.store(tq, tg);
+    if (threadIdx.x < R) {
+      tl[threadIdx.x] = stat[0];
+      td[threadIdx.x] = stat[1];
     }
     __syncthreads();
-    if (first + kBlockRows < rows) stage(first + kBlockRows);
-    f32x4 s[2][KT], dp[2][KT];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int j = 0; j < KT; ++j) s[u][j] = dp[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < KK; ++c) {
-        const Frag<T> fq = read_rows<T, DP>(tq, u * 16, c * 32, lane);
-        const Frag<T> fg = read_rows<T, DP>(tg, u * 16, c * 32, lane);
-#pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          s[u][j] = mma(fq, k[j][c], s[u][j]);
-          dp[u][j] = mma(fg, v[j][c], dp[u][j]);
-        }
-      }
-      const f32x4 l4 = *reinterpret_cast<const f32x4*>(tl + u * 16 + (lane >> 4) * 4);
-      const f32x4 d4 = *reinterpret_cast<const f32x4*>(td + u * 16 + (lane >> 4) * 4);
-#pragma unroll
-      for (int j = 0; j < KT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = in[j] ? __builtin_amdgcn_exp2f(s[u][j][i] * c2 - l4[i]) : 0.f;
-          s[u][j][i] = p;
-          dp[u][j][i] = in[j] ? p * (dp[u][j][i] - d4[i]) : 0.f;
-        }
+    const int left = rows - first - R;
+    if (left > 0) {
+      st.load(a, left);
+      stat = (int)threadIdx.x < std::min(left, R) ? row_stats[first + R + threadIdx.x] : none;
     }
 #pragma unroll
-    for (int j = 0; j < KT; ++j) {
-      const Frag<T> p = pack<T>(s[0][j], s[1][j]), ds = pack<T>(dp[0][j], dp[1][j]);
+    for (int n = 0; n < R; n += 32) {
+      f32x4 s[2][KT], dp[2][KT], l4[2], d4[2];
+      Frag<T> fq[2][KK], fg[2][KK];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        l4[u] = *reinterpret_cast<const f32x4*>(tl + n + u * 16 + (lane >> 4) * 4);
+        d4[u] = *reinterpret_cast<const f32x4*>(td + n + u * 16 + (lane >> 4) * 4);
+#pragma unroll
+        for (int c = 0; c < KK; ++c) {
+          fq[u][c] = read_rows<T, DP>(tq, n + u * 16, c * 32, lane);
+          fg[u][c] = read_rows<T, DP>(tg, n + u * 16, c * 32, lane);
+        }
+      }
+      if constexpr (sizeof(T) == 2) reads_before();
+      // the products' sums start at -L / scale and -delta (in float32 the
+      // scores start at 0: there the extra rounding would show)
+#pragma unroll
+      for (int c = 0; c < KK; ++c)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < KT; ++j) {
+            const f32x4 from = sizeof(T) == 2 ? l4[u] : f32x4{0.f, 0.f, 0.f, 0.f};
+            s[u][j] = mma(fq[u][c], k[j][c], c == 0 ? from : s[u][j]);
+            dp[u][j] = mma(fg[u][c], v[j][c], c == 0 ? d4[u] : dp[u][j]);
+          }
+      Frag<T> tgf[DT], tqf[DT];  // on their way during the exponentials
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          tgf[d] = read_cols<DP>(tg, n, d * 16, lane);
+          tqf[d] = read_cols<DP>(tq, n, d * 16, lane);
+        }
+        reads_before();
+      }
+      Frag<T> p[KT], ds[KT];
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = sizeof(T) == 2 ? s[u][j][i] * c2 : s[u][j][i] * c2 - l4[u][i];
+            s[u][j][i] = __builtin_amdgcn_exp2f(x);
+            dp[u][j][i] *= s[u][j][i];
+          }
+        p[j] = pack<T>(s[0][j], s[1][j]);
+        ds[j] = pack<T>(dp[0][j], dp[1][j]);
+      }
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        dv[j][d] = mma(read_cols<DP>(tg, 0, d * 16, lane), p, dv[j][d]);
-        dk[j][d] = mma(read_cols<DP>(tq, 0, d * 16, lane), ds, dk[j][d]);
+        const Frag<T> cg = sizeof(T) == 2 ? tgf[d] : read_cols<DP>(tg, n, d * 16, lane);
+        const Frag<T> cq = sizeof(T) == 2 ? tqf[d] : read_cols<DP>(tq, n, d * 16, lane);
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+          dv[j][d] = mma(cg, p[j], dv[j][d]);
+          dk[j][d] = mma(cq, ds[j], dk[j][d]);
+        }
       }
     }
   }
@@ -658,8 +1087,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       const int d0 = d * 16 + (lane >> 4) * 4;
-      store4<T, ALN>(dkb + (long long)key * a.dks[1], d0, a.head_dim, dk[j][d] * a.scale);
-      store4<T, ALN>(dvb + (long long)key * a.dvs[1], d0, a.head_dim, dv[j][d]);
+      const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+      store4<T, ALN>(dkb + (long long)key * a.dks[1], d0, a.head_dim, in[j] ? dk[j][d] * a.scale : zero);
+      store4<T, ALN>(dvb + (long long)key * a.dvs[1], d0, a.head_dim, in[j] ? dv[j][d] : zero);
     }
   }
 }
@@ -667,11 +1097,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
 // ----------------------------------------------------------- sizes, launches
 struct AttnPlan {
   int dp, qt, kt;
-  int row_tiles, key_tiles, splits, split_keys;
-  int64_t part_o, part_ml, fwd_bytes, bwd_bytes;
+  bool few;
+  int row_tiles, key_tiles, splits, split_keys, q_splits, q_split_keys;
+  int64_t part_ml, part_dq, fwd_bytes, bwd_bytes;
 };
-
-constexpr int kMaxHeadDim = 128;
 
 recis_status check_desc(const recis_attn_desc* d) {
   if (!d || !dtype_known(d->dtype) || d->batch < 0 || d->q_len < 0 || d->kv_len < 0 || d->q_heads < 1 ||
@@ -687,6 +1116,8 @@ recis_status check_desc(const recis_attn_desc* d) {
   return RECIS_OK;
 }
 
+constexpr int kMaxSplits = 256;
+
 AttnPlan attn_plan(const recis_attn_desc* d) {
   AttnPlan p;
   p.dp = d->head_dim <= 32 ? 32 : d->head_dim <= 64 ? 64 : 128;
@@ -696,15 +1127,20 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
   p.kt = d->dtype == RECIS_DTYPE_BF16 && p.dp <= 64 ? 2 : 1;
   p.row_tiles = (int)((rows + 64 * p.qt - 1) / (64 * p.qt));
   p.key_tiles = std::max(1, (int)(((int64_t)d->kv_len + 64 * p.kt - 1) / (64 * p.kt)));
-  // keys are split until there are some 2048 blocks, at least 256 keys each
-  const int64_t blocks = std::max<int64_t>(1, bh * p.row_tiles);
-  const int64_t want = std::max<int64_t>(1, 2048 / blocks);
-  p.split_keys = (int)std::max<int64_t>(256, round_up((d->kv_len + want - 1) / want, kBlockKeys));
-  p.splits = std::max(1, (int)(((int64_t)d->kv_len + p.split_keys - 1) / p.split_keys));
-  p.part_o = 0;
+  p.few = rows <= kFewRows;
+  // keys are split until there are `want` blocks (of unequal length where the
+  // entries' are), `least` keys each, kMaxSplits ranges at most
+  auto split = [&](int64_t blocks, int64_t want, int64_t least, int* splits, int* keys) {
+    const int64_t n = std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, want / std::max<int64_t>(1, blocks)));
+    *keys = (int)std::max<int64_t>(least, round_up((d->kv_len + n - 1) / n, 2 * kBlockKeys));
+    *splits = std::max(1, (int)(((int64_t)d->kv_len + *keys - 1) / *keys));
+  };
+  split(bh * p.row_tiles, p.few ? 2048 : 1024, p.few ? 256 : 128, &p.splits, &p.split_keys);
+  split(bh * p.row_tiles, 1024, 128, &p.q_splits, &p.q_split_keys);
   p.part_ml = round_up(bh * p.splits * rows * d->head_dim * 4, 256);
   p.fwd_bytes = p.splits > 1 ? p.part_ml + round_up(bh * p.splits * rows * 8, 256) : 0;
-  p.bwd_bytes = round_up(std::max<int64_t>(bh * rows, 1) * 4, 256);
+  p.part_dq = round_up(std::max<int64_t>(bh * rows, 1) * 8, 256);
+  p.bwd_bytes = p.part_dq + (p.q_splits > 1 ? round_up(bh * p.q_splits * rows * d->head_dim * 4, 256) : 0);
   return p;
 }
 
@@ -734,9 +1170,12 @@ void fill_args(const recis_attn_desc* d, const AttnPlan& p, AttnArgs* a) {
   a->head_dim = d->head_dim;
   a->rows = d->q_len * a->group;
   a->row_tiles = p.row_tiles;
+  a->dies = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDies : 1;
   a->key_tiles = p.key_tiles;
   a->splits = p.splits;
   a->split_keys = p.split_keys;
+  a->q_splits = p.q_splits;
+  a->q_split_keys = p.q_split_keys;
   a->scale = d->scale;
   a->error = d->error;
 }
@@ -751,6 +1190,9 @@ bool rows_aligned(const recis_attn_desc* d, std::initializer_list<const void*> p
   for (const int64_t* s : strides)
     for (int i = 0; i < 3; ++i)
       if (s[i] % per) return false;
+  // 64 rows stay within 32 bits of byte offset
+  for (const int64_t* s : {d->k_strides, d->v_strides})
+    if (s[1] < 0 || s[1] >= (1 << 23)) return false;
   return true;
 }
 
@@ -761,17 +1203,19 @@ bool elements_aligned(const recis_attn_desc* d, std::initializer_list<const void
 }
 
 dim3 attn_grid(const AttnArgs& a, int per) {
-  return dim3((unsigned)(round_up((int64_t)a.batch * a.kv_heads, kDies) * per));
+  return dim3((unsigned)(round_up((int64_t)a.batch * a.kv_heads, a.dies) * per));
 }
 
-enum AttnPass { kFwd, kBwdQ, kBwdKv };
+enum AttnPass { kFwd, kFew, kBwdQ, kBwdKv };
 
 template <typename T, int DP, int N, bool ALN>
 void launch_pass(AttnPass pass, const AttnArgs& a, hipStream_t s) {
   if (pass == kFwd)
     hipLaunchKernelGGL((k_attn_fwd<T, DP, N, ALN>), attn_grid(a, a.row_tiles * a.splits), dim3(kThreads), 0, s, a);
-  else if (pass == kBwdQ)
-    hipLaunchKernelGGL((k_attn_bwd_q<T, DP, N, ALN>), attn_grid(a, a.row_tiles), dim3(kThreads), 0, s, a);
+  else if (pass == kFew) {
+    if constexpr (N == 1) hipLaunchKernelGGL((k_attn_few<T, DP, ALN>), attn_grid(a, a.splits), dim3(kThreads), 0, s, a);
+  } else if (pass == kBwdQ)
+    hipLaunchKernelGGL((k_attn_bwd_q<T, DP, N, ALN>), attn_grid(a, a.row_tiles * a.q_splits), dim3(kThreads), 0, s, a);
   else
     hipLaunchKernelGGL((k_attn_bwd_kv<T, DP, N, ALN>), attn_grid(a, a.key_tiles), dim3(kThreads), 0, s, a);
 }
@@ -793,6 +1237,19 @@ void launch_attn(AttnPass pass, int dtype, const AttnPlan& p, bool aln, const At
     p.dp == 32 ? launch_dp<float, 32>(pass, p, aln, a, s)
                : p.dp == 64 ? launch_dp<float, 64>(pass, p, aln, a, s) : launch_dp<float, 128>(pass, p, aln, a, s);
   }
+}
+
+// Four waves a row where the rows alone do not fill the chip (1024 rows of 8
+// ranges: 6.1 us against 9.8; 4158 rows of 12: 11.9 against 8.4) or the ranges
+// are many.
+template <typename T>
+void launch_join(const AttnArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
+  if (a.splits <= 16 && rows > 2048)
+    hipLaunchKernelGGL((k_attn_join<T, 1>), dim3((unsigned)((rows + kAttnWaves - 1) / kAttnWaves)), dim3(kThreads), 0,
+                       s, a);
+  else
+    hipLaunchKernelGGL((k_attn_join<T, kAttnWaves>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
 }
 
 bool grid_fits(const recis_attn_desc* d, int64_t per) {
@@ -831,18 +1288,16 @@ recis_status recis_cross_attn_fwd(const recis_attn_desc* desc, const void* q, co
   a.v = v;
   a.out = out;
   a.lse = lse;
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_o);
+  a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_ml);
   const bool aln = rows_aligned(desc, {q, k, v, out},
                                 {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides});
-  launch_attn(kFwd, desc->dtype, p, aln, a, s);
+  launch_attn(p.few ? kFew : kFwd, desc->dtype, p, aln, a, s);
   if (p.splits > 1) {
-    const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
-    const dim3 grid((unsigned)((rows + kAttnWaves - 1) / kAttnWaves));
     if (desc->dtype == RECIS_DTYPE_BF16)
-      hipLaunchKernelGGL((k_attn_join<__bf16>), grid, dim3(kThreads), 0, s, a);
+      launch_join<__bf16>(a, s);
     else
-      hipLaunchKernelGGL((k_attn_join<float>), grid, dim3(kThreads), 0, s, a);
+      launch_join<float>(a, s);
   }
   return launch_status();
 }
@@ -860,7 +1315,7 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
     return RECIS_ERR_INVALID_ARG;
   const AttnPlan p = attn_plan(desc);
   if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.bwd_bytes) return RECIS_ERR_INVALID_ARG;
-  if (!grid_fits(desc, std::max(p.row_tiles, p.key_tiles))) return RECIS_ERR_UNSUPPORTED;
+  if (!grid_fits(desc, std::max<int64_t>((int64_t)p.row_tiles * p.q_splits, p.key_tiles))) return RECIS_ERR_UNSUPPORTED;
   AttnArgs a;
   fill_args(desc, p, &a);
   a.q = q;
@@ -869,7 +1324,8 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
   a.o = out;
   a.dout = grad_out;
   a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(workspace);
+  a.stats = static_cast<f32x2*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_dq);
   a.dq = grad_q;
   a.dk = grad_k;
   a.dv = grad_v;
@@ -877,6 +1333,13 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
                                 {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides,
                                  desc->do_strides, desc->dq_strides, desc->dk_strides, desc->dv_strides});
   if (rows) launch_attn(kBwdQ, desc->dtype, p, aln, a, s);
+  if (rows && p.q_splits > 1) {
+    const dim3 grid((unsigned)(((int64_t)a.batch * a.kv_heads * a.rows + kAttnWaves - 1) / kAttnWaves));
+    if (desc->dtype == RECIS_DTYPE_BF16)
+      hipLaunchKernelGGL((k_attn_join_q<__bf16>), grid, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_attn_join_q<float>), grid, dim3(kThreads), 0, s, a);
+  }
   if (keys) launch_attn(kBwdKv, desc->dtype, p, aln, a, s);
   return launch_status();
 }

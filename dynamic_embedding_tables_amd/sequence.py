@@ -36,12 +36,12 @@ def _dtype(name: str, t) -> int:
     return d
 
 
-def _on_gpu(**tensors):
+def _on_gpu(*tensors):
     """Every tensor given is on the current GPU."""
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != here:
-            raise ValueError(f"{name} must be on the current GPU (cuda:{here}), not {t.device}")
+            raise ValueError(f"every tensor must be on the current GPU (cuda:{here}); {list(t.shape)} is on {t.device}")
 
 
 def _index(name: str, t, dtype, shape):
@@ -65,6 +65,11 @@ def _rows(t):
     if t.dim() == 2 and (t.stride(1) == 1 or dim == 1) and t.stride(0) >= dim:
         return t, t.stride(0)
     return t.contiguous(), dim
+
+
+def _like(t):
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _written(name: str, t, shape, dtype):
@@ -102,7 +107,7 @@ def embed(tokens, weight, scale: float = 1.0, out=None, error=None, stream=None)
     if stream is not None:
         with _on(stream, tokens, weight, error):
             return embed(tokens, weight, scale, out, error)
-    _on_gpu(tokens=tokens, weight=weight, out=out, error=_error_word(error))
+    _on_gpu(tokens, weight, out, _error_word(error))
     if tokens.dtype != torch.int64 or weight.dim() != 2:
         raise ValueError("tokens must be int64 and weight [rows, dim]")
     dtype = _dtype("weight", weight)
@@ -110,7 +115,7 @@ def embed(tokens, weight, scale: float = 1.0, out=None, error=None, stream=None)
     tokens = tokens.contiguous()
     weight, w_stride = _rows(weight)
     if out is None:
-        out = torch.empty(*tokens.shape, dim, dtype=weight.dtype, device=weight.device)
+        out = weight.new_empty((*tokens.shape, dim))
         stride = dim
     else:
         stride = _written("out", out, (*tokens.shape, dim), weight.dtype)
@@ -125,7 +130,7 @@ def embed_backward(tokens, grad_out, rows: int, scale: float = 1.0, dtype=None, 
     if stream is not None:
         with _on(stream, tokens, grad_out, error):
             return embed_backward(tokens, grad_out, rows, scale, dtype, out, error)
-    _on_gpu(tokens=tokens, grad_out=grad_out, out=out, error=_error_word(error))
+    _on_gpu(tokens, grad_out, out, _error_word(error))
     dim = grad_out.shape[-1] if grad_out.dim() else 0
     if tokens.dtype != torch.int64 or tuple(grad_out.shape) != (*tokens.shape, dim):
         raise ValueError("tokens must be int64 [...] and grad_out [..., dim] over the same places")
@@ -160,7 +165,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True,
     if stream is not None:
         with _on(stream, x, weight, bias):
             return layer_norm(x, weight, bias, eps, stats, out)
-    _on_gpu(x=x, weight=weight, bias=bias, out=out)
+    _on_gpu(x, weight, bias, out)
     if x.dim() < 1:
         raise ValueError("x must be [..., dim]")
     dtype, dim = _dtype("x", x), x.shape[-1]
@@ -168,7 +173,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True,
     m = x.numel() // dim if dim else 0
     x, x_stride = _rows(x)
     if out is None:
-        y, y_stride = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
+        y, y_stride = _like(x), dim
     else:
         y, y_stride = out, _written("out", out, x.shape, x.dtype)
     mean = rstd = None
@@ -185,7 +190,7 @@ def layer_norm_backward(grad_y, x, mean, rstd, weight=None, need_weight: bool = 
     if stream is not None:
         with _on(stream, grad_y, x, mean, rstd, weight):
             return layer_norm_backward(grad_y, x, mean, rstd, weight, need_weight, weight_dtype)
-    _on_gpu(grad_y=grad_y, x=x, mean=mean, rstd=rstd, weight=weight)
+    _on_gpu(grad_y, x, mean, rstd, weight)
     if x.dim() < 1 or grad_y.shape != x.shape or grad_y.dtype != x.dtype:
         raise ValueError("grad_y and x must have one shape [..., dim] and type")
     dtype, dim = _dtype("x", x), x.shape[-1]
@@ -199,7 +204,7 @@ def layer_norm_backward(grad_y, x, mean, rstd, weight=None, need_weight: bool = 
         raise ValueError("weight_dtype must be float32 or bfloat16, and weight's own type where there is one")
     x, x_stride = _rows(x)
     grad_y, g_stride = _rows(grad_y)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dx = _like(x)
     dw = db = workspace = None
     nbytes = 0
     if need_weight:
@@ -278,10 +283,10 @@ def cross_attention(q, k, v, kv_lens=None, kv_offsets=None, kv_mask=None, max_kv
     if stream is not None:
         with _on(stream, q, k, v, kv_lens, kv_offsets, kv_mask, error):
             return cross_attention(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, return_lse, error)
-    _on_gpu(q=q, k=k, v=v, kv_lens=kv_lens, kv_offsets=kv_offsets, kv_mask=kv_mask, error=error)
+    _on_gpu(q, k, v, kv_lens, kv_offsets, kv_mask, error)
     q, k, v = _heads(q), _heads(k), _heads(v)
     d, keep = _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    out = _like(q)
     d.o_strides[:] = _strides(out)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
     nbytes = recis.recis_cross_attn_workspace_bytes(d, False)
@@ -299,15 +304,14 @@ def cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens=None, kv_offse
         with _on(stream, grad_out, q, k, v, out, lse, kv_lens, kv_offsets, kv_mask, error):
             return cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens, kv_offsets, kv_mask, max_kv_len,
                                             scale, error)
-    _on_gpu(grad_out=grad_out, q=q, k=k, v=v, out=out, lse=lse, kv_lens=kv_lens, kv_offsets=kv_offsets,
-            kv_mask=kv_mask, error=error)
+    _on_gpu(grad_out, q, k, v, out, lse, kv_lens, kv_offsets, kv_mask, error)
     if not grad_out.shape == out.shape == q.shape or not grad_out.dtype == out.dtype == q.dtype:
         raise ValueError("grad_out and out must have q's shape and type")
     if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous():
         raise ValueError("lse must be cross_attention's, contiguous float32 [batch, q_len, q_heads]")
     q, k, v, out, grad_out = _heads(q), _heads(k), _heads(v), _heads(out), _heads(grad_out)
     d, keep = _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dq = _like(q)
     new = torch.empty if q.shape[0] else torch.zeros  # without a batch entry nothing is written
     dk, dv = (new(k.shape, dtype=q.dtype, device=q.device) for _ in range(2))
     d.o_strides[:], d.do_strides[:], d.dq_strides[:] = _strides(out), _strides(grad_out), _strides(dq)
