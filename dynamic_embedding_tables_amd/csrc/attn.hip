@@ -73,12 +73,27 @@ using Frag = typename FragOf<T>::type;
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-// Eight products of k = 4: the j-th takes element j of every lane, so the
-// operands' layout is the bfloat16 one.
+// Eight products of k = 4: the j-th takes element j of every lane.
+template <int N = 8>
 __device__ __forceinline__ f32x4 mma(f32x8 a, f32x8 b, f32x4 c) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+  for (int j = 0; j < N; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
   return c;
+}
+
+// Head sizes are padded to DP: 32, 48 (float32), 64, 96 or 128.  A product
+// over the head runs in KK chunks of 32; float32's operand of a chunk holds 4
+// elements from 4 * (lane / 16) and 4 from 16 further on, so that a last chunk
+// of 16 costs half of the products.
+template <int DP>
+constexpr int kChunks32 = (DP + 31) / 32;
+template <int DP>
+__device__ __forceinline__ f32x4 mma_head(bf16x8 a, bf16x8 b, f32x4 c, int) {
+  return mma(a, b, c);
+}
+template <int DP>
+__device__ __forceinline__ f32x4 mma_head(f32x8 a, f32x8 b, f32x4 c, int chunk) {
+  return DP % 32 && chunk == kChunks32<DP> - 1 ? mma<4>(a, b, c) : mma<8>(a, b, c);
 }
 
 // Four zeros that stay in registers: a product that starts from them needs no
@@ -135,6 +150,31 @@ __device__ __forceinline__ Frag<T> load8(const T* row, int d0, int dim, bool in)
   return f;
 }
 
+// A lane's operand for chunk c of a row of `dim`.
+template <typename T, bool ALN>
+__device__ __forceinline__ Frag<T> load_head(const T* row, int c, int lane, int dim, bool in) {
+  if constexpr (sizeof(T) == 2) {
+    return load8<T, ALN>(row, c * 32 + (lane >> 4) * 8, dim, in);
+  } else {
+    Frag<T> f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int d0 = c * 32 + h * 16 + (lane >> 4) * 4;
+      f32x4 x{0.f, 0.f, 0.f, 0.f};
+      if constexpr (ALN) {
+        if (in && d0 < dim) x = *reinterpret_cast<const f32x4*>(row + d0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in && d0 + i < dim) x[i] = row[d0 + i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[h * 4 + i] = x[i];
+    }
+    return f;
+  }
+}
+
 template <typename T, bool ALN>
 __device__ __forceinline__ void store4(T* row, int d0, int dim, f32x4 x) {
   if constexpr (ALN) {
@@ -155,8 +195,10 @@ __device__ __forceinline__ void store4(T* row, int d0, int dim, f32x4 x) {
 // by a number that differs over any 8 rows, and in its upper bits over any
 // aligned 4; padding the rows instead left the column reads two to a bank
 // (half of the backward's LDS time).  Float32 rows are padded by 16 bytes.
+template <int DP>
+constexpr int kCols = DP == 48 ? 64 : DP == 96 ? 128 : DP;  // columns that threads stage
 template <typename T, int DP>
-constexpr int kLd = DP + (sizeof(T) == 2 ? 0 : 4);
+constexpr int kLd = sizeof(T) == 2 ? kCols<DP> : DP + 4;
 
 template <int DP>
 __device__ __forceinline__ int exchange(int row) {
@@ -172,10 +214,19 @@ __device__ __forceinline__ int chunk_at(int row, int chunk) {
   return row * kLd<T, DP> + (sizeof(T) == 2 ? chunk ^ exchange<DP>(row) : chunk) * 8;
 }
 
-template <typename T, int DP>
-__device__ __forceinline__ Frag<T> read_rows(const T* tile, int row0, int c0, int lane) {
-  return *reinterpret_cast<const Frag<T>*>(tile + row0 * kLd<T, DP> +
-                                           chunk_at<T, DP>(lane & 15, c0 / 8 + (lane >> 4)));
+// A lane's operand for chunk c of rows row0 .. row0 + 15.
+template <int DP>
+__device__ __forceinline__ bf16x8 read_rows(const __bf16* tile, int row0, int c, int lane) {
+  return *reinterpret_cast<const bf16x8*>(tile + row0 * kLd<__bf16, DP> +
+                                          chunk_at<__bf16, DP>(lane & 15, c * 4 + (lane >> 4)));
+}
+template <int DP>
+__device__ __forceinline__ f32x8 read_rows(const float* tile, int row0, int c, int lane) {
+  const float* p = tile + (row0 + (lane & 15)) * kLd<float, DP> + c * 32 + (lane >> 4) * 4;
+  const f32x4 lo = *reinterpret_cast<const f32x4*>(p);
+  f32x4 hi{0.f, 0.f, 0.f, 0.f};
+  if (c * 32 + 16 < DP) hi = *reinterpret_cast<const f32x4*>(p + 16);
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // Column c0 + lane % 16 of 32 rows, in the slot order of pack().
@@ -275,43 +326,53 @@ __device__ __forceinline__ Frag<T> load_at(const T* base, unsigned bytes) {
 // A tile of R rows x DP held in registers on its way to LDS.
 template <typename T, int DP, int R, bool ALN>
 struct Stage {
-  static constexpr int kChunks = R * (DP / 8);
-  static constexpr int kPer = (kChunks + kThreads - 1) / kThreads;
-  static constexpr int kStep = kThreads / (DP / 8);  // rows between a thread's chunks
+  static constexpr int kAcross = kCols<DP> / 8;     // chunks of 8 columns
+  static constexpr int kStep = kThreads / kAcross;  // rows between a thread's chunks
+  static constexpr int kPer = (R + kStep - 1) / kStep;
   Frag<T> f[kPer];
   const T* base;
   int row, d0;
   unsigned at;
   __device__ __forceinline__ void start(const T* from, long long stride, int first) {
-    row = threadIdx.x / (DP / 8);
-    d0 = (threadIdx.x % (DP / 8)) * 8;
+    row = threadIdx.x / kAcross;
+    d0 = (threadIdx.x % kAcross) * 8;
     at = (unsigned)((row * stride + d0) * (long long)sizeof(T));  // ALN: fits (rows_aligned)
     base = from + (long long)first * stride;
   }
   // rows whose bit is clear are zero, whatever memory holds there
   __device__ __forceinline__ void load(long long stride, unsigned long long bits, int dim) {
-    const bool all = ALN && dim == DP && bits == ~0ull && kChunks % kThreads == 0;
+    if (ALN && R == kPer * kStep && bits == ~0ull) {
+      if (dim == kCols<DP>) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const T* from = base + (long long)(i * kStep) * stride;
-      const int r = row + i * kStep;
-      const bool in = r < R && ((bits >> (r & 63)) & 1);
-      if (all) {
-        f[i] = load_at<T>(from, at);
-      } else if constexpr (ALN) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[i][k] = (T)0.f;
-        if (in && d0 < dim) f[i] = load_at<T>(from, at);
+        for (int i = 0; i < kPer; ++i) f[i] = load_at<T>(base + (long long)(i * kStep) * stride, at);
       } else {
-        f[i] = load8<T, ALN>(from + (long long)row * stride, d0, dim, in);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f[i] = Frag<T>{};
+        if (d0 < dim) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) f[i] = load_at<T>(base + (long long)(i * kStep) * stride, at);
+        }
+      }
+    } else {
+      const unsigned long long mine = bits >> row;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const bool in = row + i * kStep < R && ((mine >> (i * kStep)) & 1);
+        if constexpr (ALN) {
+          f[i] = Frag<T>{};
+          if (in && d0 < dim) f[i] = load_at<T>(base + (long long)(i * kStep) * stride, at);
+        } else {
+          f[i] = load8<T, ALN>(base + (long long)(row + i * kStep) * stride, d0, dim, in);
+        }
       }
     }
     base += (long long)R * stride;
   }
   __device__ __forceinline__ void store(T* tile) const {
+    if (d0 >= DP) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (kChunks % kThreads == 0 || row + i * kStep < R)
+      if (R == kPer * kStep || row + i * kStep < R)
         *reinterpret_cast<Frag<T>*>(tile + chunk_at<T, DP>(row + i * kStep, d0 / 8)) = f[i];
   }
 };
@@ -329,7 +390,7 @@ constexpr int kAttnWaves = kThreads / 64;
 constexpr float kSlack = 8.f;
 template <typename T, int DP, int QT, bool ALN>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void k_attn_fwd(AttnArgs a) {
-  constexpr int KK = DP / 32, DT = DP / 16, NT = kBlockKeys / 16;
+  constexpr int KK = kChunks32<DP>, DT = DP / 16, NT = kBlockKeys / 16;
   constexpr int kTile = kBlockKeys * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, t;
@@ -349,7 +410,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void 
     const bool in = r < a.rows;
     const T* p = static_cast<const T*>(a.q) + (in ? row_at(a, a.qs, b, h, r) : 0);
 #pragma unroll
-    for (int c = 0; c < KK; ++c) q[j][c] = load8<T, ALN>(p, c * 32 + (lane >> 4) * 8, a.head_dim, in);
+    for (int c = 0; c < KK; ++c) q[j][c] = load_head<T, ALN>(p, c, lane, a.head_dim, in);
   }
   f32x4 o[QT][DT];
   // maximum, the same in log2 of the weight (0 before the first key), how far a
@@ -396,7 +457,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void 
 #pragma unroll
       for (int n = 0; n < kAhead; ++n)
 #pragma unroll
-        for (int c = 0; c < KK; ++c) f[n][c] = read_rows<T, DP>(tk, (n0 + n) * 16, c * 32, lane);
+        for (int c = 0; c < KK; ++c) f[n][c] = read_rows<DP>(tk, (n0 + n) * 16, c, lane);
       reads_before();
       // a sum's next product is issued as late as it can be
 #pragma unroll
@@ -404,14 +465,15 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void 
 #pragma unroll
         for (int n = 0; n < kAhead; ++n)
 #pragma unroll
-          for (int j = 0; j < QT; ++j) s[n0 + n][j] = mma(f[n][c], q[j][c], c == 0 ? zero : s[n0 + n][j]);
+          for (int j = 0; j < QT; ++j) s[n0 + n][j] = mma_head<DP>(f[n][c], q[j][c], c == 0 ? zero : s[n0 + n][j], c);
     }
     if (now != ~0ull) {
+      const unsigned long long mine = now >> ((lane >> 4) * 4);  // this lane's keys: constant bits from here on
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!((now >> (n * 16 + (lane >> 4) * 4 + i)) & 1))
+          if (!((mine >> (n * 16 + i)) & 1))
 #pragma unroll
             for (int j = 0; j < QT; ++j) s[n][j][i] = -INFINITY;
     }
@@ -495,7 +557,8 @@ constexpr int kFewRows = 16, kFewKeys = 32;
 
 template <typename T, int DP, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
-  constexpr int KK = DP / 32, DT = DP / 16, kPer = DP / 16;  // chunks of values a lane
+  constexpr int KK = kChunks32<DP>, DT = DP / 16;
+  constexpr int kAcross = kCols<DP> / 8, kRows = 64 / kAcross, kPer = kFewKeys / kRows;  // chunks of values a lane
   constexpr int kTile = kFewKeys * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[kAttnWaves * kTile];
   __shared__ float refs[kAttnWaves][kFewRows], sums[kAttnWaves][kFewRows];
@@ -516,22 +579,32 @@ __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
     const bool in = r < a.rows;
     const T* p = static_cast<const T*>(a.q) + (in ? row_at(a, a.qs, b, h, r) : 0);
 #pragma unroll
-    for (int c = 0; c < KK; ++c) q[c] = load8<T, ALN>(p, c * 32 + (lane >> 4) * 8, a.head_dim, in);
+    for (int c = 0; c < KK; ++c) q[c] = load_head<T, ALN>(p, c, lane, a.head_dim, in);
   }
   Frag<T> kf[2][KK], vf[kPer];
-  // a lane's place in the operand of 16 keys, and in 64 chunks of values
-  const int kr = lane & 15, kd = (lane >> 4) * 8, vr = lane / (DP / 8), vd = (lane % (DP / 8)) * 8;
-  constexpr int kRows = 64 / (DP / 8);
+  // a lane's key in the operand of 16 keys, and its place in 64 chunks of values
+  const int kr = lane & 15, vr = lane / kAcross, vd = (lane % kAcross) * 8;
+  constexpr int kHalf = sizeof(T) == 2 ? 8 : 4;  // the operand's first elements (load_head)
+  const int kd = (lane >> 4) * kHalf;
   const unsigned k_at = (unsigned)((kr * a.ks[1] + kd) * (long long)sizeof(T));  // ALN: fits (rows_aligned)
   const unsigned v_at = (unsigned)((vr * a.vs[1] + vd) * (long long)sizeof(T));
   auto fetch = [&](int first, unsigned bits) {
     const T* kp = kb + (long long)first * a.ks[1];
     const T* vp = vb + (long long)first * a.vs[1];
-    if (ALN && a.head_dim == DP && bits == ~0u) {
+    if (ALN && bits == ~0u && a.head_dim == kCols<DP>) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < KK; ++c) kf[u][c] = load_at<T>(kp + u * 16 * a.ks[1] + c * 32, k_at);
+        for (int c = 0; c < KK; ++c) {
+          const T* from = kp + u * 16 * a.ks[1] + c * 32;
+          if constexpr (sizeof(T) == 2) {
+            kf[u][c] = load_at<T>(from, k_at);
+          } else {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(from) + k_at);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(reinterpret_cast<const char*>(from + 16) + k_at);
+            kf[u][c] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+        }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) vf[i] = load_at<T>(vp + (long long)(i * kRows) * a.vs[1], v_at);
       return;
@@ -540,11 +613,19 @@ __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int c = 0; c < KK; ++c)
-        kf[u][c] = load8<T, ALN>(kp + (long long)(u * 16 + kr) * a.ks[1], c * 32 + kd, a.head_dim,
-                                 (bits >> (u * 16 + kr)) & 1);
+        kf[u][c] = load_head<T, ALN>(kp + (long long)(u * 16 + kr) * a.ks[1], c, lane, a.head_dim,
+                                     (bits >> (u * 16 + kr)) & 1);
+    const unsigned mine = bits >> vr;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      vf[i] = load8<T, ALN>(vp + (long long)(i * kRows + vr) * a.vs[1], vd, a.head_dim, (bits >> (i * kRows + vr)) & 1);
+    for (int i = 0; i < kPer; ++i) {
+      const bool in = (mine >> (i * kRows)) & 1;
+      if constexpr (ALN) {
+        vf[i] = Frag<T>{};
+        if (in && vd < a.head_dim) vf[i] = load_at<T>(vp + (long long)(i * kRows) * a.vs[1], v_at);
+      } else {
+        vf[i] = load8<T, ALN>(vp + (long long)(i * kRows + vr) * a.vs[1], vd, a.head_dim, in);
+      }
+    }
   };
   f32x4 o[DT];
 #pragma unroll
@@ -565,12 +646,12 @@ __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
     for (int u = 0; u < 2; ++u) {
       s[u] = zero;
 #pragma unroll
-      for (int c = 0; c < KK; ++c) s[u] = mma(kf[u][c], q[c], s[u]);
+      for (int c = 0; c < KK; ++c) s[u] = mma_head<DP>(kf[u][c], q[c], s[u], c);
     }
+    if (vd < DP) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = i * 64 + lane;
-      *reinterpret_cast<Frag<T>*>(tv + chunk_at<T, DP>(c / (DP / 8), c % (DP / 8))) = vf[i];
+      for (int i = 0; i < kPer; ++i)
+        *reinterpret_cast<Frag<T>*>(tv + chunk_at<T, DP>(i * kRows + vr, vd / 8)) = vf[i];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are executed in order
     if (first + kStep < key1) {
@@ -578,11 +659,12 @@ __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
       fetch(first + kStep, bits);
     }
     if (now != ~0u) {
+      const unsigned mine = now >> ((lane >> 4) * 4);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!((now >> (u * 16 + (lane >> 4) * 4 + i)) & 1)) s[u][i] = -INFINITY;
+          if (!((mine >> (u * 16 + i)) & 1)) s[u][i] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
@@ -716,7 +798,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
 // sums with: the forward's walk over the keys, with P from the saved L.
 template <typename T, int DP, int QT, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
-  constexpr int KK = DP / 32, DT = DP / 16;
+  constexpr int KK = kChunks32<DP>, DT = DP / 16;
   constexpr int kTile = kBlockKeys * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, tile;
@@ -744,10 +826,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < KK; ++c) {
-      const int d0 = c * 32 + (lane >> 4) * 8;
-      q[j][c] = load8<T, ALN>(pq, d0, a.head_dim, in);
-      g[j][c] = load8<T, ALN>(pg, d0, a.head_dim, in);
-      const Frag<T> o = load8<T, ALN>(po, d0, a.head_dim, in);
+      q[j][c] = load_head<T, ALN>(pq, c, lane, a.head_dim, in);
+      g[j][c] = load_head<T, ALN>(pg, c, lane, a.head_dim, in);
+      const Frag<T> o = load_head<T, ALN>(po, c, lane, a.head_dim, in);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += (float)g[j][c][i] * (float)o[i];
     }
@@ -793,8 +874,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int c = 0; c < KK; ++c) {
-          fk[u][c] = read_rows<T, DP>(tk, n + u * 16, c * 32, lane);
-          fv[u][c] = read_rows<T, DP>(tv, n + u * 16, c * 32, lane);
+          fk[u][c] = read_rows<DP>(tk, n + u * 16, c, lane);
+          fv[u][c] = read_rows<DP>(tv, n + u * 16, c, lane);
         }
       if constexpr (sizeof(T) == 2) reads_before();
 #pragma unroll
@@ -803,8 +884,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < QT; ++j) {
-            s[u][j] = mma(fk[u][c], q[j][c], c == 0 ? zero : s[u][j]);
-            dp[u][j] = mma(fv[u][c], g[j][c], c == 0 ? start[j] : dp[u][j]);  // dP - delta, for nothing
+            s[u][j] = mma_head<DP>(fk[u][c], q[j][c], c == 0 ? zero : s[u][j], c);
+            dp[u][j] = mma_head<DP>(fv[u][c], g[j][c], c == 0 ? start[j] : dp[u][j], c);  // dP - delta, for nothing
           }
       Frag<T> ft[DT];  // on their way during the exponentials
       if constexpr (sizeof(T) == 2) {
@@ -821,11 +902,12 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
             s[u][j][i] = __builtin_amdgcn_exp2f(s[u][j][i] * c2 - lse2[j]) * dp[u][j][i];
       }
       if (now != ~0ull) {
+        const unsigned long long mine = now >> ((lane >> 4) * 4);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (!((now >> (n + u * 16 + (lane >> 4) * 4 + i)) & 1))
+            if (!((mine >> (n + u * 16 + i)) & 1))
 #pragma unroll
               for (int j = 0; j < QT; ++j) s[u][j][i] = 0.f;
       }
@@ -885,16 +967,14 @@ constexpr int kBlockRows = DP <= 64 ? 64 : 32;
 template <typename T, int DP, bool ALN>
 struct RowStage {
   static constexpr int R = kBlockRows<DP>;
-  static constexpr int kChunks = R * (DP / 8);
-  static constexpr int kPer = (kChunks + kThreads - 1) / kThreads;
-  static constexpr int kStep = kThreads / (DP / 8);
+  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = (R + kStep - 1) / kStep;
   Frag<T> fq[kPer], fg[kPer];
   const T *pq[kPer], *pg[kPer];  // of the row that comes next
   int head[kPer];                // its head in the group
   int row, d0;
   __device__ __forceinline__ void start(const AttnArgs& a, int b, int h) {
-    row = threadIdx.x / (DP / 8);
-    d0 = (threadIdx.x % (DP / 8)) * 8;
+    row = threadIdx.x / kAcross;
+    d0 = (threadIdx.x % kAcross) * 8;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = row + i * kStep;
@@ -905,18 +985,23 @@ struct RowStage {
   }
   // `left` rows from the next one on exist; the others are zero
   __device__ __forceinline__ void load(const AttnArgs& a, int left) {
-    const bool all = ALN && a.head_dim == DP && left >= R && kChunks % kThreads == 0;
     const int dq = R / a.group, dh = R % a.group;  // R rows on
+    if (ALN && R == kPer * kStep && left >= R && a.head_dim == kCols<DP>) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (all) {
+      for (int i = 0; i < kPer; ++i) {
         fq[i] = *reinterpret_cast<const Frag<T>*>(pq[i] + d0);
         fg[i] = *reinterpret_cast<const Frag<T>*>(pg[i] + d0);
-      } else {
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
         const bool in = row + i * kStep < std::min(left, R);
         fq[i] = load8<T, ALN>(pq[i], d0, a.head_dim, in);
         fg[i] = load8<T, ALN>(pg[i], d0, a.head_dim, in);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
       pq[i] += dq * a.qs[1] + dh * a.qs[2];
       pg[i] += dq * a.dos[1] + dh * a.dos[2];
       if (dh) {
@@ -930,9 +1015,10 @@ struct RowStage {
     }
   }
   __device__ __forceinline__ void store(T* tq, T* tg) const {
+    if (d0 >= DP) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (kChunks % kThreads == 0 || row + i * kStep < R) {
+      if (R == kPer * kStep || row + i * kStep < R) {
         const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
         *reinterpret_cast<Frag<T>*>(tq + at) = fq[i];
         *reinterpret_cast<Frag<T>*>(tg + at) = fg[i];
@@ -942,7 +1028,7 @@ struct RowStage {
 
 template <typename T, int DP, int KT, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
-  constexpr int KK = DP / 32, DT = DP / 16;
+  constexpr int KK = kChunks32<DP>, DT = DP / 16;
   constexpr int R = kBlockRows<DP>, kTile = R * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   __shared__ __attribute__((aligned(16))) float stats[2][2 * R];
@@ -981,9 +1067,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
       in[j] = a.kv_mask[(a.kv_offsets ? sp.row0 : (long long)b * a.mask_stride) + key] != 0;
 #pragma unroll
     for (int c = 0; c < KK; ++c) {
-      const int d0 = c * 32 + (lane >> 4) * 8;
-      k[j][c] = load8<T, ALN>(kb + (long long)key * a.ks[1], d0, a.head_dim, in[j]);
-      v[j][c] = load8<T, ALN>(vb + (long long)key * a.vs[1], d0, a.head_dim, in[j]);
+      k[j][c] = load_head<T, ALN>(kb + (long long)key * a.ks[1], c, lane, a.head_dim, in[j]);
+      v[j][c] = load_head<T, ALN>(vb + (long long)key * a.vs[1], c, lane, a.head_dim, in[j]);
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) dk[j][d] = dv[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1026,8 +1111,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
         d4[u] = *reinterpret_cast<const f32x4*>(td + n + u * 16 + (lane >> 4) * 4);
 #pragma unroll
         for (int c = 0; c < KK; ++c) {
-          fq[u][c] = read_rows<T, DP>(tq, n + u * 16, c * 32, lane);
-          fg[u][c] = read_rows<T, DP>(tg, n + u * 16, c * 32, lane);
+          fq[u][c] = read_rows<DP>(tq, n + u * 16, c, lane);
+          fg[u][c] = read_rows<DP>(tg, n + u * 16, c, lane);
         }
       }
       if constexpr (sizeof(T) == 2) reads_before();
@@ -1040,8 +1125,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
 #pragma unroll
           for (int j = 0; j < KT; ++j) {
             const f32x4 from = sizeof(T) == 2 ? l4[u] : f32x4{0.f, 0.f, 0.f, 0.f};
-            s[u][j] = mma(fq[u][c], k[j][c], c == 0 ? from : s[u][j]);
-            dp[u][j] = mma(fg[u][c], v[j][c], c == 0 ? d4[u] : dp[u][j]);
+            s[u][j] = mma_head<DP>(fq[u][c], k[j][c], c == 0 ? from : s[u][j], c);
+            dp[u][j] = mma_head<DP>(fg[u][c], v[j][c], c == 0 ? d4[u] : dp[u][j], c);
           }
       Frag<T> tgf[DT], tqf[DT];  // on their way during the exponentials
       if constexpr (sizeof(T) == 2) {
@@ -1120,7 +1205,8 @@ constexpr int kMaxSplits = 256;
 
 AttnPlan attn_plan(const recis_attn_desc* d) {
   AttnPlan p;
-  p.dp = d->head_dim <= 32 ? 32 : d->head_dim <= 64 ? 64 : 128;
+  const bool f32 = d->dtype == RECIS_DTYPE_F32;
+  p.dp = d->head_dim <= 32 ? 32 : f32 && d->head_dim <= 48 ? 48 : d->head_dim <= 64 ? 64 : d->head_dim <= 96 ? 96 : 128;
   const int group = d->q_heads / d->kv_heads;
   const int64_t rows = (int64_t)d->q_len * group, bh = (int64_t)d->batch * d->kv_heads;
   p.qt = rows > 64 && d->dtype == RECIS_DTYPE_BF16 && p.dp <= 64 ? 2 : 1;
@@ -1229,14 +1315,24 @@ void launch_dp(AttnPass pass, const AttnPlan& p, bool aln, const AttnArgs& a, hi
   aln ? launch_pass<T, DP, 1, true>(pass, a, s) : launch_pass<T, DP, 1, false>(pass, a, s);
 }
 
-void launch_attn(AttnPass pass, int dtype, const AttnPlan& p, bool aln, const AttnArgs& a, hipStream_t s) {
-  if (dtype == RECIS_DTYPE_BF16) {
-    p.dp == 32 ? launch_dp<__bf16, 32>(pass, p, aln, a, s)
-               : p.dp == 64 ? launch_dp<__bf16, 64>(pass, p, aln, a, s) : launch_dp<__bf16, 128>(pass, p, aln, a, s);
-  } else {
-    p.dp == 32 ? launch_dp<float, 32>(pass, p, aln, a, s)
-               : p.dp == 64 ? launch_dp<float, 64>(pass, p, aln, a, s) : launch_dp<float, 128>(pass, p, aln, a, s);
+template <typename T>
+void launch_type(AttnPass pass, const AttnPlan& p, bool aln, const AttnArgs& a, hipStream_t s) {
+  switch (p.dp) {
+    case 32: return launch_dp<T, 32>(pass, p, aln, a, s);
+    case 48:
+      if constexpr (sizeof(T) == 4) launch_dp<T, 48>(pass, p, aln, a, s);
+      return;
+    case 64: return launch_dp<T, 64>(pass, p, aln, a, s);
+    case 96: return launch_dp<T, 96>(pass, p, aln, a, s);
+    default: return launch_dp<T, 128>(pass, p, aln, a, s);
   }
+}
+
+void launch_attn(AttnPass pass, int dtype, const AttnPlan& p, bool aln, const AttnArgs& a, hipStream_t s) {
+  if (dtype == RECIS_DTYPE_BF16)
+    launch_type<__bf16>(pass, p, aln, a, s);
+  else
+    launch_type<float>(pass, p, aln, a, s);
 }
 
 // Four waves a row where the rows alone do not fill the chip (1024 rows of 8

@@ -315,7 +315,8 @@ def test_layer_norm_gradient_is_the_difference_quotient(seq):
 ATTN = [  # batch, q_len, kv_len, q_heads, kv_heads, head_dim
     (1, 1, 1, 1, 1, 1), (2, 1, 200, 4, 4, 32), (3, 3, 65, 4, 2, 40), (2, 17, 64, 2, 1, 128), (2, 70, 130, 6, 2, 64),
     (1, 129, 257, 2, 2, 20), (2, 1, 1500, 8, 2, 128), (5, 33, 31, 1, 1, 7), (1, 200, 100, 3, 3, 64), (3, 2, 700, 4, 1, 96),
-    (2, 40, 16, 4, 2, 33), (9, 5, 300, 2, 2, 16),
+    (2, 40, 16, 4, 2, 33), (9, 5, 300, 2, 2, 16), (2, 37, 150, 2, 1, 48), (2, 66, 140, 2, 2, 96), (1, 20, 90, 2, 1, 88),
+    (2, 1, 400, 4, 1, 80), (2, 3, 333, 2, 2, 48),
 ]
 KINDS = ["all", "lens", "packed", "mask", "packed mask"]
 
