@@ -45,7 +45,7 @@ struct AttnArgs {
   int batch, q_len, kv_len, q_heads, kv_heads, group, head_dim;
   int rows;                // q_len * group
   int row_tiles, key_tiles;
-  int dies;                    // pairs of (batch entry, key head) side by side in the grid
+  int dies, unit;              // `unit` pairs of (batch entry, key head) share a die, `dies` units lie side by side
   int splits, split_keys;      // forward: key ranges of a row tile, joined by k_attn_join
   int q_splits, q_split_keys;  // dQ: the same, joined by k_attn_join_q
   float scale;
@@ -291,15 +291,23 @@ __device__ __forceinline__ unsigned long long key_bits(const AttnArgs& a, const 
   return __ballot(in);
 }
 
-// Consecutive blocks go to the eight dies in turn.  With many (batch entry, key
-// head) pairs the blocks of one are given to the same die, so its keys stay in
-// one L2; with few, that would leave dies idle (9 entries of 0 to 1499 keys,
-// 2 heads: 31 us against 21), and a pair's blocks go to every die.
-constexpr int kDies = 8, kPairsForDies = 128;
+// Consecutive blocks go to the eight dies in turn; `unit` (batch entry, key
+// head) pairs, all blocks of each, share a die and its L2.
+//  - Where the keys are read once (one row tile), all heads of an entry: its
+//    positions' memory is then read by one die, in one stretch (64 entries of
+//    up to 8192 keys, 4 heads of 128: 112 us against 122), and heads shorter
+//    than a 128-byte line are not fetched once per die (512 entries, 4 heads
+//    of 32: 35 us against 47).
+//  - Where there is more to compute than to read, one pair, so that entries of
+//    unequal length spread over the dies.
+//  - With few pairs that would leave dies idle, and a pair's blocks go to every
+//    die (9 entries of 0 to 1499 keys, 2 heads: 25 us against 31).
+constexpr int kDies = 8, kEntriesForDies = 64, kPairsForDies = 128;
 __device__ __forceinline__ bool place(const AttnArgs& a, int per, int* b, int* h, int* t) {
-  const int slot = blockIdx.x / a.dies;
-  const int bh = (slot / per) * a.dies + blockIdx.x % a.dies;
-  *t = slot % per;
+  const int slot = blockIdx.x / a.dies, across = per * a.unit;
+  const int rest = slot % across;
+  const int bh = ((slot / across) * a.dies + blockIdx.x % a.dies) * a.unit + rest / per;
+  *t = rest % per;
   *b = bh / a.kv_heads;
   *h = bh % a.kv_heads;
   return bh < a.batch * a.kv_heads;
@@ -1256,6 +1264,7 @@ void fill_args(const recis_attn_desc* d, const AttnPlan& p, AttnArgs* a) {
   a->head_dim = d->head_dim;
   a->rows = d->q_len * a->group;
   a->row_tiles = p.row_tiles;
+  a->unit = p.row_tiles <= 1 && d->batch >= kEntriesForDies ? d->kv_heads : 1;
   a->dies = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDies : 1;
   a->key_tiles = p.key_tiles;
   a->splits = p.splits;
@@ -1289,7 +1298,7 @@ bool elements_aligned(const recis_attn_desc* d, std::initializer_list<const void
 }
 
 dim3 attn_grid(const AttnArgs& a, int per) {
-  return dim3((unsigned)(round_up((int64_t)a.batch * a.kv_heads, a.dies) * per));
+  return dim3((unsigned)(round_up((int64_t)a.batch * a.kv_heads, a.dies * a.unit) * per));
 }
 
 enum AttnPass { kFwd, kFew, kBwdQ, kBwdKv };
@@ -1349,7 +1358,7 @@ void launch_join(const AttnArgs& a, hipStream_t s) {
 }
 
 bool grid_fits(const recis_attn_desc* d, int64_t per) {
-  return round_up((int64_t)d->batch * d->kv_heads, kDies) * per < (1ll << 31);
+  return round_up((int64_t)d->batch * d->kv_heads, (int64_t)kDies * d->kv_heads) * per < (1ll << 31);
 }
 
 }  // namespace
