@@ -25,7 +25,7 @@ template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void k_embed_fwd(const long long* __restrict__ tokens, long long n,
                                                         const T* __restrict__ w, long long rows, long long w_stride,
                                                         int per_row, unsigned m, float scale, T* __restrict__ out,
-                                                        long long out_stride, unsigned* error) {
+                                                        long long out_stride, int stream, unsigned* error) {
   const long long first = (long long)blockIdx.x * kFwdTile;
   const long long row0 = first / per_row;
   const unsigned rem = (unsigned)(first - row0 * per_row);
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_fwd(const long long* __restr
     if (row[b] >= n) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[b][i] *= scale;
-    store_f32<T, V>(out + row[b] * out_stride + col[b], v[b]);
+    store_or_stream<T, V>(stream, out + row[b] * out_stride + col[b], v[b]);
   }
 }
 
@@ -68,7 +68,7 @@ void launch_fwd(const int64_t* tokens, int64_t n, const void* w, int64_t rows, i
   hipLaunchKernelGGL((k_embed_fwd<T, V>), dim3((unsigned)blocks), dim3(kThreads), 0, s,
                      reinterpret_cast<const long long*>(tokens), (long long)n, static_cast<const T*>(w),
                      (long long)rows, (long long)w_stride, per_row, m, scale, static_cast<T*>(out),
-                     (long long)out_stride, error);
+                     (long long)out_stride, (int)(n * dim * (int64_t)sizeof(T) > kStreamBytes), error);
 }
 
 // ------------------------------------------------------------- sorted tokens
@@ -268,7 +268,7 @@ struct SumArgs {
   void* out;
   long long out_stride;
   float scale;
-  int dim, quantum;
+  int dim, quantum, stream;
   int lane_bits;  // 2^lane_bits lanes a row; blockIdx.y counts tiles of 2^lane_bits * V columns
   // per block: the row it starts in, whether that row has earlier tokens, and
   // the parts it leaves: `head` ends the first row, `tail` belongs to the row
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] *= a.scale;
-        store_f32<TW, V>(out + (long long)row * a.out_stride + col, acc);
+        store_or_stream<TW, V>(a.stream, out + (long long)row * a.out_stride + col, acc);
       }
     }
 #pragma unroll
@@ -665,6 +665,7 @@ recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_
   a.scale = scale;
   a.dim = dim;
   a.quantum = p.quantum;
+  a.stream = rows * dim * ws > kStreamBytes;
   a.lane_bits = p.lane_bits;
   a.first_row = reinterpret_cast<int*>(w + p.first_row);
   a.began = reinterpret_cast<int*>(w + p.began);

@@ -14,21 +14,26 @@
 namespace recis {
 namespace {
 
-// Sum over the L lanes of a group (L <= 64), or over the block (L = blockDim).
-template <int L>
-__device__ __forceinline__ float group_sum(float v, float* shared) {
+// Sums of N values over the L lanes of a group, or over the block (L = its size).
+template <int L, int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float (*shared)[N]) {
 #pragma unroll
-  for (int o = 1; o < (L < 64 ? L : 64); o <<= 1) v += __shfl_xor(v, o);
+  for (int n = 0; n < N; ++n) v[n] = lane_sum<(L < 64 ? L : 64)>(v[n]);
   if constexpr (L > 64) {
     constexpr int kW = L / 64;
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.f;
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int w = 0; w < kW; ++w) v += shared[w];
+      for (int n = 0; n < N; ++n) shared[threadIdx.x >> 6][n] = v[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      v[n] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) v[n] += shared[w][n];
+    }
     __syncthreads();
   }
-  return v;
 }
 
 struct NormArgs {
@@ -45,15 +50,30 @@ struct NormArgs {
   float eps;
 };
 
-__device__ __forceinline__ float weight_at(const void* w, int bf16, int i) {
-  return bf16 ? (float)static_cast<const __bf16*>(w)[i] : static_cast<const float*>(w)[i];
-}
-
-template <typename T, int V, int K>
-__device__ __forceinline__ void load_row(const T* row, int dim, int lane, int lanes, float (&v)[K][V]) {
+// The lane's columns of the weight (or `none` without one).
+template <int V, int K, int L>
+__device__ __forceinline__ void load_weight(const void* w, int bf16, int dim, int lane, float none, float (&v)[K][V]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * lanes + lane) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[k][i] = none;
+    const int c = (k * L + lane) * V;
+    if (!w || c >= dim) continue;
+    if (bf16) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = (float)static_cast<const __bf16*>(w)[c + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = static_cast<const float*>(w)[c + i];
+    }
+  }
+}
+
+template <typename T, int V, int K, int L>
+__device__ __forceinline__ void load_row(const T* row, int dim, int lane, float (&v)[K][V]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * L + lane) * V;
     if (c < dim) {
       load_f32<T, V>(row + c, v[k]);
     } else {
@@ -63,56 +83,71 @@ __device__ __forceinline__ void load_row(const T* row, int dim, int lane, int la
   }
 }
 
-template <typename T, int V, int L, int K, int THREADS>
+// s / n to the last bit or nearly: a constant row has its constant as mean.
+__device__ __forceinline__ float over(float s, float n, float inv) {
+  const float q = s * inv;
+  return fmaf(fmaf(-q, n, s), inv, q);
+}
+
+// R rows a group at a time: their loads are all under way before the first sum.
+template <typename T, int V, int L, int K, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormArgs a) {
-  constexpr int kRows = THREADS / L;
-  __shared__ float shared[THREADS / 64];
-  const int lane = threadIdx.x % L;
+  constexpr int kGroups = THREADS / L;
+  __shared__ float shared[THREADS / 64][R];
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const float n = (float)a.dim, inv = 1.f / n;
   float w[K][V], b[K][V];
+  load_weight<V, K, L>(a.w, a.w_bf16, a.dim, lane, 1.f, w);
+  load_weight<V, K, L>(a.b, a.w_bf16, a.dim, lane, 0.f, b);
+  for (int64_t r0 = (int64_t)blockIdx.x * (kGroups * R); r0 < a.m; r0 += (int64_t)gridDim.x * (kGroups * R)) {
+    float v[R][K][V], s[R];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (k * L + lane) * V + i;
-      w[k][i] = a.w && c < a.dim ? weight_at(a.w, a.w_bf16, c) : 1.f;
-      b[k][i] = a.b && c < a.dim ? weight_at(a.b, a.w_bf16, c) : 0.f;
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = r0 + r * kGroups + group;
+      load_row<T, V, K, L>(static_cast<const T*>(a.x) + row * a.x_stride, row < a.m ? a.dim : 0, lane, v[r]);
     }
-  // divided, not multiplied by 1 / dim: a constant row has its constant as mean
-  const float dim_f = (float)a.dim;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.m; r0 += (int64_t)gridDim.x * kRows) {
-    const int64_t row = r0 + threadIdx.x / L;
-    const bool in = row < a.m;
-    float v[K][V];
-    load_row<T, V, K>(static_cast<const T*>(a.x) + row * a.x_stride, in ? a.dim : 0, lane, L, v);
-    float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int r = 0; r < R; ++r) {
+      s[r] = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) s += v[k][i];
-    const float mean = group_sum<L>(s, shared) / dim_f;
-    float q = 0.f;
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+        for (int i = 0; i < V; ++i) s[r] += v[r][k][i];
+    }
+    group_sums<L, R>(s, shared);
+    float mean[R];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float d = (k * L + lane) * V < a.dim ? v[k][i] - mean : 0.f;
-        v[k][i] = d;
-        q += d * d;
+    for (int r = 0; r < R; ++r) {
+      mean[r] = over(s[r], n, inv);
+      s[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = (k * L + lane) * V < a.dim ? v[r][k][i] - mean[r] : 0.f;
+          v[r][k][i] = d;
+          s[r] += d * d;
+        }
+    }
+    group_sums<L, R>(s, shared);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = r0 + r * kGroups + group;
+      if (row >= a.m) continue;
+      const float rstd = __builtin_amdgcn_rsqf(over(s[r], n, inv) + a.eps);
+      if (lane == 0 && a.mean) {
+        a.mean[row] = mean[r];
+        a.rstd[row] = rstd;
       }
-    const float rstd = 1.f / sqrtf(group_sum<L>(q, shared) / dim_f + a.eps);
-    if (!in) continue;
-    if (lane == 0 && a.mean) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
-    T* y = static_cast<T*>(a.y) + row * a.y_stride;
+      T* y = static_cast<T*>(a.y) + row * a.y_stride;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * L + lane) * V;
-      if (c >= a.dim) continue;
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * L + lane) * V;
+        if (c >= a.dim) continue;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * rstd * w[k][i] + b[k][i];
-      store_f32<T, V>(y + c, v[k]);
+        for (int i = 0; i < V; ++i) v[r][k][i] = v[r][k][i] * rstd * w[k][i] + b[k][i];
+        store_f32<T, V>(y + c, v[r][k]);
+      }
     }
   }
 }
@@ -120,60 +155,70 @@ __global__ __launch_bounds__(THREADS) void k_norm_fwd(NormArgs a) {
 // dx, and the block's part of dw and db: every lane adds up its columns over
 // the rows its group takes, the groups are joined in LDS in order, and
 // k_norm_bwd_weight adds the blocks' parts in order.
-template <typename T, int V, int L, int K, int THREADS>
+template <typename T, int V, int L, int K, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormArgs a) {
-  constexpr int kRows = THREADS / L;
-  __shared__ float shared[THREADS / 64];
-  __shared__ float join[kRows > 1 ? THREADS * K * V : 1];
+  constexpr int kGroups = THREADS / L;
+  __shared__ float shared[THREADS / 64][2 * R];
+  __shared__ float join[kGroups > 1 ? THREADS * K * V : 1];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const float n = (float)a.dim, inv = 1.f / n;
   float w[K][V], dw[K][V], db[K][V];
+  load_weight<V, K, L>(a.w, a.w_bf16, a.dim, lane, 1.f, w);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (k * L + lane) * V + i;
-      w[k][i] = a.w && c < a.dim ? weight_at(a.w, a.w_bf16, c) : 1.f;
-      dw[k][i] = db[k][i] = 0.f;
+    for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * (kGroups * R); r0 < a.m; r0 += (int64_t)gridDim.x * (kGroups * R)) {
+    float x[R][K][V], g[R][K][V], rstd[R], s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = r0 + r * kGroups + group;
+      const bool in = row < a.m;
+      load_row<T, V, K, L>(static_cast<const T*>(a.x) + row * a.x_stride, in ? a.dim : 0, lane, x[r]);
+      load_row<T, V, K, L>(static_cast<const T*>(a.dy) + row * a.dy_stride, in ? a.dim : 0, lane, g[r]);
+      s[r] = in ? a.mean[row] : 0.f;
+      rstd[r] = in ? a.rstd[row] : 0.f;
     }
-  const float dim_f = (float)a.dim;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.m; r0 += (int64_t)gridDim.x * kRows) {
-    const int64_t row = r0 + group;
-    const bool in = row < a.m;
-    const int dim = in ? a.dim : 0;
-    float x[K][V], g[K][V];
-    load_row<T, V, K>(static_cast<const T*>(a.x) + row * a.x_stride, dim, lane, L, x);
-    load_row<T, V, K>(static_cast<const T*>(a.dy) + row * a.dy_stride, dim, lane, L, g);
-    const float mean = in ? a.mean[row] : 0.f, rstd = in ? a.rstd[row] : 0.f;
-    float s = 0.f, q = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int r = 0; r < R; ++r) {
+      const float mean = s[r];
+      s[r] = s[R + r] = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const bool live = (k * L + lane) * V < dim;
-        const float xh = live ? (x[k][i] - mean) * rstd : 0.f;
-        dw[k][i] += g[k][i] * xh;
-        db[k][i] += g[k][i];
-        x[k][i] = xh;
-        g[k][i] *= w[k][i];
-        s += g[k][i];
-        q += g[k][i] * xh;
+      for (int k = 0; k < K; ++k) {
+        // (a row that does not exist has gradient 0 and rstd 0)
+        const bool live = (k * L + lane) * V < a.dim;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = live ? (x[r][k][i] - mean) * rstd[r] : 0.f;
+          dw[k][i] += g[r][k][i] * xh;
+          db[k][i] += g[r][k][i];
+          x[r][k][i] = xh;
+          g[r][k][i] *= w[k][i];
+          s[r] += g[r][k][i];
+          s[R + r] += g[r][k][i] * xh;
+        }
       }
-    s = group_sum<L>(s, shared) / dim_f;
-    q = group_sum<L>(q, shared) / dim_f;
-    if (!in) continue;
-    T* dx = static_cast<T*>(a.y) + row * a.y_stride;
+    }
+    group_sums<L, 2 * R>(s, shared);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * L + lane) * V;
-      if (c >= a.dim) continue;
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = r0 + r * kGroups + group;
+      if (row >= a.m) continue;
+      T* dx = static_cast<T*>(a.y) + row * a.y_stride;
+      const float m1 = s[r] * inv, m2 = s[R + r] * inv;
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[k][i] = (g[k][i] - s - x[k][i] * q) * rstd;
-      store_f32<T, V>(dx + c, g[k]);
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * L + lane) * V;
+        if (c >= a.dim) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[r][k][i] = (g[r][k][i] - m1 - x[r][k][i] * m2) * rstd[r];
+        store_f32<T, V>(dx + c, g[r][k]);
+      }
     }
   }
   if (!a.partial) return;
   float* part = a.partial + (int64_t)blockIdx.x * 2 * a.dim;
-  if constexpr (kRows == 1) {
+  if constexpr (kGroups == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -196,14 +241,15 @@ __global__ __launch_bounds__(THREADS) void k_norm_bwd(NormArgs a) {
       for (int c = threadIdx.x; c < C; c += THREADS) {
         if (c >= a.dim) break;
         float sum = 0.f;
-        for (int r = 0; r < kRows; ++r) sum += join[r * C + c];
+#pragma unroll
+        for (int r = 0; r < kGroups; ++r) sum += join[r * C + c];
         part[half * a.dim + c] = sum;
       }
     }
   }
 }
 
-constexpr int kJoinCols = 32, kJoinRows = 32;
+constexpr int kJoinCols = 16, kJoinRows = 64;
 
 // Columns 0 .. 2 dim - 1 of the blocks' parts: dw, then db.
 __global__ __launch_bounds__(kJoinCols* kJoinRows) void k_norm_bwd_weight(const float* __restrict__ partial,
@@ -214,6 +260,7 @@ __global__ __launch_bounds__(kJoinCols* kJoinRows) void k_norm_bwd_weight(const 
   const int c = blockIdx.x * kJoinCols + tc;
   float sum = 0.f;
   if (c < 2 * dim)
+#pragma unroll 8
     for (int b = tr; b < blocks; b += kJoinRows) sum += partial[(int64_t)b * 2 * dim + c];
   join[tr][tc] = sum;
   __syncthreads();
@@ -237,6 +284,13 @@ struct RowPlan {
   int v, lanes, k, threads;
 };
 
+// Rows a group holds at once, of `held` floats a lane each.  Forward: more
+// loads under way (2.05M rows of 128 bf16: 2 rows 180 us, 1 row 188, 4 rows
+// 199).  Backward: one, the registers are better spent on more waves (1 row
+// 298 us, 2 rows 314, 4 rows 449).
+constexpr int forward_rows(int held) { return held <= 4 ? 4 : held <= 8 ? 2 : 1; }
+constexpr int backward_rows(int held) { return held <= 4 ? 2 : 1; }
+
 constexpr int kMaxNormDim = 16384;
 
 bool row_plan(int dim, int v, RowPlan* p) {
@@ -256,50 +310,82 @@ bool row_plan(int dim, int v, RowPlan* p) {
   return false;
 }
 
+// The backward's blocks stay for the whole call, each with a part of dw and db
+// to write: as many as run at once (the same case: 1536 blocks, 6 a CU, 298 us;
+// with 2048 a third of the work waits for a second turn, 379 us).
+constexpr int kMaxBwdThreads = 256 * 6 * 256;
+
+template <void (*KERNEL)(NormArgs)>
+int blocks_at_once(int threads) {
+  static const int n = [&] {
+    int per_cu = 0, device = 0, cus = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, KERNEL, threads, 0) != hipSuccess || per_cu < 1) per_cu = 1;
+    if (hipGetDevice(&device) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || cus < 1)
+      cus = 256;
+    (void)hipGetLastError();
+    return std::min(per_cu * cus, kMaxBwdThreads / threads);
+  }();
+  return n;
+}
+
+// Returns the blocks of the launch.
 template <typename T, int V, int L, int K, int THREADS>
-void launch_norm(bool bwd, const NormArgs& a, int blocks, hipStream_t s) {
+int launch_norm(bool bwd, const NormArgs& a, hipStream_t s) {
   if constexpr (K * V <= 32) {
-    if (bwd)
-      hipLaunchKernelGGL((k_norm_bwd<T, V, L, K, THREADS>), dim3(blocks), dim3(THREADS), 0, s, a);
-    else
-      hipLaunchKernelGGL((k_norm_fwd<T, V, L, K, THREADS>), dim3(blocks), dim3(THREADS), 0, s, a);
+    auto blocks_of = [&](int64_t rows, int64_t most) { return (int)std::min<int64_t>(most, (a.m + rows - 1) / rows); };
+    if (bwd) {
+      constexpr int R = backward_rows(K * V);
+      const int most = blocks_at_once<k_norm_bwd<T, V, L, K, THREADS, R>>(THREADS);
+      const int blocks = blocks_of(THREADS / L * R, most);
+      hipLaunchKernelGGL((k_norm_bwd<T, V, L, K, THREADS, R>), dim3(blocks), dim3(THREADS), 0, s, a);
+      return blocks;
+    }
+    constexpr int R = forward_rows(K * V);
+    const int blocks = blocks_of(THREADS / L * R, 1 << 14);
+    hipLaunchKernelGGL((k_norm_fwd<T, V, L, K, THREADS, R>), dim3(blocks), dim3(THREADS), 0, s, a);
+    return blocks;
   }
+  return 0;
 }
 
 template <typename T, int V, int L, int THREADS>
-void launch_norm_k(bool bwd, int k, const NormArgs& a, int blocks, hipStream_t s) {
+int launch_norm_k(bool bwd, int k, const NormArgs& a, hipStream_t s) {
   switch (k) {
-    case 1: return launch_norm<T, V, L, 1, THREADS>(bwd, a, blocks, s);
-    case 2: return launch_norm<T, V, L, 2, THREADS>(bwd, a, blocks, s);
-    case 4: return launch_norm<T, V, L, 4, THREADS>(bwd, a, blocks, s);
-    case 8: return launch_norm<T, V, L, 8, THREADS>(bwd, a, blocks, s);
-    default: return launch_norm<T, V, L, 16, THREADS>(bwd, a, blocks, s);
+    case 1: return launch_norm<T, V, L, 1, THREADS>(bwd, a, s);
+    case 2: return launch_norm<T, V, L, 2, THREADS>(bwd, a, s);
+    case 4: return launch_norm<T, V, L, 4, THREADS>(bwd, a, s);
+    case 8: return launch_norm<T, V, L, 8, THREADS>(bwd, a, s);
+    default: return launch_norm<T, V, L, 16, THREADS>(bwd, a, s);
   }
 }
 
 template <typename T, int V>
-void launch_norm_v(bool bwd, const RowPlan& p, const NormArgs& a, int blocks, hipStream_t s) {
+int launch_norm_v(bool bwd, const RowPlan& p, const NormArgs& a, hipStream_t s) {
   switch (p.lanes) {
-    case 16: return launch_norm<T, V, 16, 1, 256>(bwd, a, blocks, s);
-    case 64: return launch_norm_k<T, V, 64, 256>(bwd, p.k, a, blocks, s);
-    case 256: return launch_norm_k<T, V, 256, 256>(bwd, p.k, a, blocks, s);
-    default: return launch_norm_k<T, V, 1024, 1024>(bwd, p.k, a, blocks, s);
+    case 16: return launch_norm<T, V, 16, 1, 256>(bwd, a, s);
+    case 64: return launch_norm_k<T, V, 64, 256>(bwd, p.k, a, s);
+    case 256: return launch_norm_k<T, V, 256, 256>(bwd, p.k, a, s);
+    default: return launch_norm_k<T, V, 1024, 1024>(bwd, p.k, a, s);
   }
 }
 
-void launch_norm_any(bool bwd, int dtype, const RowPlan& p, const NormArgs& a, int blocks, hipStream_t s) {
+int launch_norm_any(bool bwd, int dtype, const RowPlan& p, const NormArgs& a, hipStream_t s) {
   if (dtype == RECIS_DTYPE_BF16) {
-    p.v == 8 ? launch_norm_v<__bf16, 8>(bwd, p, a, blocks, s) : launch_norm_v<__bf16, 1>(bwd, p, a, blocks, s);
+    return p.v == 8 ? launch_norm_v<__bf16, 8>(bwd, p, a, s) : launch_norm_v<__bf16, 1>(bwd, p, a, s);
   } else {
-    p.v == 4 ? launch_norm_v<float, 4>(bwd, p, a, blocks, s) : launch_norm_v<float, 1>(bwd, p, a, blocks, s);
+    return p.v == 4 ? launch_norm_v<float, 4>(bwd, p, a, s) : launch_norm_v<float, 1>(bwd, p, a, s);
   }
 }
 
-constexpr int kBwdBlocks = 1024;
-
-int norm_blocks(int64_t m, const RowPlan& p, int most) {
-  const int64_t rows = p.threads / p.lanes;
-  return (int)std::min<int64_t>(most, (m + rows - 1) / rows);
+// Parts of dw and db that a call of either access width may write.
+int64_t most_bwd_blocks(int64_t m, int dim) {
+  int64_t most = 0;
+  for (int v : {1, 4, 8}) {
+    RowPlan p;
+    if (row_plan(dim, v, &p)) most = std::max<int64_t>(most, kMaxBwdThreads / p.threads);
+  }
+  return std::min(most, std::max<int64_t>(m, 1));
 }
 
 int whole_or_one(int dtype, int v) { return v == 16 / dtype_size(dtype) ? v : 1; }
@@ -340,13 +426,13 @@ recis_status recis_layernorm_fwd(const void* x, int32_t dtype, int64_t x_stride,
   a.dim = dim;
   a.w_bf16 = weight_dtype == RECIS_DTYPE_BF16;
   a.eps = eps;
-  launch_norm_any(false, dtype, p, a, norm_blocks(m, p, 1 << 14), s);
+  launch_norm_any(false, dtype, p, a, s);
   return launch_status();
 }
 
 int64_t recis_layernorm_bwd_workspace_bytes(int64_t m, int32_t dim) {
   if (m < 0 || dim < 1 || dim > kMaxNormDim) return -1;
-  return round_up(std::min<int64_t>(kBwdBlocks, std::max<int64_t>(m, 1)) * 2 * dim * 4, 256);
+  return round_up(most_bwd_blocks(m, dim) * 2 * dim * 4, 256);
 }
 
 recis_status recis_layernorm_bwd(const void* grad_y, int64_t grad_stride, const void* x, int64_t x_stride,
@@ -385,11 +471,10 @@ recis_status recis_layernorm_bwd(const void* grad_y, int64_t grad_stride, const 
   a.y_stride = grad_x_stride;
   a.dim = dim;
   a.w_bf16 = weight_dtype == RECIS_DTYPE_BF16;
-  const int blocks = norm_blocks(m, p, kBwdBlocks);
-  if (m > 0) launch_norm_any(true, dtype, p, a, blocks, s);
+  const int blocks = m > 0 ? launch_norm_any(true, dtype, p, a, s) : 0;
   if (sums)
     hipLaunchKernelGGL(k_norm_bwd_weight, dim3((2 * dim + kJoinCols - 1) / kJoinCols), dim3(kJoinCols * kJoinRows), 0,
-                       s, a.partial, m > 0 ? blocks : 0, dim, grad_weight, grad_bias, a.w_bf16);
+                       s, a.partial, blocks, dim, grad_weight, grad_bias, a.w_bf16);
   return launch_status();
 }
 

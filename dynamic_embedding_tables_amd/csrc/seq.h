@@ -38,6 +38,59 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
   }
 }
 
+// Results of more bytes than the L2s hold together are stored past them: no
+// reader would find them there, and the stores would push out what the kernel
+// itself reads again (embedding of 2.05M tokens, 128 bf16: 79 us against 143).
+constexpr int64_t kStreamBytes = 32ll << 20;
+
+template <typename T, int V>
+__device__ __forceinline__ void stream_f32(T* p, const float (&v)[V]) {
+  constexpr int W = V * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
+  typedef T TV __attribute__((ext_vector_type(W)));
+#pragma unroll
+  for (int j = 0; j < V; j += W) {
+    if constexpr (W == 1) {
+      __builtin_nontemporal_store((T)v[j], p + j);
+    } else {
+      TV x;
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = (T)v[j + i];
+      __builtin_nontemporal_store(x, reinterpret_cast<TV*>(p + j));
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_or_stream(bool stream, T* p, const float (&v)[V]) {
+  if (stream)
+    stream_f32<T, V>(p, v);
+  else
+    store_f32<T, V>(p, v);
+}
+
+// Sum over the L lanes of an aligned group (a power of two up to 64), in every
+// lane, by register permutations.
+template <int CTRL>
+__device__ __forceinline__ float add_permuted(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (L > 1) v = add_permuted<0xB1>(v);    // lanes 1 0 3 2
+  if constexpr (L > 2) v = add_permuted<0x4E>(v);    // lanes 2 3 0 1
+  if constexpr (L > 4) v = add_permuted<0x141>(v);   // 8 lanes reversed
+  if constexpr (L > 8) v = add_permuted<0x140>(v);   // 16 lanes reversed
+  if constexpr (L > 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if constexpr (L > 32) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  return v;
+}
+
 // Widest access, in elements of `size` bytes, that the pointers, the row
 // strides (in elements) and the row length allow: 16 bytes down to one element.
 inline int access_width(int size, int64_t dim, std::initializer_list<const void*> ptrs,
