@@ -193,14 +193,20 @@ def _check(st: int, where: str):
         raise RecisError(st, where)
 
 
+_raw_stream = _current_device = None
+
+
 def _stream(stream=None):
     """The HIP stream handle of `stream`, or of torch's current stream (asked
     for directly: building the Stream object takes 3 us, more than most calls'
     whole work on the host)."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    global _raw_stream, _current_device
+    if _raw_stream is None:
+        import torch
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    return _raw_stream(_current_device())
 
 
 def _ptr(t) -> Optional[int]:

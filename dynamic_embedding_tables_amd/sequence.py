@@ -152,11 +152,13 @@ def embed_backward(tokens, grad_out, rows: int, scale: float = 1.0, dtype=None, 
 
 # --------------------------------------------------------------- layer norm
 def _norm_weights(weight, bias, dim: int) -> int:
-    given = [t for t in (weight, bias) if t is not None]
-    for t in given:
-        if tuple(t.shape) != (dim,) or not t.is_contiguous() or t.dtype != given[0].dtype:
+    one = weight if weight is not None else bias
+    if one is None:
+        return RECIS_DTYPE_F32
+    for t in (weight, bias):
+        if t is not None and (t.shape != (dim,) or t.dtype != one.dtype or not t.is_contiguous()):
             raise ValueError(f"weight and bias must be contiguous [{dim}] of one type")
-    return _dtype("weight", given[0]) if given else RECIS_DTYPE_F32
+    return _dtype("weight", one)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True, out=None, stream=None):

@@ -38,7 +38,7 @@ def generator(*key):
 
 # ---------------------------------------------------------------- embedding
 EMBED = [  # tokens, rows, dim
-    (1, 1, 1), (1, 50, 8), (7, 3, 5), (64, 100, 16), (129, 1000, 33), (1000, 17, 64), (4097, 257, 100),
+    (1, 1, 1), (1, 50, 8), (7, 3, 5), (64, 100, 16), (129, 1000, 33), (1024, 5000, 40), (1025, 5000, 40), (700, 3, 128), (1000, 4100, 8), (1000, 17, 64), (4097, 257, 100),
     (5000, 70000, 30), (300, 9, 1030), (2048, 65535, 128), (9000, 1, 24),
 ]
 
