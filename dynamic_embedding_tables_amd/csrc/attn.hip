@@ -144,6 +144,8 @@ __device__ __forceinline__ Frag<T> load8(const T* row, int d0, int dim, bool in)
       for (int i = 0; i < 8; ++i) f[i] = (T)0.f;
     }
   } else {
+    // (one unaligned access for the 8 was measured too, and is slower: dK and dV
+    // of head size 77, 573 us against 329)
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = in && d0 + i < dim ? row[d0 + i] : (T)0.f;
   }
@@ -749,50 +751,77 @@ __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
   if (a.lse && d0 == 0) a.lse[stat_at(a, b, h, r)] = sum == 0.f ? -INFINITY : top * kLn2 + __logf(sum);
 }
 
-// Joins the key ranges of a row: WAVES waves a row, consecutive ranges each.
-template <typename T, int WAVES>
-__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
+// Joins the key ranges of many rows: V elements of a row a thread.
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void k_attn_join_many(AttnArgs a) {
+  const unsigned per = a.head_dim / V;
+  const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned row = id / per, d = (id - row * per) * V;
+  const unsigned bh = row / a.rows, r = row - bh * a.rows;
+  if (bh >= (unsigned)(a.batch * a.kv_heads)) return;
+  const int h = (int)bh % a.kv_heads, b = (int)bh / a.kv_heads;
+  const long long at = (long long)bh * a.splits * a.rows + r;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.part_ml);
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, ml[at + (long long)s * a.rows][0]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float o[V] = {}, l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const long long p = at + (long long)s * a.rows;
+    const f32x2 x = ml[p];
+    const float weight = __builtin_amdgcn_exp2f(x[0] - ref);
+    l += weight * x[1];
+    float v[V];
+    load_f32<float, V>(a.part_o + p * a.head_dim + d, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] += weight * v[i];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(a.out) + row_at(a, a.os, b, h, r) + d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = (T)(o[i] * inv);
+  if (a.lse && d == 0) a.lse[stat_at(a, b, h, r)] = l == 0.f ? -INFINITY : top * kLn2 + __logf(l);
+}
+
+// The same for few rows: a block a row, consecutive ranges for each wave.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
   constexpr int kParts = kMaxHeadDim / 64;
   __shared__ float part[kAttnWaves][kMaxHeadDim + 1];
-  const int lane = threadIdx.x & 63, wave = wave_of(), w = wave % WAVES;
-  const long long id = (long long)blockIdx.x * (kAttnWaves / WAVES) + wave / WAVES;
-  const bool in = id < (long long)a.batch * a.kv_heads * a.rows;
-  const int r = (int)(id % a.rows), bh = (int)(id / a.rows);
+  const int lane = threadIdx.x & 63, wave = wave_of();
+  const int r = (int)(blockIdx.x % a.rows), bh = (int)(blockIdx.x / a.rows);
   const int h = bh % a.kv_heads, b = bh / a.kv_heads;
   const long long at = (long long)bh * a.splits * a.rows + r;
-  float top = -INFINITY, ref = 0.f, o[kParts] = {}, l = 0.f;
-  if (in) {
-    for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.part_ml[2 * (at + (long long)s * a.rows)]);
-    top = group_max(top);
+  float top = -INFINITY, o[kParts] = {}, l = 0.f;
+  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.part_ml[2 * (at + (long long)s * a.rows)]);
+  top = group_max(top);
 #pragma unroll
-    for (int k = 1; k < 16; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-    ref = top == -INFINITY ? 0.f : top;
-    const int per = (a.splits + WAVES - 1) / WAVES;
-    const int s1 = std::min(a.splits, (w + 1) * per);
+  for (int k = 1; k < 16; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+  const float ref = top == -INFINITY ? 0.f : top;
+  const int per = (a.splits + kAttnWaves - 1) / kAttnWaves;
+  const int s1 = std::min(a.splits, (wave + 1) * per);
 #pragma unroll 4
-    for (int s = w * per; s < s1; ++s) {
-      const long long p = at + (long long)s * a.rows;
-      const float weight = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ref);
-      l += weight * a.part_ml[2 * p + 1];
+  for (int s = wave * per; s < s1; ++s) {
+    const long long p = at + (long long)s * a.rows;
+    const float weight = __builtin_amdgcn_exp2f(a.part_ml[2 * p] - ref);
+    l += weight * a.part_ml[2 * p + 1];
 #pragma unroll
-      for (int i = 0; i < kParts; ++i)
-        if (lane + 64 * i < a.head_dim) o[i] += weight * a.part_o[p * a.head_dim + lane + 64 * i];
-    }
+    for (int i = 0; i < kParts; ++i)
+      if (lane + 64 * i < a.head_dim) o[i] += weight * a.part_o[p * a.head_dim + lane + 64 * i];
   }
-  if constexpr (WAVES > 1) {
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) part[wave][lane + 64 * i] = o[i];
-    if (lane == 0) part[wave][kMaxHeadDim] = l;
-    __syncthreads();
-    if (w > 0) return;
+  for (int i = 0; i < kParts; ++i) part[wave][lane + 64 * i] = o[i];
+  if (lane == 0) part[wave][kMaxHeadDim] = l;
+  __syncthreads();
+  if (wave > 0) return;
 #pragma unroll
-    for (int k = 1; k < WAVES; ++k) {
-      l += part[wave + k][kMaxHeadDim];
+  for (int k = 1; k < kAttnWaves; ++k) {
+    l += part[k][kMaxHeadDim];
 #pragma unroll
-      for (int i = 0; i < kParts; ++i) o[i] += part[wave + k][lane + 64 * i];
-    }
+    for (int i = 0; i < kParts; ++i) o[i] += part[k][lane + 64 * i];
   }
-  if (!in) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* out = static_cast<T*>(a.out) + row_at(a, a.os, b, h, r);
 #pragma unroll
@@ -947,21 +976,26 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
   }
 }
 
-// Adds the key ranges' parts of dQ, in order: a wave a row.
-template <typename T>
+// Adds the key ranges' parts of dQ, in order: V elements of a row a thread.
+template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void k_attn_join_q(AttnArgs a) {
-  const long long id = (long long)blockIdx.x * kAttnWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (id >= (long long)a.batch * a.kv_heads * a.rows) return;
-  const int r = (int)(id % a.rows), bh = (int)(id / a.rows);
-  const float* from = a.part_o + ((long long)bh * a.q_splits * a.rows + r) * a.head_dim;
-  T* out = static_cast<T*>(a.dq) + row_at(a, a.dqs, bh / a.kv_heads, bh % a.kv_heads, r);
-  for (int d = lane; d < a.head_dim; d += 64) {
-    float sum = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < a.q_splits; ++s) sum += from[(long long)s * a.rows * a.head_dim + d];
-    out[d] = (T)(sum * a.scale);
+  const unsigned per = a.head_dim / V;
+  const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned row = id / per, d = (id - row * per) * V;
+  const unsigned bh = row / a.rows, r = row - bh * a.rows;
+  if (bh >= (unsigned)(a.batch * a.kv_heads)) return;
+  const float* from = a.part_o + ((long long)bh * a.q_splits * a.rows + r) * a.head_dim + d;
+  T* out = static_cast<T*>(a.dq) + row_at(a, a.dqs, (int)bh / a.kv_heads, (int)bh % a.kv_heads, r) + d;
+  float sum[V] = {};
+#pragma unroll 4
+  for (int s = 0; s < a.q_splits; ++s) {
+    float v[V];
+    load_f32<float, V>(from + (long long)s * a.rows * a.head_dim, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] += v[i];
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = (T)(sum[i] * a.scale);
 }
 
 // dK and dV: a wave holds KT tiles of 16 keys and walks the rows, kBlockRows
@@ -1229,8 +1263,8 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
     *keys = (int)std::max<int64_t>(least, round_up((d->kv_len + n - 1) / n, 2 * kBlockKeys));
     *splits = std::max(1, (int)(((int64_t)d->kv_len + *keys - 1) / *keys));
   };
-  split(bh * p.row_tiles, p.few ? 2048 : 1024, p.few ? 256 : 128, &p.splits, &p.split_keys);
-  split(bh * p.row_tiles, 1024, 128, &p.q_splits, &p.q_split_keys);
+  split(bh * p.row_tiles, p.few || f32 ? 2048 : 1024, p.few ? 256 : 128, &p.splits, &p.split_keys);
+  split(bh * p.row_tiles, f32 ? 2048 : 1024, 128, &p.q_splits, &p.q_split_keys);
   p.part_ml = round_up(bh * p.splits * rows * d->head_dim * 4, 256);
   p.fwd_bytes = p.splits > 1 ? p.part_ml + round_up(bh * p.splits * rows * 8, 256) : 0;
   p.part_dq = round_up(std::max<int64_t>(bh * rows, 1) * 8, 256);
@@ -1344,17 +1378,32 @@ void launch_attn(AttnPass pass, int dtype, const AttnPlan& p, bool aln, const At
     launch_type<float>(pass, p, aln, a, s);
 }
 
-// Four waves a row where the rows alone do not fill the chip (1024 rows of 8
-// ranges: 6.1 us against 9.8; 4158 rows of 12: 11.9 against 8.4) or the ranges
-// are many.
+// Blocks for every V elements of every row of the folded queries; split calls
+// have few row tiles (attn_plan), so this is far below 2^31 threads.
+dim3 join_grid(const AttnArgs& a, int v) {
+  const int64_t threads = (int64_t)a.batch * a.kv_heads * a.rows * (a.head_dim / v);
+  return dim3((unsigned)((threads + kThreads - 1) / kThreads));
+}
+
+// A block a row where the rows alone do not fill the chip (1024 rows of 8
+// ranges, head size 128: 6 us against 10).
 template <typename T>
 void launch_join(const AttnArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
-  if (a.splits <= 16 && rows > 2048)
-    hipLaunchKernelGGL((k_attn_join<T, 1>), dim3((unsigned)((rows + kAttnWaves - 1) / kAttnWaves)), dim3(kThreads), 0,
-                       s, a);
+  if (rows <= 2048)
+    hipLaunchKernelGGL((k_attn_join_few<T>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
+  else if (a.head_dim % 4 == 0)
+    hipLaunchKernelGGL((k_attn_join_many<T, 4>), join_grid(a, 4), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((k_attn_join<T, kAttnWaves>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_attn_join_many<T, 1>), join_grid(a, 1), dim3(kThreads), 0, s, a);
+}
+
+template <typename T>
+void launch_join_q(const AttnArgs& a, hipStream_t s) {
+  if (a.head_dim % 4 == 0)
+    hipLaunchKernelGGL((k_attn_join_q<T, 4>), join_grid(a, 4), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_attn_join_q<T, 1>), join_grid(a, 1), dim3(kThreads), 0, s, a);
 }
 
 bool grid_fits(const recis_attn_desc* d, int64_t per) {
@@ -1439,11 +1488,10 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
                                  desc->do_strides, desc->dq_strides, desc->dk_strides, desc->dv_strides});
   if (rows) launch_attn(kBwdQ, desc->dtype, p, aln, a, s);
   if (rows && p.q_splits > 1) {
-    const dim3 grid((unsigned)(((int64_t)a.batch * a.kv_heads * a.rows + kAttnWaves - 1) / kAttnWaves));
     if (desc->dtype == RECIS_DTYPE_BF16)
-      hipLaunchKernelGGL((k_attn_join_q<__bf16>), grid, dim3(kThreads), 0, s, a);
+      launch_join_q<__bf16>(a, s);
     else
-      hipLaunchKernelGGL((k_attn_join_q<float>), grid, dim3(kThreads), 0, s, a);
+      launch_join_q<float>(a, s);
   }
   if (keys) launch_attn(kBwdKv, desc->dtype, p, aln, a, s);
   return launch_status();

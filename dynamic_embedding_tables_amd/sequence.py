@@ -105,7 +105,7 @@ def embed(tokens, weight, scale: float = 1.0, out=None, error=None, stream=None)
     """scale * weight[tokens]: tokens int64 of any shape, weight [rows, dim];
     a negative token is padding and gives zeros.  Returns [*tokens.shape, dim]."""
     if stream is not None:
-        with _on(stream, tokens, weight, error):
+        with _on(stream, tokens, weight, out, error):
             return embed(tokens, weight, scale, out, error)
     _on_gpu(tokens, weight, out, _error_word(error))
     if tokens.dtype != torch.int64 or weight.dim() != 2:
@@ -128,7 +128,7 @@ def embed_backward(tokens, grad_out, rows: int, scale: float = 1.0, dtype=None, 
     grad_out's rows of equal tokens, the rows no token names zero.  dtype:
     float32 or bfloat16 (default: grad_out's)."""
     if stream is not None:
-        with _on(stream, tokens, grad_out, error):
+        with _on(stream, tokens, grad_out, out, error):
             return embed_backward(tokens, grad_out, rows, scale, dtype, out, error)
     _on_gpu(tokens, grad_out, out, _error_word(error))
     dim = grad_out.shape[-1] if grad_out.dim() else 0
@@ -165,7 +165,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True,
     """Layer norm over x's last axis.  Returns (y, mean, rstd), the statistics
     float32 over the other axes; with stats False only y."""
     if stream is not None:
-        with _on(stream, x, weight, bias):
+        with _on(stream, x, weight, bias, out):
             return layer_norm(x, weight, bias, eps, stats, out)
     _on_gpu(x, weight, bias, out)
     if x.dim() < 1:
