@@ -293,6 +293,17 @@ __device__ __forceinline__ unsigned long long key_bits(const AttnArgs& a, const 
   return __ballot(in);
 }
 
+// The same for a tile of KEYS keys; the bits past it are set (a whole tile is all ones).
+template <int KEYS>
+__device__ __forceinline__ unsigned long long tile_bits(const AttnArgs& a, const Span& s, int b, int first, int lane) {
+  const unsigned long long bits = key_bits(a, s, b, first, lane);
+  return KEYS == 64 ? bits : bits | (~0ull << 32);
+}
+template <int KEYS>
+__device__ __forceinline__ bool no_key(unsigned long long bits) {
+  return KEYS == 64 ? bits == 0 : (unsigned)bits == 0;
+}
+
 // Consecutive blocks go to the eight dies in turn; `unit` (batch entry, key
 // head) pairs, all blocks of each, share a die and its L2.
 //  - Where the keys are read once (one row tile), all heads of an entry: its
@@ -387,7 +398,10 @@ struct Stage {
   }
 };
 
+// Keys a tile: 64, or 32 where two buffers of 64 would leave one block a CU.
 constexpr int kBlockKeys = 64;
+template <typename T, int DP>
+constexpr int kTileKeys = sizeof(T) == 4 && DP > 64 ? 32 : 64;
 constexpr int kAttnWaves = kThreads / 64;
 
 // ------------------------------------------------------------------ forward
@@ -400,8 +414,8 @@ constexpr int kAttnWaves = kThreads / 64;
 constexpr float kSlack = 8.f;
 template <typename T, int DP, int QT, bool ALN>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void k_attn_fwd(AttnArgs a) {
-  constexpr int KK = kChunks32<DP>, DT = DP / 16, NT = kBlockKeys / 16;
-  constexpr int kTile = kBlockKeys * kLd<T, DP>;
+  constexpr int KK = kChunks32<DP>, DT = DP / 16, kKeys = kTileKeys<T, DP>, NT = kKeys / 16;
+  constexpr int kTile = kKeys * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, t;
   if (!place(a, a.row_tiles * a.splits, &b, &h, &t)) return;
@@ -435,29 +449,29 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void 
   }
   const float c2 = a.scale * kLog2e;
   const f32x4 zero = zeros();
-  Stage<T, DP, kBlockKeys, ALN> sk, sv;
+  Stage<T, DP, kKeys, ALN> sk, sv;
   unsigned long long bits = 0;
   if (key0 < key1) {
     sk.start(kb, a.ks[1], key0);
     sv.start(vb, a.vs[1], key0);
-    bits = key_bits(a, sp, b, key0, lane);
+    bits = tile_bits<kKeys>(a, sp, b, key0, lane);
     sk.load(a.ks[1], bits, a.head_dim);
     sv.load(a.vs[1], bits, a.head_dim);
   }
   int buffer = 0;
-  for (int first = key0; first < key1; first += kBlockKeys, buffer ^= 1) {
+  for (int first = key0; first < key1; first += kKeys, buffer ^= 1) {
     T* tk = tiles + buffer * 2 * kTile;
     T* tv = tk + kTile;
     sk.store(tk);
     sv.store(tv);
     __syncthreads();
     const unsigned long long now = bits;
-    if (first + kBlockKeys < key1) {
-      bits = key_bits(a, sp, b, first + kBlockKeys, lane);
+    if (first + kKeys < key1) {
+      bits = tile_bits<kKeys>(a, sp, b, first + kKeys, lane);
       sk.load(a.ks[1], bits, a.head_dim);
       sv.load(a.vs[1], bits, a.head_dim);
     }
-    if (now == 0) continue;
+    if (no_key<kKeys>(now)) continue;
     f32x4 s[NT][QT];
     // as many operands ahead as 32 registers hold
     constexpr int kAhead = std::max(1, std::min(NT, 16 * 4 / (KK * (int)sizeof(Frag<T>))));
@@ -836,7 +850,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
 template <typename T, int DP, int QT, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
   constexpr int KK = kChunks32<DP>, DT = DP / 16;
-  constexpr int kTile = kBlockKeys * kLd<T, DP>;
+  constexpr int kKeys = kTileKeys<T, DP>, kTile = kKeys * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, tile;
   if (!place(a, a.row_tiles * a.q_splits, &b, &h, &tile)) return;
@@ -873,38 +887,67 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
     start[j] = f32x4{-sum, -sum, -sum, -sum};
     const float lse = in ? a.lse[stat_at(a, b, h, r)] : 0.f;
     lse2[j] = in && lse != -INFINITY ? lse * kLog2e : INFINITY;  // exp2(s - inf) = 0
-    if (in && lane < 16 && split == 0)
-      a.stats[((long long)b * a.kv_heads + h) * a.rows + r] = f32x2{sizeof(T) == 2 ? -lse2[j] / c2 : lse2[j], -sum};
 #pragma unroll
     for (int d = 0; d < DT; ++d) dq[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  Stage<T, DP, kBlockKeys, ALN> sk, sv;
+  // delta from out carries out's rounding.  Over many keys that is far below
+  // dS's own; an entry of one tile (with bfloat16) gets delta from P and dP
+  // instead: with two keys left, dS would be mostly rounding.
+  const bool short_entry = sizeof(T) == 2 && sp.len <= kKeys;
+  Stage<T, DP, kKeys, ALN> sk, sv;
   unsigned long long bits = 0;
   const int key0 = split * a.q_split_keys;
   const int key1 = std::min(sp.len, key0 + a.q_split_keys);
   if (key0 < key1) {
     sk.start(kb, a.ks[1], key0);
     sv.start(vb, a.vs[1], key0);
-    bits = key_bits(a, sp, b, key0, lane);
+    bits = tile_bits<kKeys>(a, sp, b, key0, lane);
     sk.load(a.ks[1], bits, a.head_dim);
     sv.load(a.vs[1], bits, a.head_dim);
   }
   int buffer = 0;
-  for (int first = key0; first < key1; first += kBlockKeys, buffer ^= 1) {
+  for (int first = key0; first < key1; first += kKeys, buffer ^= 1) {
     T* tk = tiles + buffer * 2 * kTile;
     T* tv = tk + kTile;
     sk.store(tk);
     sv.store(tv);
     __syncthreads();
     const unsigned long long now = bits;
-    if (first + kBlockKeys < key1) {
-      bits = key_bits(a, sp, b, first + kBlockKeys, lane);
+    if (first + kKeys < key1) {
+      bits = tile_bits<kKeys>(a, sp, b, first + kKeys, lane);
       sk.load(a.ks[1], bits, a.head_dim);
       sv.load(a.vs[1], bits, a.head_dim);
     }
-    if (now == 0) continue;
+    if (no_key<kKeys>(now)) continue;
+    if (short_entry) {
+      float sum[QT] = {};
 #pragma unroll
-    for (int n = 0; n < kBlockKeys; n += 32) {
+      for (int n = 0; n < kKeys; n += 16) {
+        f32x4 s[QT], dp[QT];
+#pragma unroll
+        for (int c = 0; c < KK; ++c) {
+          const Frag<T> fk = read_rows<DP>(tk, n, c, lane), fv = read_rows<DP>(tv, n, c, lane);
+#pragma unroll
+          for (int j = 0; j < QT; ++j) {
+            s[j] = mma_head<DP>(fk, q[j][c], c == 0 ? zero : s[j], c);
+            dp[j] = mma_head<DP>(fv, g[j][c], c == 0 ? zero : dp[j], c);
+          }
+        }
+        const unsigned mine = (unsigned)(now >> (n + (lane >> 4) * 4));
+#pragma unroll
+        for (int j = 0; j < QT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((mine >> i) & 1) sum[j] += __builtin_amdgcn_exp2f(s[j][i] * c2 - lse2[j]) * dp[j][i];
+      }
+#pragma unroll
+      for (int j = 0; j < QT; ++j) {
+        const float x = -group_add(sum[j]);
+        start[j] = f32x4{x, x, x, x};
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kKeys; n += 32) {
       f32x4 s[2][QT], dp[2][QT];
       Frag<T> fk[2][KK], fv[2][KK];
 #pragma unroll
@@ -963,6 +1006,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
   for (int j = 0; j < QT; ++j) {
     const int r = row0 + j * 16;
     if (r >= a.rows) continue;
+    if (lane < 16 && split == 0)
+      a.stats[((long long)b * a.kv_heads + h) * a.rows + r] =
+          f32x2{sizeof(T) == 2 ? -lse2[j] / c2 : lse2[j], start[j][0]};
     if (a.q_splits > 1) {
       const long long at = (((long long)b * a.kv_heads + h) * a.q_splits + split) * a.rows + r;
 #pragma unroll

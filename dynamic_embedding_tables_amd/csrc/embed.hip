@@ -465,8 +465,6 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
     for (int b = 0; b < kBatch; ++b) x[b] = ahead[b];
   }
   while (row < row_end) finish_row();
-  // join the rows that span groups: thread c carries column c through the
-  // groups in order
   const int rows_of = threadIdx.x < groups ? row_of(threadIdx.x) : 0;
   const int begun_of = threadIdx.x < groups ? has_tokens(threadIdx.x) : 0;
   const int last_row = row_of(groups);
@@ -482,26 +480,28 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) tail[g * C + lane * V + i] = acc[i];
   __syncthreads();
-  for (int c = threadIdx.x; c < C; c += kThreads) {
-    const int column = blockIdx.y * C + c;
-    if (column >= a.dim) break;
-    float run = 0.f;
-    bool open = group_began[0];  // the row in `run` has tokens before this block
-    for (int k = 0; k < groups; ++k) {
-      const int r = group_row[k];
-      if (group_row[k + 1] > r) {  // the group ends row r
-        if (open) {
-          a.head[(long long)blockIdx.x * a.dim + column] = run + head[k * C + c];
-        } else if (group_began[k]) {
-          out[(long long)r * a.out_stride + column] = (TW)((run + head[k * C + c]) * a.scale);
-        }
-        run = tail[k * C + c];
-        open = false;
-      } else {
-        run += tail[k * C + c];
-      }
+  // join the rows that span groups, one (group that ends such a row, column) a
+  // thread: the tails of the groups the row runs through, in order, and the
+  // group's head.  Past the last group the same gives the block's tail.
+  for (int item = threadIdx.x; item < C * (groups + (FEW ? 0 : 1)); item += kThreads) {
+    const int k = item / C, c = item % C, column = blockIdx.y * C + c;
+    if (column >= a.dim) continue;
+    const int r = group_row[k];
+    if (k < groups && (group_row[k + 1] == r || !group_began[k])) continue;
+    int j = k;
+    while (j > 0 && (j == k || group_row[j] == r)) --j;
+    float sum = 0.f;
+    for (int g0 = j; g0 < k; ++g0) sum += tail[g0 * C + c];
+    if (k == groups) {
+      a.tail[(long long)blockIdx.x * a.dim + column] = sum;
+      continue;
     }
-    if constexpr (!FEW) a.tail[(long long)blockIdx.x * a.dim + column] = run;
+    sum += head[k * C + c];
+    // does the row have tokens before this block?
+    if (j == 0 && group_row[0] == r && group_began[0])
+      a.head[(long long)blockIdx.x * a.dim + column] = sum;
+    else
+      out[(long long)r * a.out_stride + column] = (TW)(sum * a.scale);
   }
   if (!FEW && threadIdx.x == 0 && blockIdx.y == 0) {
     a.first_row[blockIdx.x] = group_row[0];
@@ -590,7 +590,7 @@ BwdPlan bwd_plan(int64_t n, int64_t rows, int dim, int v) {
   p.col_tiles = (dim + columns - 1) / columns;
   const int64_t units = n + rows;
   const int64_t most = std::min(128, kMaxUnits / groups);
-  p.quantum = (int)std::min<int64_t>(most, std::max<int64_t>(4, units / ((int64_t)groups * 1024)));
+  p.quantum = (int)std::min<int64_t>(most, std::max<int64_t>(8, units / ((int64_t)groups * 1024)));
   p.blocks = (units + (int64_t)groups * p.quantum - 1) / ((int64_t)groups * p.quantum);
   p.few = n <= kFewTokens;
   if (p.few) {

@@ -388,6 +388,20 @@ def test_cross_attention(seq, shape, dtype, kind):
     check_attention(seq, q, k, v, kw, kept, grad=normal(gen, *q.shape, dtype=dtype), what=(shape, kind))
 
 
+def test_cross_attention_single_keys_leave_no_score_gradient(seq):
+    """One key: the weight is 1 whatever the score, so q and k have no gradient; what remains is the rounding of the
+    weight (scores of 64 products, |s| < 8: 2^-16) times dP, not the rounding of out (2^-9)."""
+    gen = generator(18)
+    q, k, v, grad = (normal(gen, 4, n, 2, 64, dtype=BF16) for n in (7, 1, 1, 7))
+    dev = [t.cuda() for t in (q, k, v)]
+    o, lse = seq.cross_attention(*dev, return_lse=True)
+    dq, dk, dv = (t.cpu().double() for t in seq.cross_attention_backward(grad.cuda(), *dev, o, lse))
+    dp = torch.einsum("bqhd,bkhd->bqhk", grad.double(), v.double()).abs().max()
+    size = 64**-0.5 * dp * max(t.double().abs().max() for t in (q, k))
+    assert dq.abs().max() <= 2.0**-15 * size and dk.abs().max() <= 7 * 2.0**-15 * size
+    within(dv[:, 0], grad.double().sum(1), 9 * 2.0**-8 * grad.double().abs().sum(1))
+
+
 def test_cross_attention_no_keys_no_queries(seq):
     for q_len, kv_len in ((3, 0), (0, 5), (0, 0)):
         q, k = torch.randn(2, q_len, 2, 16).cuda(), torch.randn(2, kv_len, 2, 16).cuda()
