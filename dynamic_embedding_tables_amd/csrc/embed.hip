@@ -132,7 +132,9 @@ __global__ __launch_bounds__(kThreads) void k_sort_hist(SortArgs a) {
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const long long i = base + j * kThreads + threadIdx.x;
-    if (i < a.n) atomicAdd(&h[(sort_key<FIRST>(a.tokens, a.in, i, a.rows, a.error).key >> a.shift) & (a.digits - 1)], 1u);
+    if (i >= a.n) continue;
+    const unsigned key = sort_key<FIRST>(a.tokens, a.in, i, a.rows, a.error).key;
+    atomicAdd(&h[(key >> a.shift) & (a.digits - 1)], 1u);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < a.digits; d += kThreads) a.hist[(long long)blockIdx.x * a.digits + d] = h[d];

@@ -325,7 +325,8 @@ template <void (*KERNEL)(NormArgs)>
 int blocks_at_once(int threads) {
   static const int n = [&] {
     int per_cu = 0, device = 0, cus = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, KERNEL, threads, 0) != hipSuccess || per_cu < 1) per_cu = 1;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, KERNEL, threads, 0) != hipSuccess || per_cu < 1)
+      per_cu = 1;
     if (hipGetDevice(&device) != hipSuccess ||
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || cus < 1)
       cus = 256;

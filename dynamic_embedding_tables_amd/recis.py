@@ -371,12 +371,15 @@ def recis_get_error(h, stream=None) -> int:
     return int(load_library().recis_get_error(h, _stream(stream)))
 
 
-# Sequence operators: pointers and sizes as in the header.  ``sequence`` has
+# Sequence operators: pointers and sizes as in the header (tensors that a call
+# always has give their pointer directly: these calls are made for a few
+# microseconds of work).  ``sequence`` has
 # the forms that take tensors, check them and allocate what a call returns.
 def recis_embed_fwd(tokens, n: int, weight, dtype: int, rows: int, dim: int, weight_stride: int, scale: float,
                     out, out_stride: int, error=None, stream=None):
-    _check(load_library().recis_embed_fwd(_ptr(tokens), n, _ptr(weight), dtype, rows, dim, weight_stride, scale,
-                                          _ptr(out), out_stride, _ptr(error), _stream(stream)), "recis_embed_fwd")
+    _check(load_library().recis_embed_fwd(
+        tokens.data_ptr(), n, weight.data_ptr(), dtype, rows, dim, weight_stride, scale, out.data_ptr(), out_stride,
+        _ptr(error), _stream(stream)), "recis_embed_fwd")
 
 
 def recis_embed_bwd_workspace_bytes(n: int, rows: int, dim: int) -> int:
@@ -386,16 +389,17 @@ def recis_embed_bwd_workspace_bytes(n: int, rows: int, dim: int) -> int:
 def recis_embed_bwd(tokens, n: int, grad_out, grad_dtype: int, grad_stride: int, rows: int, dim: int, scale: float,
                     grad_weight, weight_dtype: int, weight_stride: int, workspace, workspace_bytes: int,
                     error=None, stream=None):
-    _check(load_library().recis_embed_bwd(_ptr(tokens), n, _ptr(grad_out), grad_dtype, grad_stride, rows, dim, scale,
-                                          _ptr(grad_weight), weight_dtype, weight_stride, _ptr(workspace),
-                                          workspace_bytes, _ptr(error), _stream(stream)), "recis_embed_bwd")
+    _check(load_library().recis_embed_bwd(
+        tokens.data_ptr(), n, grad_out.data_ptr(), grad_dtype, grad_stride, rows, dim, scale, grad_weight.data_ptr(),
+        weight_dtype, weight_stride, workspace.data_ptr(), workspace_bytes, _ptr(error), _stream(stream)),
+        "recis_embed_bwd")
 
 
 def recis_layernorm_fwd(x, dtype: int, x_stride: int, m: int, dim: int, weight, bias, weight_dtype: int, eps: float,
                         y, y_stride: int, mean=None, rstd=None, stream=None):
-    _check(load_library().recis_layernorm_fwd(_ptr(x), dtype, x_stride, m, dim, _ptr(weight), _ptr(bias),
-                                              weight_dtype, eps, _ptr(y), y_stride, _ptr(mean), _ptr(rstd),
-                                              _stream(stream)), "recis_layernorm_fwd")
+    _check(load_library().recis_layernorm_fwd(
+        x.data_ptr(), dtype, x_stride, m, dim, _ptr(weight), _ptr(bias), weight_dtype, eps, y.data_ptr(), y_stride,
+        _ptr(mean), _ptr(rstd), _stream(stream)), "recis_layernorm_fwd")
 
 
 def recis_layernorm_bwd_workspace_bytes(m: int, dim: int) -> int:
@@ -405,10 +409,10 @@ def recis_layernorm_bwd_workspace_bytes(m: int, dim: int) -> int:
 def recis_layernorm_bwd(grad_y, grad_stride: int, x, x_stride: int, dtype: int, m: int, dim: int, mean, rstd, weight,
                         weight_dtype: int, grad_x, grad_x_stride: int, grad_weight, grad_bias, workspace,
                         workspace_bytes: int, stream=None):
-    _check(load_library().recis_layernorm_bwd(_ptr(grad_y), grad_stride, _ptr(x), x_stride, dtype, m, dim, _ptr(mean),
-                                              _ptr(rstd), _ptr(weight), weight_dtype, _ptr(grad_x), grad_x_stride,
-                                              _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace), workspace_bytes,
-                                              _stream(stream)), "recis_layernorm_bwd")
+    _check(load_library().recis_layernorm_bwd(
+        grad_y.data_ptr(), grad_stride, x.data_ptr(), x_stride, dtype, m, dim, mean.data_ptr(), rstd.data_ptr(),
+        _ptr(weight), weight_dtype, grad_x.data_ptr(), grad_x_stride, _ptr(grad_weight), _ptr(grad_bias),
+        _ptr(workspace), workspace_bytes, _stream(stream)), "recis_layernorm_bwd")
 
 
 def recis_cross_attn_workspace_bytes(desc: recis_attn_desc, backward: bool) -> int:
@@ -416,16 +420,17 @@ def recis_cross_attn_workspace_bytes(desc: recis_attn_desc, backward: bool) -> i
 
 
 def recis_cross_attn_fwd(desc: recis_attn_desc, q, k, v, out, lse, workspace, workspace_bytes: int, stream=None):
-    _check(load_library().recis_cross_attn_fwd(C.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                               _ptr(workspace), workspace_bytes, _stream(stream)),
-           "recis_cross_attn_fwd")
+    _check(load_library().recis_cross_attn_fwd(
+        C.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _stream(stream)), "recis_cross_attn_fwd")
 
 
 def recis_cross_attn_bwd(desc: recis_attn_desc, grad_out, q, k, v, out, lse, grad_q, grad_k, grad_v, workspace,
                          workspace_bytes: int, stream=None):
-    _check(load_library().recis_cross_attn_bwd(C.byref(desc), _ptr(grad_out), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                               _ptr(lse), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(workspace),
-                                               workspace_bytes, _stream(stream)), "recis_cross_attn_bwd")
+    _check(load_library().recis_cross_attn_bwd(
+        C.byref(desc), grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), workspace.data_ptr(), workspace_bytes,
+        _stream(stream)), "recis_cross_attn_bwd")
 
 
 # --------------------------------------------------------- conveniences

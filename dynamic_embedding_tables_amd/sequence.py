@@ -69,7 +69,7 @@ def _rows(t):
 
 def _like(t):
     """A new contiguous tensor of t's shape and type."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _written(name: str, t, shape, dtype):
@@ -139,12 +139,12 @@ def embed_backward(tokens, grad_out, rows: int, scale: float = 1.0, dtype=None, 
     tokens = tokens.contiguous()
     grad_out, g_stride = _rows(grad_out)
     if out is None:
-        out = torch.empty(rows, dim, dtype=dtype or grad_out.dtype, device=grad_out.device)
+        out = grad_out.new_empty((rows, dim), dtype=dtype or grad_out.dtype)
         stride = dim
     else:
         stride = _written("out", out, (rows, dim), dtype or out.dtype)
     nbytes = recis.recis_embed_bwd_workspace_bytes(n, rows, dim)
-    workspace = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=grad_out.device)
+    workspace = grad_out.new_empty(max(nbytes, 0), dtype=torch.uint8)
     recis.recis_embed_bwd(tokens, n, grad_out, g_dtype, g_stride, rows, dim, scale, out, _dtype("out", out), stride,
                           workspace, nbytes, error)
     return out
@@ -180,7 +180,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True,
         y, y_stride = out, _written("out", out, x.shape, x.dtype)
     mean = rstd = None
     if stats:
-        mean, rstd = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32).unbind(0)
     recis.recis_layernorm_fwd(x, dtype, x_stride, m, dim, weight, bias, w_dtype, eps, y, y_stride, mean, rstd)
     return (y, mean, rstd) if stats else y
 
@@ -210,9 +210,9 @@ def layer_norm_backward(grad_y, x, mean, rstd, weight=None, need_weight: bool = 
     dw = db = workspace = None
     nbytes = 0
     if need_weight:
-        dw, db = torch.empty(2, dim, dtype=wt, device=x.device)
+        dw, db = x.new_empty((2, dim), dtype=wt).unbind(0)
         nbytes = recis.recis_layernorm_bwd_workspace_bytes(m, dim)
-        workspace = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(max(nbytes, 0), dtype=torch.uint8)
     recis.recis_layernorm_bwd(grad_y, g_stride, x, x_stride, dtype, m, dim, mean, rstd, weight, _DTYPES[wt], dx, dim,
                               dw, db, workspace, nbytes)
     return dx, dw, db
@@ -290,9 +290,9 @@ def cross_attention(q, k, v, kv_lens=None, kv_offsets=None, kv_mask=None, max_kv
     d, keep = _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error)
     out = _like(q)
     d.o_strides[:] = _strides(out)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty(q.shape[:3], dtype=torch.float32) if return_lse else None
     nbytes = recis.recis_cross_attn_workspace_bytes(d, False)
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
+    workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
     recis.recis_cross_attn_fwd(d, q, k, v, out, lse, workspace, nbytes)
     return (out, lse) if return_lse else out
 
@@ -314,11 +314,12 @@ def cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens=None, kv_offse
     q, k, v, out, grad_out = _heads(q), _heads(k), _heads(v), _heads(out), _heads(grad_out)
     d, keep = _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error)
     dq = _like(q)
-    new = torch.empty if q.shape[0] else torch.zeros  # without a batch entry nothing is written
-    dk, dv = (new(k.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+    dk, dv = _like(k), _like(v)
+    if not q.shape[0]:  # without a batch entry nothing is written
+        dk.zero_(), dv.zero_()
     d.o_strides[:], d.do_strides[:], d.dq_strides[:] = _strides(out), _strides(grad_out), _strides(dq)
     d.dk_strides[:], d.dv_strides[:] = _strides(dk), _strides(dv)
     nbytes = recis.recis_cross_attn_workspace_bytes(d, True)
-    workspace = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=q.device)
+    workspace = q.new_empty(max(nbytes, 0), dtype=torch.uint8)
     recis.recis_cross_attn_bwd(d, grad_out, q, k, v, out, lse, dq, dk, dv, workspace, nbytes)
     return dq, dk, dv
