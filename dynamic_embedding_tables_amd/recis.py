@@ -374,43 +374,55 @@ def recis_get_error(h, stream=None) -> int:
 # Sequence operators: pointers and sizes as in the header (tensors that a call
 # always has give their pointer directly: these calls are made for a few
 # microseconds of work).  ``sequence`` has
-# the forms that take tensors, check them and allocate what a call returns.
+# the forms that take tensors, check them and allocate what a call returns.  An
+# int that the C ABI takes in 32 bits goes through int32().
+_INT32_MAX = (1 << 31) - 1
+
+
+def int32(x: int) -> int:
+    """x, or the end of the 32-bit range nearest to it, which the calls refuse
+    as they would x (ctypes by itself passes on the low 32 bits)."""
+    if -_INT32_MAX <= x <= _INT32_MAX:
+        return x
+    return _INT32_MAX if x > 0 else -_INT32_MAX
+
+
 def recis_embed_fwd(tokens, n: int, weight, dtype: int, rows: int, dim: int, weight_stride: int, scale: float,
                     out, out_stride: int, error=None, stream=None):
     _check(load_library().recis_embed_fwd(
-        tokens.data_ptr(), n, weight.data_ptr(), dtype, rows, dim, weight_stride, scale, out.data_ptr(), out_stride,
-        _ptr(error), _stream(stream)), "recis_embed_fwd")
+        tokens.data_ptr(), n, weight.data_ptr(), dtype, rows, int32(dim), weight_stride, scale, out.data_ptr(),
+        out_stride, _ptr(error), _stream(stream)), "recis_embed_fwd")
 
 
 def recis_embed_bwd_workspace_bytes(n: int, rows: int, dim: int) -> int:
-    return int(load_library().recis_embed_bwd_workspace_bytes(n, rows, dim))
+    return int(load_library().recis_embed_bwd_workspace_bytes(n, rows, int32(dim)))
 
 
 def recis_embed_bwd(tokens, n: int, grad_out, grad_dtype: int, grad_stride: int, rows: int, dim: int, scale: float,
                     grad_weight, weight_dtype: int, weight_stride: int, workspace, workspace_bytes: int,
                     error=None, stream=None):
     _check(load_library().recis_embed_bwd(
-        tokens.data_ptr(), n, grad_out.data_ptr(), grad_dtype, grad_stride, rows, dim, scale, grad_weight.data_ptr(),
-        weight_dtype, weight_stride, workspace.data_ptr(), workspace_bytes, _ptr(error), _stream(stream)),
-        "recis_embed_bwd")
+        tokens.data_ptr(), n, grad_out.data_ptr(), grad_dtype, grad_stride, rows, int32(dim), scale,
+        grad_weight.data_ptr(), weight_dtype, weight_stride, workspace.data_ptr(), workspace_bytes, _ptr(error),
+        _stream(stream)), "recis_embed_bwd")
 
 
 def recis_layernorm_fwd(x, dtype: int, x_stride: int, m: int, dim: int, weight, bias, weight_dtype: int, eps: float,
                         y, y_stride: int, mean=None, rstd=None, stream=None):
     _check(load_library().recis_layernorm_fwd(
-        x.data_ptr(), dtype, x_stride, m, dim, _ptr(weight), _ptr(bias), weight_dtype, eps, y.data_ptr(), y_stride,
-        _ptr(mean), _ptr(rstd), _stream(stream)), "recis_layernorm_fwd")
+        x.data_ptr(), dtype, x_stride, m, int32(dim), _ptr(weight), _ptr(bias), weight_dtype, eps, y.data_ptr(),
+        y_stride, _ptr(mean), _ptr(rstd), _stream(stream)), "recis_layernorm_fwd")
 
 
 def recis_layernorm_bwd_workspace_bytes(m: int, dim: int) -> int:
-    return int(load_library().recis_layernorm_bwd_workspace_bytes(m, dim))
+    return int(load_library().recis_layernorm_bwd_workspace_bytes(m, int32(dim)))
 
 
 def recis_layernorm_bwd(grad_y, grad_stride: int, x, x_stride: int, dtype: int, m: int, dim: int, mean, rstd, weight,
                         weight_dtype: int, grad_x, grad_x_stride: int, grad_weight, grad_bias, workspace,
                         workspace_bytes: int, stream=None):
     _check(load_library().recis_layernorm_bwd(
-        grad_y.data_ptr(), grad_stride, x.data_ptr(), x_stride, dtype, m, dim, mean.data_ptr(), rstd.data_ptr(),
+        grad_y.data_ptr(), grad_stride, x.data_ptr(), x_stride, dtype, m, int32(dim), mean.data_ptr(), rstd.data_ptr(),
         _ptr(weight), weight_dtype, grad_x.data_ptr(), grad_x_stride, _ptr(grad_weight), _ptr(grad_bias),
         _ptr(workspace), workspace_bytes, _stream(stream)), "recis_layernorm_bwd")
 

@@ -239,19 +239,20 @@ def _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error):
     b, q_len, q_heads, head_dim = q.shape
     if k.shape[-1] != head_dim or (kv_offsets is None and k.shape[0] != b):
         raise ValueError("k and v must have q's head_dim and batch")
+    kv_len = k.shape[1] if kv_offsets is None else max_kv_len or 0
     d = recis.recis_attn_desc()
-    d.dtype, d.batch, d.q_len, d.q_heads, d.head_dim = _dtype("q", q), b, q_len, q_heads, head_dim
-    d.kv_heads = k.shape[-2]
+    d.dtype = _dtype("q", q)
+    d.batch, d.q_len, d.kv_len, d.q_heads, d.kv_heads, d.head_dim = map(
+        recis.int32, (b, q_len, kv_len, q_heads, k.shape[-2], head_dim))
     d.scale = head_dim ** -0.5 if scale is None else scale
     keep = []
     if kv_offsets is not None:
         if kv_lens is not None or max_kv_len is None:
             raise ValueError("packed keys (kv_offsets) take max_kv_len, and no kv_lens")
         keep.append(_index("kv_offsets", kv_offsets, torch.int32, (b + 1,)))
-        d.kv_offsets, d.kv_len, d.kv_rows = keep[-1].data_ptr(), max_kv_len, k.shape[0]
+        d.kv_offsets, d.kv_rows = keep[-1].data_ptr(), k.shape[0]
     else:
-        d.kv_len = k.shape[1]
-        if max_kv_len is not None and max_kv_len != k.shape[1]:
+        if max_kv_len is not None and max_kv_len != kv_len:
             raise ValueError("max_kv_len goes with kv_offsets")
         if kv_lens is not None:
             keep.append(_index("kv_lens", kv_lens, torch.int32, (b,)))

@@ -139,3 +139,42 @@ def test_nothing_to_do_is_no_error(lib):
     d = desc(lib, batch=0)
     assert L.recis_cross_attn_fwd(C.byref(d), None, None, None, None, None, None, 0, None) == 0
     assert L.recis_cross_attn_bwd(C.byref(d), *[None] * 10, 0, None) == 0
+
+
+# Sizes past the C ABI's 32-bit integers are refused as the ABI refuses large ones, not taken by their low 32 bits.
+WIDE = [(1 << 31) + 64, (1 << 32) + 64, 1 << 40]
+
+
+@pytest.mark.parametrize("size", WIDE)
+def test_sizes_past_32_bits_have_no_workspace(lib, size):
+    assert lib.recis_layernorm_bwd_workspace_bytes(4, size) == -1
+    assert lib.recis_embed_bwd_workspace_bytes(4, 10, size) == -1
+    d = desc(lib)
+    d.kv_len = lib.int32(size)
+    assert lib.recis_cross_attn_workspace_bytes(d, True) == -1
+
+
+@pytest.mark.parametrize("size", WIDE)
+def test_rows_past_32_bits_are_refused(lib, size):
+    import torch
+    t, stream = torch.zeros(64), type("Stream", (), {"cuda_stream": None})
+    for call in (lambda: lib.recis_embed_fwd(t, 4, t, 0, 10, size, size, 1.0, t, size, stream=stream),
+                 lambda: lib.recis_embed_bwd(t, 4, t, 0, size, 10, size, 1.0, t, 0, size, t, 1 << 40, stream=stream),
+                 lambda: lib.recis_layernorm_fwd(t, 0, size, 4, size, None, None, 0, 1e-5, t, size, stream=stream),
+                 lambda: lib.recis_layernorm_bwd(t, size, t, size, 0, 4, size, t, t, None, 0, t, size, t, t, t, 1 << 40,
+                                                 stream=stream)):
+        with pytest.raises(lib.RecisError) as e:
+            call()
+        assert e.value.status == UNSUPPORTED
+
+
+@pytest.mark.parametrize("most,status", [(size, UNSUPPORTED) for size in WIDE] + [(-(1 << 32) + 5, INVALID)])
+def test_key_counts_past_32_bits_are_refused(lib, most, status):
+    import torch
+
+    from dynamic_embedding_tables_amd import sequence
+    q, k, offsets = torch.zeros(2, 3, 2, 8), torch.zeros(9, 2, 8), torch.tensor([0, 4, 9], dtype=torch.int32)
+    d, _ = sequence._attn_desc(q, k, k, None, offsets, None, most, None, None)
+    L = lib.load_library()
+    assert L.recis_cross_attn_fwd(C.byref(d), P, P, P, P, P, P, 1 << 40, None) == status
+    assert L.recis_cross_attn_bwd(C.byref(d), P, P, P, P, P, P, P, P, P, P, 1 << 40, None) == status

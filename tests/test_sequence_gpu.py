@@ -638,3 +638,16 @@ def test_refusals_on_tensors(seq):
     with pytest.raises(recis.RecisError) as e:
         seq.layer_norm(torch.randn(1, 16385).cuda())
     assert e.value.status == recis.RECIS_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("most", [(1 << 31) + 64, (1 << 32) + 9, 1 << 40])
+def test_key_counts_past_32_bits_are_refused(seq, most):
+    from dynamic_embedding_tables_amd import recis
+    q, k = torch.randn(2, 3, 2, 16).cuda(), torch.randn(9, 2, 16).cuda()
+    off = torch.tensor([0, 4, 9], dtype=torch.int32).cuda()
+    o, lse = seq.cross_attention(q, k, k, kv_offsets=off, max_kv_len=9, return_lse=True)
+    for call in (lambda: seq.cross_attention(q, k, k, kv_offsets=off, max_kv_len=most),
+                 lambda: seq.cross_attention_backward(q, q, k, k, o, lse, kv_offsets=off, max_kv_len=most)):
+        with pytest.raises(recis.RecisError) as e:
+            call()
+        assert e.value.status == recis.RECIS_ERR_UNSUPPORTED
