@@ -318,9 +318,9 @@ __device__ __forceinline__ bool no_key(unsigned long long bits) {
 //    die (9 entries of 0 to 1499 keys, 2 heads: 25 us against 31).
 constexpr int kDies = 8, kEntriesForDies = 64, kPairsForDies = 128;
 __device__ __forceinline__ bool place(const AttnArgs& a, int per, int* b, int* h, int* t) {
-  const int slot = blockIdx.x / a.dies, across = per * a.unit;
+  const int id = block_id(), slot = id / a.dies, across = per * a.unit;
   const int rest = slot % across;
-  const int bh = ((slot / across) * a.dies + blockIdx.x % a.dies) * a.unit + rest / per;
+  const int bh = ((slot / across) * a.dies + id % a.dies) * a.unit + rest / per;
   *t = rest % per;
   *b = bh / a.kv_heads;
   *h = bh % a.kv_heads;
@@ -1339,7 +1339,7 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
   };
   split(bh * p.row_tiles, p.few || f32 ? 2048 : 1024, p.few ? 256 : 128, &p.splits, &p.split_keys);
   split(bh * p.row_tiles, f32 ? 2048 : 1024, 128, &p.q_splits, &p.q_split_keys);
-  p.part_ml = round_up(bh * p.splits * rows * d->head_dim * 4, 256);
+  p.part_ml = p.splits > 1 ? round_up(bh * p.splits * rows * d->head_dim * 4, 256) : 0;
   p.fwd_bytes = p.splits > 1 ? p.part_ml + round_up(bh * p.splits * rows * 8, 256) : 0;
   p.part_dq = round_up(std::max<int64_t>(bh * rows, 1) * 8, 256);
   p.bwd_bytes = p.part_dq + (p.q_splits > 1 ? round_up(bh * p.q_splits * rows * d->head_dim * 4, 256) : 0);
@@ -1406,7 +1406,7 @@ bool elements_aligned(const recis_attn_desc* d, std::initializer_list<const void
 }
 
 dim3 attn_grid(const AttnArgs& a, int per) {
-  return dim3((unsigned)(round_up((int64_t)a.batch * a.kv_heads, a.dies * a.unit) * per));
+  return grid_of(round_up((int64_t)a.batch * a.kv_heads, a.dies * a.unit) * per);
 }
 
 enum AttnPass { kFwd, kFew, kBwdQ, kBwdKv };
@@ -1480,8 +1480,11 @@ void launch_join_q(const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_attn_join_q<T, 1>), join_grid(a, 1), dim3(kThreads), 0, s, a);
 }
 
-bool grid_fits(const recis_attn_desc* d, int64_t per) {
-  return round_up((int64_t)d->batch * d->kv_heads, (int64_t)kDies * d->kv_heads) * per < (1ll << 31);
+// A pass's blocks can be launched.
+bool grid_fits(const recis_attn_desc* d, const AttnPlan& p, bool backward) {
+  const int64_t per = backward ? std::max<int64_t>((int64_t)p.row_tiles * p.q_splits, p.key_tiles)
+                               : (int64_t)p.row_tiles * p.splits;
+  return round_up((int64_t)d->batch * d->kv_heads, (int64_t)kDies * d->kv_heads) * per <= kMaxBlocks;
 }
 
 }  // namespace
@@ -1494,6 +1497,7 @@ extern "C" {
 int64_t recis_cross_attn_workspace_bytes(const recis_attn_desc* desc, int32_t backward) {
   if (check_desc(desc) != RECIS_OK) return -1;
   const AttnPlan p = attn_plan(desc);
+  if (!grid_fits(desc, p, backward)) return -1;
   return backward ? p.bwd_bytes : p.fwd_bytes;
 }
 
@@ -1506,9 +1510,9 @@ recis_status recis_cross_attn_fwd(const recis_attn_desc* desc, const void* q, co
   if (!elements_aligned(desc, {q, out}) || (keys && !elements_aligned(desc, {k, v})) || !aligned_to(lse, 4))
     return RECIS_ERR_INVALID_ARG;
   const AttnPlan p = attn_plan(desc);
+  if (!grid_fits(desc, p, false)) return RECIS_ERR_UNSUPPORTED;
   if (p.fwd_bytes && (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.fwd_bytes))
     return RECIS_ERR_INVALID_ARG;
-  if (!grid_fits(desc, (int64_t)p.row_tiles * p.splits)) return RECIS_ERR_UNSUPPORTED;
   AttnArgs a;
   fill_args(desc, p, &a);
   a.q = q;
@@ -1542,8 +1546,8 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
       (keys && !elements_aligned(desc, {k, v, grad_k, grad_v})) || (rows && !lse) || !aligned_to(lse, 4))
     return RECIS_ERR_INVALID_ARG;
   const AttnPlan p = attn_plan(desc);
+  if (!grid_fits(desc, p, true)) return RECIS_ERR_UNSUPPORTED;
   if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.bwd_bytes) return RECIS_ERR_INVALID_ARG;
-  if (!grid_fits(desc, std::max<int64_t>((int64_t)p.row_tiles * p.q_splits, p.key_tiles))) return RECIS_ERR_UNSUPPORTED;
   AttnArgs a;
   fill_args(desc, p, &a);
   a.q = q;

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_fwd(const long long* __restr
                                                         const T* __restrict__ w, long long rows, long long w_stride,
                                                         int per_row, unsigned m, float scale, T* __restrict__ out,
                                                         long long out_stride, int stream, unsigned* error) {
-  const long long first = (long long)blockIdx.x * kFwdTile;
+  const long long first = (long long)block_id() * kFwdTile;
   const long long row0 = first / per_row;
   const unsigned rem = (unsigned)(first - row0 * per_row);
   long long row[kFwdBatch], tok[kFwdBatch];
@@ -69,7 +69,7 @@ void launch_fwd(const int64_t* tokens, int64_t n, const void* w, int64_t rows, i
   const int per_row = dim / V;
   const unsigned m = (unsigned)(((1ull << 32) + per_row - 1) / per_row);
   const int64_t blocks = (n * per_row + kFwdTile - 1) / kFwdTile;
-  hipLaunchKernelGGL((k_embed_fwd<T, V>), dim3((unsigned)blocks), dim3(kThreads), 0, s,
+  hipLaunchKernelGGL((k_embed_fwd<T, V>), grid_of(blocks), dim3(kThreads), 0, s,
                      reinterpret_cast<const long long*>(tokens), (long long)n, static_cast<const T*>(w),
                      (long long)rows, (long long)w_stride, per_row, m, scale, static_cast<T*>(out),
                      (long long)out_stride, (int)(n * dim * (int64_t)sizeof(T) > kStreamBytes), error);
@@ -608,6 +608,7 @@ BwdPlan bwd_plan(int64_t n, int64_t rows, int dim, int v) {
   const int64_t units = n + rows;
   const int64_t most = std::min(128, kMaxUnits / groups);
   p.quantum = (int)std::min<int64_t>(most, std::max<int64_t>(8, units / ((int64_t)groups * 1024)));
+  // (512 units a block or more in large calls: 2^23 blocks at most)
   p.blocks = (units + (int64_t)groups * p.quantum - 1) / ((int64_t)groups * p.quantum);
   p.few = n <= kFewTokens;
   if (p.few) {
@@ -670,6 +671,8 @@ void launch_sum(const BwdPlan& p, int v, const SumArgs& a, hipStream_t s) {
 constexpr int64_t kMaxTokens = (1ll << 31) - 4096;
 constexpr int64_t kMaxVocab = 1ll << 30;
 constexpr int kMaxDim = 1 << 16;
+constexpr int64_t kMaxElements = 1ll << 40;  // of the forward's result
+static_assert(kMaxElements / kFwdTile <= kMaxBlocks, "the forward's blocks can be launched");
 
 }  // namespace
 }  // namespace recis
@@ -683,14 +686,13 @@ recis_status recis_embed_fwd(const int64_t* tokens, int64_t n, const void* weigh
                              uint32_t* error, hipStream_t s) {
   if (!dtype_known(dtype) || n < 0 || rows < 1 || dim < 1 || weight_stride < dim || out_stride < dim)
     return RECIS_ERR_INVALID_ARG;
-  if (n > kMaxTokens || rows > kMaxVocab || dim > kMaxDim) return RECIS_ERR_UNSUPPORTED;
+  if (n > kMaxTokens || rows > kMaxVocab || dim > kMaxDim || n * dim > kMaxElements) return RECIS_ERR_UNSUPPORTED;
   if (n == 0) return RECIS_OK;
   const int size = dtype_size(dtype);
   if (!tokens || !weight || !out || !aligned_to(tokens, 8) || !aligned_to(weight, size) || !aligned_to(out, size) ||
       !aligned_to(error, 4))
     return RECIS_ERR_INVALID_ARG;
   const int v = access_width(size, dim, {weight, out}, {weight_stride, out_stride});
-  if ((n * (dim / v) + kFwdTile - 1) / kFwdTile > (1ll << 31) - 1) return RECIS_ERR_UNSUPPORTED;
   auto go = [&](auto launch) {
     launch(tokens, n, weight, rows, dim, weight_stride, scale, out, out_stride, error, s);
   };
@@ -730,7 +732,6 @@ recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_
   const int v = gv == 8 && wv == 4 && ws == 4 ? 8 : std::min(gv, wv);
   const BwdPlan p = bwd_plan(n, rows, dim, v);
   if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.bytes) return RECIS_ERR_INVALID_ARG;
-  if (p.blocks > (1ll << 31) - 1) return RECIS_ERR_UNSUPPORTED;
   char* w = static_cast<char*>(workspace);
   SortArgs o;
   o.tokens = reinterpret_cast<const long long*>(tokens);

@@ -112,6 +112,19 @@ inline bool dtype_known(int dtype) { return dtype == RECIS_DTYPE_F32 || dtype ==
 // Tensors hold naturally aligned elements; anything else is refused.
 inline bool aligned_to(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)size == 0; }
 
+// The blocks (of kThreads) of a launch that may have very many: a dimension of a
+// launch holds 2^32 - 1 threads at most, so from kRowBlocks on they lie in rows
+// of that many.  The last row's blocks past `blocks` have ids past it too, which
+// the kernel has to leave alone.  kRowBlocks is a multiple of the dies, so the
+// order in which blocks go to them is that of the ids.
+constexpr int64_t kRowBlocks = 1 << 22;
+constexpr int64_t kMaxBlocks = (1ll << 31) - kRowBlocks;  // every id fits an int
+inline dim3 grid_of(int64_t blocks) {
+  if (blocks <= kRowBlocks) return dim3((unsigned)blocks);
+  return dim3((unsigned)kRowBlocks, (unsigned)((blocks + kRowBlocks - 1) / kRowBlocks));
+}
+__device__ __forceinline__ int block_id() { return (int)(blockIdx.y * (unsigned)kRowBlocks + blockIdx.x); }
+
 inline recis_status launch_status() {
   return hipGetLastError() == hipSuccess ? RECIS_OK : RECIS_ERR_HIP;
 }

@@ -496,8 +496,8 @@ recis_status recis_profile_kernel(recis_table* t, const char* kernel, hipEvent_t
  * a negative token is padding and gives zeros.  tokens device [n]; weight
  * device [rows] rows of dim elements; out device [n] rows of dim elements, in
  * the weight's dtype.  A token >= rows gives zeros and records
- * RECIS_ERR_KEY_RANGE.  n <= 2^31 - 4096, rows <= 2^30, dim <= 65536 (else
- * UNSUPPORTED).  Passage: page "RecIS: Sparse to Dense, A Unified Training
+ * RECIS_ERR_KEY_RANGE.  n <= 2^31 - 4096, rows <= 2^30, dim <= 65536, n * dim
+ * <= 2^40 (else UNSUPPORTED).  Passage: page "RecIS: Sparse to Dense, A Unified Training
  * Framework for Recommendation Models", abstract (sparse and dense trained together). */
 recis_status recis_embed_fwd(const int64_t* tokens, int64_t n, const void* weight, int32_t dtype, int64_t rows,
                              int32_t dim, int64_t weight_stride, float scale, void* out, int64_t out_stride,
@@ -507,7 +507,7 @@ recis_status recis_embed_fwd(const int64_t* tokens, int64_t n, const void* weigh
  * every row written (zeros where no token fell), summed in float32 in the
  * order of the tokens sorted by value, equal tokens by place, and rounded once to
  * weight_dtype.  Tokens outside [0, rows) add nothing; one >= rows records
- * RECIS_ERR_KEY_RANGE.  Limits as above. */
+ * RECIS_ERR_KEY_RANGE.  The limits of n, rows and dim as above. */
 int64_t recis_embed_bwd_workspace_bytes(int64_t n, int64_t rows, int32_t dim);
 recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_out, int32_t grad_dtype,
                              int64_t grad_stride, int64_t rows, int32_t dim, float scale, void* grad_weight,
@@ -537,7 +537,12 @@ recis_status recis_layernorm_bwd(const void* grad_y, int64_t grad_stride, const 
                                  hipStream_t s);
 
 /* Cross attention's sizes, layouts and masks.  Strides are those of (batch
- * entry, position, head); the head vectors' elements are contiguous. */
+ * entry, position, head); the head vectors' elements are contiguous.  Limits
+ * (else UNSUPPORTED), with the q_heads / kv_heads query heads of a key head
+ * counted as queries of it: 2^30 queries and 2^30 keys an entry, 2^24 pairs of
+ * (entry, key head), and 2^31 - 2^22 tiles, which are the pairs, rounded up to a
+ * multiple of 8 * kv_heads, times an entry's queries (and for the backward its
+ * kv_len) in 64s. */
 typedef struct {
   int32_t dtype;              /* of q, k, v, out and every gradient */
   int32_t batch;

@@ -178,3 +178,22 @@ def test_key_counts_past_32_bits_are_refused(lib, most, status):
     L = lib.load_library()
     assert L.recis_cross_attn_fwd(C.byref(d), P, P, P, P, P, P, 1 << 40, None) == status
     assert L.recis_cross_attn_bwd(C.byref(d), P, P, P, P, P, P, P, P, P, P, 1 << 40, None) == status
+
+
+def test_sizes_past_a_launch_are_refused(lib):
+    """2^23 pairs of (entry, key head): 255 tiles of 64 keys can be launched for their gradients, 256 cannot."""
+    L = lib.load_library()
+    d = desc(lib, batch=1 << 20, q_heads=8, kv_heads=8, q_len=1, kv_len=255 * 64)
+    assert L.recis_cross_attn_workspace_bytes(C.byref(d), 0) == 0
+    assert L.recis_cross_attn_workspace_bytes(C.byref(d), 1) > 0
+    d.kv_len += 1
+    assert L.recis_cross_attn_workspace_bytes(C.byref(d), 0) == 0
+    assert L.recis_cross_attn_workspace_bytes(C.byref(d), 1) == -1
+    assert L.recis_cross_attn_bwd(C.byref(d), *[P] * 10, 1 << 60, None) == UNSUPPORTED
+    d.q_len, d.kv_len = 255 * 64 + 1, 5
+    for backward in (0, 1):
+        assert L.recis_cross_attn_workspace_bytes(C.byref(d), backward) == -1
+    assert L.recis_cross_attn_fwd(C.byref(d), *[P] * 6, 1 << 60, None) == UNSUPPORTED
+    assert L.recis_cross_attn_bwd(C.byref(d), *[P] * 10, 1 << 60, None) == UNSUPPORTED
+    many = dict(n=1 << 25, dim=(1 << 15) + 1, weight_stride=1 << 16, out_stride=1 << 16)
+    assert L.recis_embed_fwd(*{**EMBED_FWD, **many}.values()) == UNSUPPORTED

@@ -651,3 +651,42 @@ def test_key_counts_past_32_bits_are_refused(seq, most):
         with pytest.raises(recis.RecisError) as e:
             call()
         assert e.value.status == recis.RECIS_ERR_UNSUPPORTED
+
+
+def test_embed_of_more_blocks_than_a_launch_dimension(seq):
+    """2^24 + 64 blocks of 1024 elements."""
+    dim = 65535
+    n = ((1 << 34) + (1 << 16)) // dim + 1
+    gen = generator(19)
+    w = normal(gen, 3, dim, dtype=BF16).cuda()
+    t = (torch.arange(n) % 4 - 1).cuda()
+    out = seq.embed(t, w, scale=2.0)
+    want = torch.cat([torch.zeros(1, dim, dtype=BF16, device="cuda"), w * 2])
+    for first in range(4):   # every row, a quarter of them at a time
+        assert bool((out[first::4] == want[first]).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_cross_attention_of_more_blocks_than_a_launch_dimension(seq, dtype):
+    """65536 entries of 0 to 2 packed keys, 8 heads, max_kv_len 4096 (f32) or 8192: 2^25 key tiles.  Every tile past
+    an entry's keys has nothing to do, so the results are those of max_kv_len 2."""
+    gen = generator(20)
+    lens = torch.arange(1 << 16, dtype=torch.int32) % 3
+    off = torch.zeros((1 << 16) + 1, dtype=torch.int32)
+    off[1:] = lens.cumsum(0)
+    q, grad = (normal(gen, 1 << 16, 1, 8, 8, dtype=dtype).cuda() for _ in range(2))
+    k, v = (normal(gen, int(off[-1]), 8, 8, dtype=dtype).cuda() for _ in range(2))
+
+    def both(most):
+        kw = {"kv_offsets": off.cuda(), "max_kv_len": most}
+        o, lse = seq.cross_attention(q, k, v, return_lse=True, **kw)
+        return o, lse, *seq.cross_attention_backward(grad, q, k, v, o, lse, **kw)
+
+    wide, narrow = both(4096 if dtype == F32 else 8192), both(2)
+    assert all(torch.equal(a, b) for a, b in zip(wide, narrow))
+    some = slice((1 << 16) - 30, 1 << 16)   # the last entries against the definition
+    first = int(off[some.start])
+    kept = [torch.arange(int(off[i]) - first, int(off[i + 1]) - first) for i in range(some.start, some.stop)]
+    want = plain.attention(q[some].cpu(), k[first:].cpu(), v[first:].cpu(), 8**-0.5, kept, True, grad[some].cpu())
+    for name, t in zip(("o", "lse", "dq", "dk", "dv"), wide):
+        within(t[some] if t.shape[0] == 1 << 16 else t[first:], *want[name], what=name)
