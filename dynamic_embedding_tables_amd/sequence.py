@@ -92,9 +92,15 @@ def _on(stream, *tensors):
             t.record_stream(stream)
 
 
-def check(error):
-    """Raises RecisError for what the GPU recorded in an error word (waits for it)."""
-    bits = int(error.item())
+def check(error, stream=None):
+    """Raises RecisError for what the GPU recorded in an error word.  Waits for
+    `stream`, which has to be the one of every call that was given the word; by
+    default for all the GPU's streams."""
+    if stream is None:
+        torch.cuda.synchronize(error.device)
+        stream = torch.cuda.current_stream(error.device)
+    with torch.cuda.stream(stream):
+        bits = int(error.item())
     for status in (recis.RECIS_ERR_KEY_RANGE, recis.RECIS_ERR_INVALID_ARG):
         if bits >> status & 1:
             raise recis.RecisError(status, "device error")

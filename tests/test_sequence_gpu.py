@@ -690,3 +690,19 @@ def test_cross_attention_of_more_blocks_than_a_launch_dimension(seq, dtype):
     want = plain.attention(q[some].cpu(), k[first:].cpu(), v[first:].cpu(), 8**-0.5, kept, True, grad[some].cpu())
     for name, t in zip(("o", "lse", "dq", "dk", "dv"), wide):
         within(t[some] if t.shape[0] == 1 << 16 else t[first:], *want[name], what=name)
+
+
+def test_check_waits_for_the_stream_that_records(seq):
+    from dynamic_embedding_tables_amd import recis
+    side = torch.cuda.Stream()
+    w, t = torch.randn(10, 8).cuda(), torch.tensor([3, 10]).cuda()
+    for stream in (None, side):
+        error = torch.zeros(1, dtype=torch.int32).cuda()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1 << 27)   # some 50 ms of the stream's time
+        seq.embed(t, w, error=error, stream=side)
+        with pytest.raises(recis.RecisError) as e:
+            seq.check(error, **({"stream": stream} if stream else {}))
+        assert e.value.status == recis.RECIS_ERR_KEY_RANGE
+        torch.cuda.synchronize()
