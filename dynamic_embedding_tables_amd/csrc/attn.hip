@@ -1142,6 +1142,32 @@ struct RowStage {
   }
 };
 
+// Packed rows before the first entry and after the last have gradient zero: a
+// part of them from every block of the head, number `block` of `blocks`.  (512
+// entries of 0 to 1000 keys, 4 heads of 32 bfloat16, 50 queries, in a buffer of
+// twice the rows in use: the backward takes 151 us, 141 without the spare rows,
+// and 7.1 ms with one block a head for all of them.)
+template <typename T, int DP, bool ALN>
+__device__ __forceinline__ void zero_outside(const AttnArgs& a, int h, int block, int blocks) {
+  constexpr int V = ALN ? 8 : 1, kAcross = kCols<DP> / V, kRows = kThreads / kAcross;
+  const long long lo = std::min<long long>(std::max(a.kv_offsets[0], 0), a.kv_rows);
+  const long long hi = std::min<long long>(std::max(a.kv_offsets[a.batch], 0), a.kv_rows);
+  const long long n = lo + a.kv_rows - hi;
+  const int d = (int)(threadIdx.x % kAcross) * V;
+  if (d >= a.head_dim) return;
+  for (long long i = (long long)block * kRows + threadIdx.x / kAcross; i < n; i += (long long)blocks * kRows) {
+    const long long r = i < lo ? i : hi + (i - lo);
+    T* dk = static_cast<T*>(a.dk) + r * a.dks[1] + h * a.dks[2] + d;
+    T* dv = static_cast<T*>(a.dv) + r * a.dvs[1] + h * a.dvs[2] + d;
+    if constexpr (ALN) {
+      *reinterpret_cast<Frag<T>*>(dk) = Frag<T>{};
+      *reinterpret_cast<Frag<T>*>(dv) = Frag<T>{};
+    } else {
+      *dk = *dv = (T)0.f;
+    }
+  }
+}
+
 template <typename T, int DP, int KT, bool ALN>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int KK = kChunks32<DP>, DT = DP / 16;
@@ -1153,18 +1179,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = wave_of();
   const Span sp = kv_span(a, b);
   const int block_key = tile * (16 * KT * kAttnWaves);
-  if (tile == 0 && a.kv_offsets) {  // packed rows before the first entry and after the last: zero
-    const long long lo = std::min<long long>(std::max(a.kv_offsets[0], 0), a.kv_rows);
-    const long long hi = std::min<long long>(std::max(a.kv_offsets[a.batch], 0), a.kv_rows);
-    const long long n0 = b == 0 ? lo : 0, n = n0 + (b == a.batch - 1 ? a.kv_rows - hi : 0);
-    for (long long i = wave; i < n; i += kAttnWaves) {
-      const long long r = i < n0 ? i : hi + (i - n0);
-      for (int d = lane; d < a.head_dim; d += 64) {
-        static_cast<T*>(a.dk)[r * a.dks[1] + h * a.dks[2] + d] = (T)0.f;
-        static_cast<T*>(a.dv)[r * a.dvs[1] + h * a.dvs[2] + d] = (T)0.f;
-      }
-    }
-  }
+  if (a.kv_offsets) zero_outside<T, DP, ALN>(a, h, b * a.key_tiles + tile, a.batch * a.key_tiles);
   // padded keys past the length still get their (zero) gradient
   const int end = a.kv_offsets ? sp.len : a.kv_len;
   if (block_key >= end) return;
@@ -1317,7 +1332,7 @@ recis_status check_desc(const recis_attn_desc* d) {
   return RECIS_OK;
 }
 
-constexpr int kMaxSplits = 256;
+constexpr int kMaxSplits = 256, kBlocksForOutside = 512;
 
 AttnPlan attn_plan(const recis_attn_desc* d) {
   AttnPlan p;
@@ -1329,6 +1344,12 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
   p.kt = d->dtype == RECIS_DTYPE_BF16 && p.dp <= 64 ? 2 : 1;
   p.row_tiles = (int)((rows + 64 * p.qt - 1) / (64 * p.qt));
   p.key_tiles = std::max(1, (int)(((int64_t)d->kv_len + 64 * p.kt - 1) / (64 * p.kt)));
+  // few pairs over a large packed buffer: further tiles, without keys, for its
+  // rows outside the entries (zero_outside; one entry, 2 heads of 64, 2M spare
+  // rows: 232 us, 53 ms from its two blocks)
+  if (d->kv_offsets && bh > 0 && bh < kBlocksForOutside)
+    p.key_tiles = std::max(p.key_tiles, (int)std::min<int64_t>((kBlocksForOutside + bh - 1) / bh,
+                                                               d->kv_rows / ((int64_t)d->batch * kBlockKeys)));
   p.few = rows <= kFewRows;
   // keys are split until there are `want` blocks (of unequal length where the
   // entries' are), `least` keys each, kMaxSplits ranges at most

@@ -706,3 +706,31 @@ def test_check_waits_for_the_stream_that_records(seq):
             seq.check(error, **({"stream": stream} if stream else {}))
         assert e.value.status == recis.RECIS_ERR_KEY_RANGE
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [32, 33])
+@pytest.mark.parametrize("front,back", [(0, 5000), (4001, 0), (70000, 90001)])
+def test_packed_rows_outside_the_entries_get_zeros(seq, front, back, dim, dtype):
+    """Buffers of a fixed capacity, of which the entries take a part."""
+    gen = generator(24, front, back, dim)
+    lens = [130, 0, 7]
+    off = torch.tensor([front + sum(lens[:i]) for i in range(4)], dtype=torch.int32)
+    rows = front + sum(lens) + back
+    q, grad = normal(gen, 3, 5, 4, dim, dtype=dtype), normal(gen, 3, 5, 4, dim, dtype=dtype)
+    k, v = torch.full((rows, 2, dim), math.nan, dtype=dtype), torch.full((rows, 2, dim), math.nan, dtype=dtype)
+    used = slice(front, front + sum(lens))
+    k[used], v[used] = normal(gen, sum(lens), 2, dim, dtype=dtype), normal(gen, sum(lens), 2, dim, dtype=dtype)
+    kw = on_gpu({"kv_offsets": off, "max_kv_len": 150})
+    dev = [t.cuda() for t in (q, k, v)]
+    o, lse = seq.cross_attention(*dev, return_lse=True, **kw)
+    for fill in (math.nan, 3.0):   # what the allocator's memory holds before
+        junk = [torch.full((rows, 2, dim), fill, dtype=dtype, device="cuda") for _ in range(3)]
+        del junk
+        _, dk, dv = seq.cross_attention_backward(grad.cuda(), *dev, o, lse, **kw)
+        for t in (dk, dv):
+            assert not bool(t[:front].any()) and not bool(t[used.stop:].any())
+    kept = [torch.arange(int(off[i]), int(off[i + 1])) - front for i in range(3)]
+    want = plain.attention(q, k[used], v[used], dim**-0.5, kept, True, grad)
+    within(dk[used], *want["dk"])
+    within(dv[used], *want["dv"])
