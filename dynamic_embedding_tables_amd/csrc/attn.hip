@@ -50,6 +50,7 @@ struct AttnArgs {
   int q_splits, q_split_keys;  // dQ: the same, joined by k_attn_join_q
   float scale;
   float *part_o, *part_ml;     // [batch * kv_heads][splits][rows][head_dim], [..][2]
+  int* kept;                   // [batch][kKeptWords], from k_attn_kept to k_attn_bwd_q; or null
   unsigned* error;
 };
 
@@ -860,13 +861,57 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
 }
 
 // ----------------------------------------------------------------- backward
+// The keys that a mask leaves an entry, where they are 64 at most: their number
+// and places, in order.  (More: a number above 64.)  A block an entry, 8 * 64
+// keys a wave and round.  A kernel of its own because k_attn_bwd_q's blocks would
+// each count again: 4 entries of 8192 keys, 50 queries, 8 heads of 64, about 40
+// keys left, the backward takes 71 us so, 111 us otherwise and 58 with delta from
+// out; with 90% left 68 us, 71 and 65.
+constexpr int kMostKept = 64, kKeptWords = 1 + kMostKept;
+__global__ __launch_bounds__(kThreads) void k_attn_kept(AttnArgs a) {
+  __shared__ int counts[kAttnWaves];
+  const int b = block_id(), lane = threadIdx.x & 63, wave = wave_of();
+  if (b >= a.batch) return;
+  const Span sp = kv_span(a, b);
+  int* list = a.kept + (long long)b * kKeptWords;
+  constexpr int kTiles = 8;
+  int kept = 0;
+  for (int round = 0; round < sp.len && kept <= kMostKept; round += kAttnWaves * kTiles * 64) {
+    const int first = round + wave * kTiles * 64;
+    unsigned long long bits[kTiles];
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u) bits[u] = key_bits(a, sp, b, first + u * 64, lane);
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u) mine += __popcll(bits[u]);
+    if (lane == 0) counts[wave] = mine;
+    __syncthreads();
+    int at = kept;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      if (w < wave) at += counts[w];
+      kept += counts[w];
+    }
+    if (kept <= kMostKept) {
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
+        if ((bits[u] >> lane) & 1)
+          list[1 + at + __popcll(bits[u] & ((1ull << lane) - 1))] = first + u * 64 + lane;
+        at += __popcll(bits[u]);
+      }
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) list[0] = kept;
+}
+
 // Three products of the forward's two sizes and the exponentials again.  The
 // registers of Q, dO and dQ leave two waves a SIMD; held to three the kernel
 // spills (222 us against 207 for the case above, 100 GFLOP: 485 TFLOP/s).
 //
 // dQ, and for k_attn_bwd_kv each row's L and delta in the form it starts its
 // sums with: the forward's walk over the keys, with P from the saved L.
-template <typename T, int DP, int QT, bool ALN>
+template <typename T, int DP, int QT, bool ALN, bool MASKED>
 __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
   constexpr int KK = kChunks32<DP>, DT = DP / 16;
   constexpr int kKeys = kTileKeys<T, DP>, kTile = kKeys * kLd<T, DP>;
@@ -909,11 +954,65 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) dq[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  // delta from out carries out's rounding.  Over many keys that is far below
-  // dS's own; an entry of one tile (with bfloat16) gets delta from P and dP
-  // instead: with two keys left, dS would be mostly rounding.
-  const bool short_entry = sizeof(T) == 2 && sp.len <= kKeys;
+  // delta from out carries out's rounding, which a key with nearly all the
+  // weight sees whole.  So with bfloat16 an entry of which 64 keys at most count
+  // gets delta from P and dP: in the loop where it has one tile, and where a
+  // mask leaves so few (MASKED), from a tile of their own.
   Stage<T, DP, kKeys, ALN> sk, sv;
+  float from_p[QT];
+  auto add_delta = [&](const T* tk, const T* tv, unsigned long long now) {
+#pragma unroll
+    for (int n = 0; n < kKeys; n += 16) {
+      f32x4 s[QT], dp[QT];
+#pragma unroll
+      for (int c = 0; c < KK; ++c) {
+        const Frag<T> fk = read_rows<DP>(tk, n, c, lane), fv = read_rows<DP>(tv, n, c, lane);
+#pragma unroll
+        for (int j = 0; j < QT; ++j) {
+          s[j] = mma_head<DP>(fk, q[j][c], c == 0 ? zero : s[j], c);
+          dp[j] = mma_head<DP>(fv, g[j][c], c == 0 ? zero : dp[j], c);
+        }
+      }
+      const unsigned mine = (unsigned)(now >> (n + (lane >> 4) * 4));
+#pragma unroll
+      for (int j = 0; j < QT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((mine >> i) & 1) from_p[j] += __builtin_amdgcn_exp2f(s[j][i] * c2 - lse2[j]) * dp[j][i];
+    }
+  };
+  auto take_delta = [&] {
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+      const float x = -group_add(from_p[j]);
+      start[j] = f32x4{x, x, x, x};
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < QT; ++j) from_p[j] = 0.f;
+  const bool short_entry = sizeof(T) == 2 && sp.len <= kKeys;
+  if constexpr (MASKED) {
+    const int* list = a.kept + (long long)b * kKeptWords;
+    const int kept = list[0];
+    if (!short_entry && kept <= kKeys) {  // in every block of the entry
+      const int row = threadIdx.x / sk.kAcross, d0 = (threadIdx.x % sk.kAcross) * 8;
+      sk.row = sv.row = row;
+      sk.d0 = sv.d0 = d0;
+#pragma unroll
+      for (int i = 0; i < sk.kPer; ++i) {
+        const bool in = row + i * sk.kStep < kept;
+        const long long key = in ? list[1 + row + i * sk.kStep] : 0;
+        sk.f[i] = load8<T, ALN>(kb + key * a.ks[1], d0, a.head_dim, in);
+        sv.f[i] = load8<T, ALN>(vb + key * a.vs[1], d0, a.head_dim, in);
+      }
+      sk.store(tiles);
+      sv.store(tiles + kTile);
+      __syncthreads();
+      add_delta(tiles, tiles + kTile, kept < 64 ? (1ull << kept) - 1 : ~0ull);
+      take_delta();
+      __syncthreads();  // the loop starts with the same buffer
+    }
+  }
   unsigned long long bits = 0;
   const int key0 = split * a.q_split_keys;
   const int key1 = std::min(sp.len, key0 + a.q_split_keys);
@@ -939,31 +1038,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_q(AttnArgs a) {
     }
     if (no_key<kKeys>(now)) continue;
     if (short_entry) {
-      float sum[QT] = {};
-#pragma unroll
-      for (int n = 0; n < kKeys; n += 16) {
-        f32x4 s[QT], dp[QT];
-#pragma unroll
-        for (int c = 0; c < KK; ++c) {
-          const Frag<T> fk = read_rows<DP>(tk, n, c, lane), fv = read_rows<DP>(tv, n, c, lane);
-#pragma unroll
-          for (int j = 0; j < QT; ++j) {
-            s[j] = mma_head<DP>(fk, q[j][c], c == 0 ? zero : s[j], c);
-            dp[j] = mma_head<DP>(fv, g[j][c], c == 0 ? zero : dp[j], c);
-          }
-        }
-        const unsigned mine = (unsigned)(now >> (n + (lane >> 4) * 4));
-#pragma unroll
-        for (int j = 0; j < QT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((mine >> i) & 1) sum[j] += __builtin_amdgcn_exp2f(s[j][i] * c2 - lse2[j]) * dp[j][i];
-      }
-#pragma unroll
-      for (int j = 0; j < QT; ++j) {
-        const float x = -group_add(sum[j]);
-        start[j] = f32x4{x, x, x, x};
-      }
+      add_delta(tk, tv, now);
+      take_delta();
     }
 #pragma unroll
     for (int n = 0; n < kKeys; n += 32) {
@@ -1315,7 +1391,7 @@ struct AttnPlan {
   int dp, qt, kt;
   bool few;
   int row_tiles, key_tiles, splits, split_keys, q_splits, q_split_keys;
-  int64_t part_ml, part_dq, fwd_bytes, bwd_bytes;
+  int64_t part_ml, part_dq, kept, fwd_bytes, bwd_bytes;
 };
 
 recis_status check_desc(const recis_attn_desc* d) {
@@ -1363,7 +1439,8 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
   p.part_ml = p.splits > 1 ? round_up(bh * p.splits * rows * d->head_dim * 4, 256) : 0;
   p.fwd_bytes = p.splits > 1 ? p.part_ml + round_up(bh * p.splits * rows * 8, 256) : 0;
   p.part_dq = round_up(std::max<int64_t>(bh * rows, 1) * 8, 256);
-  p.bwd_bytes = p.part_dq + (p.q_splits > 1 ? round_up(bh * p.q_splits * rows * d->head_dim * 4, 256) : 0);
+  p.kept = p.part_dq + (p.q_splits > 1 ? round_up(bh * p.q_splits * rows * d->head_dim * 4, 256) : 0);
+  p.bwd_bytes = p.kept + (f32 ? 0 : round_up((int64_t)d->batch * kKeptWords * 4, 256));
   return p;
 }
 
@@ -1438,9 +1515,13 @@ void launch_pass(AttnPass pass, const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_attn_fwd<T, DP, N, ALN>), attn_grid(a, a.row_tiles * a.splits), dim3(kThreads), 0, s, a);
   else if (pass == kFew) {
     if constexpr (N == 1) hipLaunchKernelGGL((k_attn_few<T, DP, ALN>), attn_grid(a, a.splits), dim3(kThreads), 0, s, a);
-  } else if (pass == kBwdQ)
-    hipLaunchKernelGGL((k_attn_bwd_q<T, DP, N, ALN>), attn_grid(a, a.row_tiles * a.q_splits), dim3(kThreads), 0, s, a);
-  else
+  } else if (pass == kBwdQ) {
+    const dim3 grid = attn_grid(a, a.row_tiles * a.q_splits);
+    if (sizeof(T) == 2 && a.kept)
+      hipLaunchKernelGGL((k_attn_bwd_q<T, DP, N, ALN, sizeof(T) == 2>), grid, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_attn_bwd_q<T, DP, N, ALN, false>), grid, dim3(kThreads), 0, s, a);
+  } else
     hipLaunchKernelGGL((k_attn_bwd_kv<T, DP, N, ALN>), attn_grid(a, a.key_tiles), dim3(kThreads), 0, s, a);
 }
 
@@ -1579,12 +1660,16 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
   a.lse = const_cast<float*>(lse);
   a.stats = static_cast<f32x2*>(workspace);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_dq);
+  // a mask over more than a tile of keys may leave few
+  if (desc->dtype == RECIS_DTYPE_BF16 && desc->kv_mask && desc->kv_len > kBlockKeys)
+    a.kept = reinterpret_cast<int*>(static_cast<char*>(workspace) + p.kept);
   a.dq = grad_q;
   a.dk = grad_k;
   a.dv = grad_v;
   const bool aln = rows_aligned(desc, {q, k, v, out, grad_out, grad_q, grad_k, grad_v},
                                 {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides,
                                  desc->do_strides, desc->dq_strides, desc->dk_strides, desc->dv_strides});
+  if (rows && a.kept) hipLaunchKernelGGL(k_attn_kept, grid_of(desc->batch), dim3(kThreads), 0, s, a);
   if (rows) launch_attn(kBwdQ, desc->dtype, p, aln, a, s);
   if (rows && p.q_splits > 1) {
     if (desc->dtype == RECIS_DTYPE_BF16)

@@ -586,7 +586,9 @@ recis_status recis_cross_attn_fwd(const recis_attn_desc* desc, const void* q, co
                                   float* lse, void* workspace, int64_t workspace_bytes, hipStream_t s);
 
 /* Gradients of q, k and v from the forward's out and lse.  With bfloat16 the
- * score gradients are rounded to bfloat16 before they meet k and q.  Keys that do not
+ * score gradients are rounded to bfloat16 before they meet k and q, and
+ * sum(grad_out * out) carries out's rounding for an entry of which more than 64
+ * keys count.  Keys that do not
  * count get zeros (packed rows before the first entry and after the last
  * among them); the gradients of a shared key head are summed over its query
  * heads.  With batch 0 nothing is written. */

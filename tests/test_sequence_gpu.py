@@ -734,3 +734,68 @@ def test_packed_rows_outside_the_entries_get_zeros(seq, front, back, dim, dtype)
     want = plain.attention(q, k[used], v[used], dim**-0.5, kept, True, grad)
     within(dk[used], *want["dk"])
     within(dv[used], *want["dv"])
+
+
+@pytest.mark.parametrize("layout", ["lens", "mask", "packed mask"])
+def test_cross_attention_score_gradients_of_few_keys(seq, layout):
+    """Three keys that count, by a length or by a mask over 700: delta is taken in float32, so a score gradient is off
+    by its own roundings only.  (delta from the rounded out is off by 2^-9 of sum |dO| |O|, far above a score gradient
+    whose weight is near 1.)"""
+    gen = generator(22)
+    n, d, scale = 3, 64, 0.5   # scores of deviation 4: one key often has nearly all the weight
+    q, grad = normal(gen, 3, 50, 4, d, dtype=BF16), normal(gen, 3, 50, 4, d, dtype=BF16)
+    k, v = normal(gen, 3, 700, 2, d, dtype=BF16), normal(gen, 3, 700, 2, d, dtype=BF16)
+    places = torch.tensor([[0, 350, 699], [63, 64, 65], [5, 300, 301]])
+    if layout == "lens":
+        places = torch.arange(n).expand(3, n)
+        kw = {"kv_lens": torch.full((3,), n, dtype=torch.int32)}
+    else:
+        kw = {"kv_mask": torch.zeros(3, 700, dtype=torch.bool).scatter_(1, places, True)}
+    kept = list(places)
+    want = plain.attention(q, k, v, scale, kept, False, grad)
+    packed = layout.startswith("packed")
+    if packed:
+        kw = {"kv_mask": kw["kv_mask"].reshape(-1), "kv_offsets": torch.arange(4, dtype=torch.int32) * 700,
+              "max_kv_len": 700}
+    dev = [(t.reshape(2100, 2, d) if packed and t.shape[1] == 700 else t).cuda() for t in (q, k, v)]
+    o, lse = seq.cross_attention(*dev, return_lse=True, scale=scale, **on_gpu(kw))
+    dq, dk, dv = (t.cpu().double().reshape(s.shape) for t, s in zip(
+        seq.cross_attention_backward(grad.cuda(), *dev, o, lse, scale=scale, **on_gpu(kw)), (q, k, v)))
+    for name, t in (("o", o), ("lse", lse), ("dv", dv)):
+        within(t, *want[name], what=name)
+    u, ub = plain.U32, plain.U[BF16]
+    for b in range(3):
+        for h in range(4):
+            Q, G, K, V = (t.double() for t in (q[b, :, h], grad[b, :, h], k[b, kept[b], h // 2], v[b, kept[b], h // 2]))
+            P = torch.softmax(scale * Q @ K.T, -1)
+            # a weight's relative error: its score's (a float32 sum of d products, and the lse of the forward), the exponential's
+            size = scale * Q.abs() @ K.abs().T
+            eP = (d + 16) * u * size + 2 * want["lse"][1][b, :, h][:, None] + 16 * u * (size.amax(-1, keepdim=True) + 1)
+            dP, mag = G @ V.T, G.abs() @ V.abs().T
+            edP = (d + 2) * u * mag
+            delta, edelta = (P * dP).sum(-1, keepdim=True), (P * (eP * dP.abs() + edP + (n + 2) * u * dP.abs())).sum(
+                -1, keepdim=True)
+            dS = P * (dP - delta)
+            edS = dS.abs() * (eP + ub) + P * (1 + eP) * (1 + ub) * (edP + edelta + 4 * u * (dP.abs() + delta.abs()))
+            value, bound = scale * dS @ K, scale * (edS + 8 * u * dS.abs()) @ K.abs()
+            within(dq[b, :, h], value, bound + ub * (value.abs() + bound) + plain.TINY, what=(layout, "dq"))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("d", [32, 40, 77, 128])
+def test_cross_attention_masks_that_leave_64_keys_or_65(seq, d, packed):
+    gen = generator(25, d)
+    lk, counts = 5000, (64, 65, 0, 1, 3, 4000)
+    q, k, v = (normal(gen, len(counts), n, 2, d, dtype=BF16) for n in (20, lk, lk))
+    mask = torch.zeros(len(counts), lk, dtype=torch.bool)
+    for b, n in enumerate(counts):
+        mask[b, torch.randperm(lk, generator=gen)[:n]] = True
+    mask[3:5] = False
+    mask[3, lk - 1] = True
+    mask[4, [0, 2047, 2048]] = True   # the ends of the first 2048 keys
+    kw = {"kv_mask": mask}
+    if packed:
+        off = torch.arange(len(counts) + 1, dtype=torch.int32) * lk
+        kw, k, v = {"kv_mask": mask.reshape(-1), "kv_offsets": off, "max_kv_len": lk}, k.reshape(-1, 2, d), v.reshape(-1, 2, d)
+    kept = plain.kept_keys(k, None, kw.get("kv_offsets"), kw["kv_mask"])
+    check_attention(seq, q, k, v, kw, kept, grad=normal(gen, *q.shape, dtype=BF16), what=(d, packed))
