@@ -57,8 +57,9 @@ __global__ __launch_bounds__(kThreads) void k_embed_fwd(const long long* __restr
 #pragma unroll
   for (int b = 0; b < kFwdBatch; ++b) {
     if (row[b] >= n) continue;
+    const float by = tok[b] >= 0 && tok[b] < rows ? scale : 0.f;  // (a scale may be infinite)
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[b][i] *= scale;
+    for (int i = 0; i < V; ++i) v[b][i] *= by;
     store_or_stream<T, V>(stream, out + row[b] * out_stride + col[b], v[b]);
   }
 }
@@ -455,6 +456,16 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     ++row;
   };
+  // rows up to `to`: the first may have tokens (`open`), the others have none
+  // and are zero whatever the scale
+  bool open = began;
+  auto advance = [&](int to) {
+    if (row >= to) return;
+    if (open) finish_row();
+    const float none[V] = {};
+    for (; row < to; ++row)
+      if (live) store_or_stream<TW, V>(a.stream, out + (long long)row * a.out_stride + col, none);
+  };
   // the next batch's gradient rows are on their way while one is added up
   Vec<TG, V> x[kBatch], ahead[kBatch];
   auto fetch = [&](int i, Vec<TG, V>(&to)[kBatch]) {
@@ -471,7 +482,8 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
     for (int b = 0; b < kBatch; ++b) {
       const unsigned t = i + b < i1 ? slice[i + b].key : (unsigned)a.rows;
       if (t < (unsigned)a.rows) {
-        while (row < (int)t) finish_row();
+        advance((int)t);
+        open = true;
         if (live) {
 #pragma unroll
           for (int k = 0; k < V; ++k) acc[k] += (float)x[b].e[k];
@@ -481,7 +493,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_sum(SumArgs a) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) x[b] = ahead[b];
   }
-  while (row < row_end) finish_row();
+  advance(row_end);
   const int rows_of = threadIdx.x < groups ? row_of(threadIdx.x) : 0;
   const int begun_of = threadIdx.x < groups ? has_tokens(threadIdx.x) : 0;
   const int last_row = row_of(groups);

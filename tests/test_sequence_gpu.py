@@ -799,3 +799,19 @@ def test_cross_attention_masks_that_leave_64_keys_or_65(seq, d, packed):
         kw, k, v = {"kv_mask": mask.reshape(-1), "kv_offsets": off, "max_kv_len": lk}, k.reshape(-1, 2, d), v.reshape(-1, 2, d)
     kept = plain.kept_keys(k, None, kw.get("kv_offsets"), kw["kv_mask"])
     check_attention(seq, q, k, v, kw, kept, grad=normal(gen, *q.shape, dtype=BF16), what=(d, packed))
+
+
+@pytest.mark.parametrize("scale", [math.inf, math.nan])
+@pytest.mark.parametrize("n", [600, 5000])   # gradient by one launch and by sorted tokens
+def test_embed_rows_without_a_token_are_zero_whatever_the_scale(seq, n, scale):
+    gen = generator(21, n)
+    t, w, g = tokens_of(gen, n, 40) * 3, normal(gen, 120, 33), normal(gen, n, 33)   # rows 0, 3, 6 ... and -3
+    t[5] = 120                                                                       # beyond the table
+    for dtype in DTYPES:
+        out = seq.embed(t.cuda(), w.to(dtype).cuda(), scale=scale).cpu()
+        gone = (t < 0) | (t >= 120)
+        assert bool((out[gone] == 0).all()) and not bool(torch.isfinite(out[~gone]).any())
+        dw = seq.embed_backward(t.cuda(), g.to(dtype).cuda(), 120, scale=scale).cpu()
+        named = torch.zeros(120, dtype=torch.bool)
+        named[t[~gone]] = True
+        assert bool((dw[~named] == 0).all()) and not bool(torch.isfinite(dw[named]).any())
