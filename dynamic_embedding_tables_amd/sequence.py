@@ -250,7 +250,7 @@ def _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error):
     d.dtype = _dtype("q", q)
     d.batch, d.q_len, d.kv_len, d.q_heads, d.kv_heads, d.head_dim = map(
         recis.int32, (b, q_len, kv_len, q_heads, k.shape[-2], head_dim))
-    d.scale = head_dim ** -0.5 if scale is None else scale
+    d.scale = max(head_dim, 1) ** -0.5 if scale is None else scale  # (the call refuses 0)
     keep = []
     if kv_offsets is not None:
         if kv_lens is not None or max_kv_len is None:

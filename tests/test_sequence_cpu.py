@@ -197,3 +197,12 @@ def test_sizes_past_a_launch_are_refused(lib):
     assert L.recis_cross_attn_bwd(C.byref(d), *[P] * 10, 1 << 60, None) == UNSUPPORTED
     many = dict(n=1 << 25, dim=(1 << 15) + 1, weight_stride=1 << 16, out_stride=1 << 16)
     assert L.recis_embed_fwd(*{**EMBED_FWD, **many}.values()) == UNSUPPORTED
+
+
+def test_empty_head_vectors_are_refused(lib):
+    import torch
+
+    from dynamic_embedding_tables_amd import sequence
+    q, k = torch.zeros(2, 3, 2, 0), torch.zeros(2, 5, 2, 0)
+    d, _ = sequence._attn_desc(q, k, k, None, None, None, None, None, None)
+    assert lib.load_library().recis_cross_attn_fwd(C.byref(d), P, P, P, P, P, P, 1 << 40, None) == INVALID

@@ -815,3 +815,13 @@ def test_embed_rows_without_a_token_are_zero_whatever_the_scale(seq, n, scale):
         named = torch.zeros(120, dtype=torch.bool)
         named[t[~gone]] = True
         assert bool((dw[~named] == 0).all()) and not bool(torch.isfinite(dw[named]).any())
+
+
+def test_empty_head_vectors_are_refused(seq):
+    from dynamic_embedding_tables_amd import recis
+    q, k = torch.randn(2, 3, 4, 0).cuda(), torch.randn(2, 5, 2, 0).cuda()
+    lse = torch.zeros(2, 3, 4).cuda()
+    for call in (lambda: seq.cross_attention(q, k, k), lambda: seq.cross_attention_backward(q, q, k, k, q, lse)):
+        with pytest.raises(recis.RecisError) as e:
+            call()
+        assert e.value.status == recis.RECIS_ERR_INVALID_ARG
