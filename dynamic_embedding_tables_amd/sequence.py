@@ -4,7 +4,8 @@ What reads and trains the rows a table gathers.  Each function checks its
 tensors, allocates what it returns and its workspace from torch's caching
 allocator, and makes one call of the C ABI (``include/recis.h`` states the
 formulas); the arithmetic is in the library's HIP kernels, and there is no
-fallback.  Forward and backward are separate calls, as the table's are.
+fallback.  Forward and backward are separate calls, as the table's are: no
+graph is recorded, and a forward call whose inputs require a gradient warns.
 
 Tensors are float32 or bfloat16 on the current GPU.  Rows (the last axis) are
 contiguous, the other axes may be strided; a tensor whose last axis is strided
@@ -19,6 +20,7 @@ raises for what it holds.
 from __future__ import annotations
 
 import contextlib
+import warnings
 from typing import Optional
 
 import torch
@@ -42,6 +44,16 @@ def _on_gpu(*tensors):
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"every tensor must be on the current GPU (cuda:{here}); {list(t.shape)} is on {t.device}")
+
+
+def _forward_of(name: str, *tensors):
+    """The same for a forward call; says so where a gradient would get lost."""
+    _on_gpu(*tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"sequence.{name} records no graph, so its inputs get no gradient through it: call "
+                          f"{name}_backward, and pass detached tensors or work under torch.no_grad()", stacklevel=3)
+            return
 
 
 def _index(name: str, t, dtype, shape):
@@ -113,7 +125,7 @@ def embed(tokens, weight, scale: float = 1.0, out=None, error=None, stream=None)
     if stream is not None:
         with _on(stream, tokens, weight, out, error):
             return embed(tokens, weight, scale, out, error)
-    _on_gpu(tokens, weight, out, _error_word(error))
+    _forward_of("embed", tokens, weight, out, _error_word(error))
     if tokens.dtype != torch.int64 or weight.dim() != 2:
         raise ValueError("tokens must be int64 and weight [rows, dim]")
     dtype = _dtype("weight", weight)
@@ -173,7 +185,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = True,
     if stream is not None:
         with _on(stream, x, weight, bias, out):
             return layer_norm(x, weight, bias, eps, stats, out)
-    _on_gpu(x, weight, bias, out)
+    _forward_of("layer_norm", x, weight, bias, out)
     if x.dim() < 1:
         raise ValueError("x must be [..., dim]")
     dtype, dim = _dtype("x", x), x.shape[-1]
@@ -292,7 +304,7 @@ def cross_attention(q, k, v, kv_lens=None, kv_offsets=None, kv_mask=None, max_kv
     if stream is not None:
         with _on(stream, q, k, v, kv_lens, kv_offsets, kv_mask, error):
             return cross_attention(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, return_lse, error)
-    _on_gpu(q, k, v, kv_lens, kv_offsets, kv_mask, error)
+    _forward_of("cross_attention", q, k, v, kv_lens, kv_offsets, kv_mask, error)
     q, k, v = _heads(q), _heads(k), _heads(v)
     d, keep = _attn_desc(q, k, v, kv_lens, kv_offsets, kv_mask, max_kv_len, scale, error)
     out = _like(q)

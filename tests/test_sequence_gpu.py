@@ -1,6 +1,7 @@
 """The sequence operators on the GPU against their definitions in 64 bits, at
 the sizes, layouts and masks where they can go wrong (bounds: sequence_plain)."""
 import math
+import warnings
 
 import pytest
 import torch
@@ -825,3 +826,25 @@ def test_empty_head_vectors_are_refused(seq):
         with pytest.raises(recis.RecisError) as e:
             call()
         assert e.value.status == recis.RECIS_ERR_INVALID_ARG
+
+
+def test_inputs_that_require_a_gradient_are_warned_about(seq):
+    """The calls record no graph: who asks for gradients through them is told so, and gets the same result."""
+    gen = generator(23)
+    t = tokens_of(gen, 20, 6).cuda()
+    w, x, q = normal(gen, 6, 16).cuda(), normal(gen, 20, 16).cuda(), normal(gen, 2, 5, 2, 16).cuda()
+    one = torch.ones(16).cuda()
+    calls = [(lambda a: seq.embed(t, a), w), (lambda a: seq.layer_norm(a, one)[0], x),
+             (lambda a: seq.layer_norm(x, a)[0], one), (lambda a: seq.layer_norm(x, one, a)[0], one),
+             (lambda a: seq.cross_attention(a, q, q), q), (lambda a: seq.cross_attention(q, a, q), q),
+             (lambda a: seq.cross_attention(q, q, a), q)]
+    for call, a in calls:
+        want = call(a)
+        with pytest.warns(UserWarning, match="gradient"):
+            got = call(a.clone().requires_grad_())
+        assert torch.equal(got, want) and not got.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with torch.no_grad():
+                call(a.clone().requires_grad_())
+            call(a.clone().requires_grad_().detach())
