@@ -298,14 +298,22 @@ constexpr int forward_rows(int held) { return held <= 4 ? 4 : held <= 8 ? 2 : 1;
 constexpr int backward_rows(int held) { return held <= 4 ? 2 : 1; }
 
 constexpr int kMaxNormDim = 16384;
+constexpr int most_accesses(int v, int lanes) {  // K * V <= 32 floats of a row a lane
+  return lanes == 16 ? 1 : std::min(16, 32 / v);
+}
+
+// Whether row_plan takes this form for any row length.
+constexpr bool row_form(int v, int lanes, int k) {
+  const int fewer_lanes = lanes > 16 ? lanes / 4 * most_accesses(v, lanes / 4) : 0, fewer = k > 1 ? lanes * k / 2 : 0;
+  return k <= most_accesses(v, lanes) && std::max(fewer_lanes, fewer) < std::min(lanes * k, kMaxNormDim / v);
+}
 
 bool row_plan(int dim, int v, RowPlan* p) {
   const int acc = (dim + v - 1) / v;
-  const int most = std::min(16, 32 / v);  // K * V <= 32 floats of a row a lane
   p->v = v;
   p->threads = 256;
   for (int l : {16, 64, 256, 1024}) {
-    for (int k = 1; k <= (l == 16 ? 1 : most); k *= 2) {
+    for (int k = 1; k <= most_accesses(v, l); k *= 2) {
       if ((int64_t)l * k < acc) continue;
       p->lanes = l;
       p->k = k;
@@ -339,7 +347,7 @@ int blocks_at_once(int threads) {
 // Returns the blocks of the launch.
 template <typename T, int V, int L, int K, int THREADS>
 int launch_norm(bool bwd, const NormArgs& a, hipStream_t s) {
-  if constexpr (K * V <= 32) {
+  if constexpr (row_form(V, L, K)) {
     auto blocks_of = [&](int64_t rows, int64_t most) { return (int)std::min<int64_t>(most, (a.m + rows - 1) / rows); };
     if (bwd) {
       constexpr int R = backward_rows(K * V);
