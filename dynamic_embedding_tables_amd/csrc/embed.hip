@@ -648,10 +648,10 @@ template <bool FIRST, int PER>
 void launch_sort(const BwdPlan& p, const SortArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)p.tiles), block(kThreads);
   hipLaunchKernelGGL((k_sort_hist<FIRST, PER>), grid, block, 0, s, a);
-  if (p.scanned) {
+  if (p.scanned || PER > 4) {  // (tiles of 4096 keys are more than 64: bwd_plan)
     hipLaunchKernelGGL(k_sort_scan, dim3((a.digits + kScanDigits - 1) / kScanDigits), block, 0, s, a);
     hipLaunchKernelGGL((k_sort_scatter<FIRST, PER, true>), grid, block, 0, s, a);
-  } else {
+  } else if constexpr (PER == 4) {
     hipLaunchKernelGGL((k_sort_scatter<FIRST, PER, false>), grid, block, 0, s, a);
   }
 }
