@@ -848,3 +848,75 @@ def test_inputs_that_require_a_gradient_are_warned_about(seq):
             with torch.no_grad():
                 call(a.clone().requires_grad_())
             call(a.clone().requires_grad_().detach())
+
+
+# ------------------------------------------- what only large sizes reach
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,rows,dim", [
+    (70001, 50021, 16),      # 69 tiles of 1024 keys: the counts are scanned by a kernel of their own
+    (300007, 50021, 8),      # tiles of 4096 keys
+    (262144, 300, 3), (262145, 300, 3),   # the last call of the small tiles, the first of the large
+    (5000, 4200000, 4),      # three sort passes, over a result that is stored past the caches
+    (70001, 4194303, 1), (70001, 4194304, 1), (300007, 5000000, 2),
+])
+def test_embed_backward_of_many_tokens(seq, n, rows, dim, dtype):
+    gen = generator(26, n, rows, dim)
+    t, g = tokens_of(gen, n, rows), normal(gen, n, dim, dtype=dtype)
+    t[::7] = rows // 3       # a token that fills a seventh of the call
+    t[n // 2] = rows - 1
+    got = seq.embed_backward(t.cuda(), g.cuda(), rows, scale=0.3)
+    within(got, *plain.embed_backward(t, g, rows, 0.3, dtype), what=(n, rows, dim))
+    assert torch.equal(seq.embed_backward(t.cuda(), g.cuda(), rows, scale=0.3), got), "two calls on equal inputs differ"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [128, 127])
+def test_embed_past_the_caches(seq, dim, dtype):
+    gen = generator(27, dim)
+    n = (40 << 20) // (dim * dtype.itemsize)   # 40 MiB
+    t, w = tokens_of(gen, n, 3000), normal(gen, 3000, dim, dtype=dtype)
+    want = torch.where((t >= 0)[:, None], w.float()[t.clamp_min(0)] * torch.tensor(3.7), 0).to(dtype)
+    assert torch.equal(seq.embed(t.cuda(), w.cuda(), scale=3.7).cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,dim", [
+    (1050001, 5), (33001, 1025),                       # forward: more rows than 2^14 blocks hold
+    (50001, 64), (30011, 128), (7001, 1000), (2003, 4096), (1001, 16384), (901, 8193),  # the same of the backward's
+])
+def test_layer_norm_blocks_take_turns(seq, m, dim, dtype):
+    gen = generator(28, m, dim)
+    x, g, w, b = normal(gen, m, dim, dtype=dtype), normal(gen, m, dim, dtype=dtype), normal(gen, dim), normal(gen, dim)
+    y, mean, rstd = seq.layer_norm(x.cuda(), w.cuda(), b.cuda())
+    dx, dw, db = seq.layer_norm_backward(g.cuda(), x.cuda(), mean, rstd, w.cuda())
+    want = {**plain.layer_norm(x, w, b, 1e-5, dtype), **plain.layer_norm_backward(g, x, w, 1e-5, dtype, F32)}
+    for name, got in (("y", y), ("mean", mean), ("rstd", rstd), ("dx", dx), ("dw", dw), ("db", db)):
+        within(got, *want[name], what=(name, m, dim))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [16, 15, 64, 63, 127, 128, 255, 256, 511, 512, 1023, 1024, 2047, 2048, 4095, 4096, 8191,
+                                 8192, 16383, 16384])   # every form of a row over the lanes, at its longest
+def test_layer_norm_row_forms(seq, dim, dtype):
+    gen = generator(29, dim)
+    x, g = normal(gen, 37, dim, dtype=dtype), normal(gen, 37, dim, dtype=dtype)
+    y, mean, rstd = seq.layer_norm(x.cuda())
+    within(y, *plain.layer_norm(x, None, None, 1e-5, dtype)["y"])
+    want = plain.layer_norm_backward(g, x, None, 1e-5, dtype, F32)
+    for name, got in zip(("dx", "dw", "db"), seq.layer_norm_backward(g.cuda(), x.cuda(), mean, rstd)):
+        within(got, *want[name], what=(name, dim))
+
+
+@pytest.mark.parametrize("kind", ["lens", "packed mask"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [   # batch, q_len, kv_len, q_heads, kv_heads, head_dim
+    (2, 700, 600, 2, 2, 32), (1, 1100, 300, 4, 2, 33),   # more than 2048 rows with their keys split
+    (67, 1, 300, 6, 3, 16), (67, 40, 100, 3, 3, 32),     # heads of an entry together, the last turn of the dies not full
+    (131, 150, 90, 1, 1, 24),                            # several row tiles, pairs that do not fill a turn
+    (131, 40, 330, 8, 8, 16), (131, 20, 290, 4, 4, 128), (131, 70, 200, 4, 4, 96), (131, 70, 200, 4, 4, 48),
+    (131, 1, 1000, 8, 8, 16),                            # a block walks all the keys: both tile buffers more than once
+])
+def test_cross_attention_of_many_blocks(seq, shape, dtype, kind):
+    gen = generator(*shape, len(kind), 30)
+    q, k, v, kw, kept = attn_case(gen, shape, dtype, kind)
+    check_attention(seq, q, k, v, kw, kept, grad=normal(gen, *q.shape, dtype=dtype), what=(shape, kind))
