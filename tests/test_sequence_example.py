@@ -51,3 +51,47 @@ def test_the_block_gradient_is_its_loss_difference():
             moved.append(loss())
         slope = (moved[0] - moved[1]) / (2 * h)
         assert slope == pytest.approx(float(grad[name].norm()), rel=0.15), name
+
+
+@pytest.mark.parametrize("name", ["actions", "categories"])
+def test_the_vocabulary_gradients_are_the_loss_difference(name):
+    """The two vocabularies' gradients, through layer norm and attention, along themselves against the difference
+    quotient of the same loss in 64 bits.  The block rounds some 12 times to bfloat16 on the way there and back (2^-8
+    each at most): 1/16 of the gradient's norm is more than they can move it together."""
+    import sequence_block as ex
+    block, batch = ex.Block(seed=4), ex.make_batch(16, 40, 4, 6)
+    block.forward(batch, 0)                   # the items enter the table
+    n, samples = batch["items"].numel(), 16
+    res = ex.recis.LookupResult(n, samples)
+    feature = ex.recis.DeviceFeature(batch["items"], batch["offsets"], slot=1,
+                                     ops=ex.recis.RECIS_OP_HASH | ex.recis.RECIS_OP_MOD, mod=10**8)
+    block.items.insert_find([feature], samples, res, flags=ex.recis.RECIS_FIND_ONLY)
+    rows = torch.empty(n, ex.DIM, dtype=torch.bfloat16, device="cuda")
+    block.items.forward(res, "none", rows)
+    assert bool(rows.any())
+    dense = {k: (v.bfloat16() if k in ("actions", "categories") else v).cpu().double() for k, v in block.dense.items()}
+    rows, host = rows.cpu().double(), {k: v.cpu() if isinstance(v, torch.Tensor) else v for k, v in batch.items()}
+
+    def loss(d):
+        def norm(x, w, b):
+            x = x - x.mean(-1, keepdim=True)
+            return x / (x.pow(2).mean(-1, keepdim=True) + 1e-5).sqrt() * d[w] + d[b]
+
+        hist = norm(rows + ex.DIM**0.5 * d["actions"][host["actions"]], "hist_w", "hist_b")
+        cand = norm(ex.DIM**0.5 * d["categories"][host["candidates"]], "cand_w", "cand_b")
+        total = 0.0
+        for b in range(samples):
+            kv = hist[host["offsets"][b]:host["offsets"][b + 1]].view(-1, ex.HEADS, ex.DIM // ex.HEADS).transpose(0, 1)
+            q = cand[b].view(-1, ex.HEADS, ex.DIM // ex.HEADS).transpose(0, 1)
+            s = q @ kv.transpose(1, 2) * kv.shape[-1] ** -0.5
+            out = (torch.softmax(s, -1) @ kv).transpose(0, 1) if kv.shape[1] else torch.zeros_like(q).transpose(0, 1)
+            total += 0.5 * (out - host["target"][b].double()).pow(2).sum() / samples
+        return float(total)
+
+    before = block.dense[name].clone()
+    block.items.backward_update = lambda *a, **k: None
+    block.step(batch, lr=1.0)                 # the weights move by the gradient
+    grad = (before - block.dense[name]).cpu().double()
+    way, h = grad / grad.norm(), 2.0**-8
+    slope = (loss({**dense, name: dense[name] + h * way}) - loss({**dense, name: dense[name] - h * way})) / (2 * h)
+    assert slope == pytest.approx(float(grad.norm()), rel=1 / 16)
