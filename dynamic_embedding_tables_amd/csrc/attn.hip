@@ -1218,17 +1218,13 @@ struct RowStage {
   }
 };
 
-// Packed rows before the first entry and after the last have gradient zero: a
-// part of them from every block of the head, number `block` of `blocks`.  (512
-// entries of 0 to 1000 keys, 4 heads of 32 bfloat16, 50 queries, in a buffer of
-// twice the rows in use: the backward takes 151 us, 141 without the spare rows,
-// and 7.1 ms with one block a head for all of them.)
+// Zero gradients for head h of the packed rows 0 .. lo - 1 and hi .. end - 1, a
+// part of them from block `block` of `blocks`.
 template <typename T, int DP, bool ALN>
-__device__ __forceinline__ void zero_outside(const AttnArgs& a, int h, int block, int blocks) {
+__device__ __forceinline__ void zero_rows(const AttnArgs& a, int h, long long lo, long long hi, long long end,
+                                          int block, int blocks) {
   constexpr int V = ALN ? 8 : 1, kAcross = kCols<DP> / V, kRows = kThreads / kAcross;
-  const long long lo = std::min<long long>(std::max(a.kv_offsets[0], 0), a.kv_rows);
-  const long long hi = std::min<long long>(std::max(a.kv_offsets[a.batch], 0), a.kv_rows);
-  const long long n = lo + a.kv_rows - hi;
+  const long long n = lo + end - hi;
   const int d = (int)(threadIdx.x % kAcross) * V;
   if (d >= a.head_dim) return;
   for (long long i = (long long)block * kRows + threadIdx.x / kAcross; i < n; i += (long long)blocks * kRows) {
@@ -1255,7 +1251,16 @@ __global__ __launch_bounds__(kThreads) void k_attn_bwd_kv(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = wave_of();
   const Span sp = kv_span(a, b);
   const int block_key = tile * (16 * KT * kAttnWaves);
-  if (a.kv_offsets) zero_outside<T, DP, ALN>(a, h, b * a.key_tiles + tile, a.batch * a.key_tiles);
+  // Packed rows that no entry has: before the first and after the last, by all
+  // blocks of the head (512 entries of 0 to 1000 keys, 4 heads of 32 bfloat16, 50
+  // queries, in a buffer of twice the rows in use: the backward takes 151 us, 141
+  // without the spare rows, and 7.1 ms with one block a head for all of them),
+  // and those of an entry of too many, by its own.
+  if (a.kv_offsets) {
+    auto row = [&](int i) { return std::min<long long>(std::max(a.kv_offsets[i], 0), a.kv_rows); };
+    zero_rows<T, DP, ALN>(a, h, row(0), row(a.batch), a.kv_rows, b * a.key_tiles + tile, a.batch * a.key_tiles);
+    if (sp.len == 0) zero_rows<T, DP, ALN>(a, h, 0, row(b), row(b + 1), tile, a.key_tiles);
+  }
   // padded keys past the length still get their (zero) gradient
   const int end = a.kv_offsets ? sp.len : a.kv_len;
   if (block_key >= end) return;
@@ -1421,7 +1426,7 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
   p.row_tiles = (int)((rows + 64 * p.qt - 1) / (64 * p.qt));
   p.key_tiles = std::max(1, (int)(((int64_t)d->kv_len + 64 * p.kt - 1) / (64 * p.kt)));
   // few pairs over a large packed buffer: further tiles, without keys, for its
-  // rows outside the entries (zero_outside; one entry, 2 heads of 64, 2M spare
+  // rows outside the entries (zero_rows; one entry, 2 heads of 64, 2M spare
   // rows: 232 us, 53 ms from its two blocks)
   if (d->kv_offsets && bh > 0 && bh < kBlocksForOutside)
     p.key_tiles = std::max(p.key_tiles, (int)std::min<int64_t>((kBlocksForOutside + bh - 1) / bh,

@@ -568,7 +568,8 @@ typedef struct {
                                  packed; or NULL */
   int64_t mask_stride;        /* of a batch entry in kv_mask (padded) */
   uint32_t* error;            /* a length or offset out of range records RECIS_ERR_INVALID_ARG;
-                                 its entry is then taken as empty */
+                                 its entry is then taken as empty (and where offsets decrease,
+                                 the packed gradients are unspecified) */
 } recis_attn_desc;
 
 /* Device bytes of the forward's (backward 0) or the backward's workspace; 0:

@@ -920,3 +920,28 @@ def test_cross_attention_of_many_blocks(seq, shape, dtype, kind):
     gen = generator(*shape, len(kind), 30)
     q, k, v, kw, kept = attn_case(gen, shape, dtype, kind)
     check_attention(seq, q, k, v, kw, kept, grad=normal(gen, *q.shape, dtype=dtype), what=(shape, kind))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [16, 21])
+def test_packed_entries_of_too_many_keys_get_zeros(seq, d, dtype):
+    """An entry of more than max_kv_len keys is taken as empty, in the gradients as well."""
+    gen = generator(31, d)
+    lens = [70, 300, 0, 5, 71]
+    off = torch.tensor([sum(lens[:i]) for i in range(6)], dtype=torch.int32)
+    rows = sum(lens)
+    q, grad = normal(gen, 5, 3, 4, d, dtype=dtype), normal(gen, 5, 3, 4, d, dtype=dtype)
+    k, v = normal(gen, rows, 2, d, dtype=dtype), normal(gen, rows, 2, d, dtype=dtype)
+    kw = on_gpu({"kv_offsets": off, "max_kv_len": 70, "error": torch.zeros(1, dtype=torch.int32)})
+    dev = [t.cuda() for t in (q, k, v)]
+    o, lse = seq.cross_attention(*dev, return_lse=True, **kw)
+    junk = [torch.full((rows, 2, d), math.nan, dtype=dtype, device="cuda") for _ in range(3)]
+    del junk   # what the results' memory holds before
+    got = (o, lse, *seq.cross_attention_backward(grad.cuda(), *dev, o, lse, **kw))
+    kept = [torch.arange(int(off[i]), int(off[i + 1])) if n <= 70 else torch.arange(0) for i, n in enumerate(lens)]
+    want = plain.attention(q, k, v, d**-0.5, kept, True, grad)
+    for name, t in zip(("o", "lse", "dq", "dk", "dv"), got):
+        within(t, *want[name], what=name)
+    from dynamic_embedding_tables_amd import recis
+    with pytest.raises(recis.RecisError):
+        seq.check(kw["error"])
