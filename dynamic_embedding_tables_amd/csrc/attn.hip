@@ -195,9 +195,10 @@ __device__ __forceinline__ void store4(T* row, int d0, int dim, f32x4 x) {
 // LDS tiles.  A bfloat16 tile is read by rows (8 lanes at a time take 16 bytes
 // of one column of 8 rows) and by columns (16 lanes take 32 bytes of 4 rows).
 // The 16-byte chunks of a row are exchanged by a number that differs over any
-// 8 rows, and in its upper bits over any aligned 4, so both use distinct banks
-// without padding.  (Rows padded by 16 bytes took the same time, and an eighth
-// more LDS; the counted conflicts, 4 cycles a column read, were the same too.)
+// 8 rows, and in its upper bits over any aligned 4, which spreads both over the
+// banks without padding.  The column reads still count 4 conflict cycles each,
+// 40% of the LDS cycles of the training kernels.  (Rows padded by 16 bytes took
+// the same time, with the same conflicts and an eighth more LDS.)
 // Float32 rows are padded by 16 bytes.
 template <int DP>
 constexpr int kCols = DP == 48 ? 64 : DP == 96 ? 128 : DP;  // columns that threads stage
@@ -309,14 +310,19 @@ __device__ __forceinline__ bool no_key(unsigned long long bits) {
 // Consecutive blocks go to the eight dies in turn; `unit` (batch entry, key
 // head) pairs, all blocks of each, share a die and its L2.
 //  - Where the keys are read once (one row tile), all heads of an entry: its
-//    positions' memory is then read by one die, in one stretch (64 entries of
-//    up to 8192 keys, 4 heads of 128: 112 us against 122), and heads shorter
-//    than a 128-byte line are not fetched once per die (512 entries, 4 heads
-//    of 32: 35 us against 47).
+//    positions' memory is then read by one die, in one stretch (single queries,
+//    up to 8192 keys, 4 heads of 128 bfloat16: 64 entries 116 us against 126,
+//    128 232 against 256), and heads shorter than a 128-byte line are not
+//    fetched once per die (50 queries, up to 1000 keys, 4 heads of 32: 512
+//    entries 29 us against 46).  Below 64 entries both take the same time
+//    within 5% (16: 40.3 and 40.4, 48: 89 and 91; 11.0 and 11.0 with 32).
 //  - Where there is more to compute than to read, one pair, so that entries of
-//    unequal length spread over the dies.
-//  - With few pairs that would leave dies idle, and a pair's blocks go to every
-//    die (9 entries of 0 to 1499 keys, 2 heads: 25 us against 31).
+//    unequal length spread over the dies (512 queries, up to 1000 keys, 8 heads
+//    of 64 bfloat16, both passes: 512 pairs 271 us against 303, 256 156 against
+//    169, 128 149 against 151).
+//  - With few pairs that leaves dies idle, and a pair's blocks go to every die
+//    (the same: 16 pairs 64 us against 69, 32 91 against 97, 64 112 against
+//    114; 96 123 against 122).
 constexpr int kDies = 8, kEntriesForDies = 64, kPairsForDies = 128;
 __device__ __forceinline__ bool place(const AttnArgs& a, int per, int* b, int* h, int* t) {
   const int id = block_id(), slot = id / a.dies, across = per * a.unit;
@@ -407,10 +413,11 @@ constexpr int kTileKeys = sizeof(T) == 4 && DP > 64 ? 32 : 64;
 constexpr int kAttnWaves = kThreads / 64;
 
 // ------------------------------------------------------------------ forward
-// Bound by instruction issue: a 16 x 16 tile of scores takes 4 matrix
+// Bound by vector instructions, mostly: a 16 x 16 tile of scores takes 4 matrix
 // instructions (head 64) of 16 cycles, and per lane 4 scores' multiply-add,
-// exponential (4 issue slots), sum and maximum; issue slots are 97% taken, the
-// matrix unit 26%.  128 entries, 512 queries, 8 heads of 64, 0 to 1000 keys,
+// exponential (at a quarter of the rate), sum and maximum.  Vector instructions
+// take 58% of the SIMDs' busy cycles and the exponentials' rate some 20% more,
+// the matrix unit 26%.  128 entries, 512 queries, 8 heads of 64, 0 to 1000 keys,
 // bfloat16: 150 us, 447 TFLOP/s of the keys that count (32 queries a wave, 2
 // tiles; 16: 182 us).  50 queries, 4 heads of 32, 512 entries: 35 us, 144 MB of
 // unavoidable traffic at 4.1 TB/s.
@@ -1139,8 +1146,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_q(AttnArgs a) {
   for (int i = 0; i < V; ++i) out[i] = (T)(sum[i] * a.scale);
 }
 
-// Four products; 300 us for the case above, 134 GFLOP: 447 TFLOP/s.  64% of the
-// issue slots are taken and 28% of the matrix unit; it is the products that cost
+// Four products; 300 us for the case above, 134 GFLOP: 447 TFLOP/s.  Vector
+// instructions take 47% of the SIMDs' busy cycles (the exponentials' rate
+// included), the matrix unit 28%: its two waves wait for their own results.  It
+// is the products that cost
 // (without the last two 220 us, without the exponentials 290, without reading
 // the rows 280).  32 keys a wave, or 16 at four waves a SIMD: 305 and 318 us; 32
 // rows a tile instead of 64: 314.  dQ has a kernel of its own (S and dP are
@@ -1421,6 +1430,11 @@ AttnPlan attn_plan(const recis_attn_desc* d) {
   p.dp = d->head_dim <= 32 ? 32 : f32 && d->head_dim <= 48 ? 48 : d->head_dim <= 64 ? 64 : d->head_dim <= 96 ? 96 : 128;
   const int group = d->q_heads / d->kv_heads;
   const int64_t rows = (int64_t)d->q_len * group, bh = (int64_t)d->batch * d->kv_heads;
+  // Two tiles a wave at head sizes to 64.  Above, they take a backward wave past
+  // 256 registers, so that one runs a SIMD (128 entries, 512 queries, up to 1000
+  // keys, 8 heads of 128: 1128 us against 981), and small forward calls have
+  // half the blocks (16 entries: 86 us against 51); large forward calls would
+  // gain (226 against 316) and would need a rule of their own.
   p.qt = rows > 64 && d->dtype == RECIS_DTYPE_BF16 && p.dp <= 64 ? 2 : 1;
   p.kt = d->dtype == RECIS_DTYPE_BF16 && p.dp <= 64 ? 2 : 1;
   p.row_tiles = (int)((rows + 64 * p.qt - 1) / (64 * p.qt));

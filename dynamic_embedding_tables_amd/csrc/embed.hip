@@ -269,7 +269,7 @@ __global__ __launch_bounds__(kThreads) void k_sort_scatter(SortArgs a) {
 
 // ------------------------------------------------------------------ the sums
 // Bound by memory where there is much: 2.05M gradient rows of 128 bfloat16 and
-// 1M rows of result, 780 MB in 178 us, 4.4 TB/s (a large copy: 4.8).  By its
+// 1M rows of result, 780 MB in 175 us, 4.5 TB/s (a large copy: 4.8).  By its
 // chain of dependent reads where there is little: 20011 tokens on 50021 rows of
 // 64 float32, 18 MB in 12 us (8 units a group; 4: 14 us, 16: 15 us).
 //

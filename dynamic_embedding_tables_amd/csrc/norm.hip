@@ -11,8 +11,14 @@
 // Bound by memory.  2.05M rows of 128 bfloat16: forward 1.05 GB in 180 us, 5.8
 // TB/s, backward 1.57 GB in 296 us, 5.3 TB/s (above a large copy's 4.8: part of
 // the rows is still in the memory-side cache from the pass before).  12289 rows
-// of 777 float32, whose rows allow no wider access than 4 bytes: 16.6 and 21.5
-// us, 4.6 and 5.3 TB/s, and 4.6 us to add up the blocks' weight gradients.
+// of 777 float32, whose rows allow no wider access than 4 bytes: 16.4 and 21.7
+// us, 4.6 and 5.3 TB/s, and 4.5 us to add up the blocks' weight gradients.
+// Bfloat16 rows that allow no 16-byte access are read and written by single
+// elements, and bound by the number of accesses: 2.05M rows of 100, 516 and 755
+// us, 1.6 TB/s.  Above 8192 elements a row takes 1024 lanes, whose 128 registers
+// do not hold all of the backward's values: 8 to 62 words a lane go through
+// scratch memory (10000 rows of 16384 float32: forward 241 us, 5.4 TB/s,
+// backward 385, 5.1; of 16383: 269 and 731).
 #include <algorithm>
 
 #include "seq.h"

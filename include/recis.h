@@ -505,8 +505,8 @@ recis_status recis_embed_fwd(const int64_t* tokens, int64_t n, const void* weigh
 
 /* Its gradient: grad_weight[v] = scale * sum of grad_out[i] over tokens[i] = v,
  * every row written (zeros where no token fell), summed in float32 in the
- * order of the tokens sorted by value, equal tokens by place, and rounded once to
- * weight_dtype.  Tokens outside [0, rows) add nothing; one >= rows records
+ * order of the tokens sorted by value, equal tokens by place (in parts that are
+ * joined in order), and rounded once to weight_dtype.  Tokens outside [0, rows) add nothing; one >= rows records
  * RECIS_ERR_KEY_RANGE.  The limits of n, rows and dim as above. */
 int64_t recis_embed_bwd_workspace_bytes(int64_t n, int64_t rows, int32_t dim);
 recis_status recis_embed_bwd(const int64_t* tokens, int64_t n, const void* grad_out, int32_t grad_dtype,
