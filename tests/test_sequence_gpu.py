@@ -945,3 +945,33 @@ def test_packed_entries_of_too_many_keys_get_zeros(seq, d, dtype):
     from dynamic_embedding_tables_amd import recis
     with pytest.raises(recis.RecisError):
         seq.check(kw["error"])
+
+
+def test_a_masked_backward_captured_into_a_graph(seq):
+    """Masks that leave few keys in one replay and many in the next, in a packed buffer partly in use."""
+    gen = generator(32)
+    q, grad = normal(gen, 4, 20, 4, 64, dtype=BF16).cuda(), normal(gen, 4, 20, 4, 64, dtype=BF16).cuda()
+    k, v = normal(gen, 3000, 2, 64, dtype=BF16).cuda(), normal(gen, 3000, 2, 64, dtype=BF16).cuda()
+    off, mask = torch.tensor([0, 600, 600, 1200, 1500], dtype=torch.int32).cuda(), torch.ones(3000, dtype=torch.bool).cuda()
+
+    def step():
+        kw = {"kv_offsets": off, "kv_mask": mask, "max_kv_len": 700}
+        o, lse = seq.cross_attention(q, k, v, return_lse=True, **kw)
+        return [o, lse, *seq.cross_attention_backward(grad, q, k, v, o, lse, **kw)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for i, share in enumerate((0.02, 0.9, 0.1, 0.0, 1.0)):
+        mask.copy_(torch.rand(3000, generator=gen) < share)
+        off.copy_(torch.tensor([5 * i, 600, 650 + i, 1200, 1900 - 100 * i], dtype=torch.int32))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, held):
+            assert torch.equal(a, b), share
