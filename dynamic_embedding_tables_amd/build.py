@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librecis.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-SOURCES = ["table.hip", "lookup.hip", "fwd_bwd.hip", "maint.hip", "embed.hip", "norm.hip", "attn.hip"]
+SOURCES = ["table.hip", "lookup.hip", "fwd_bwd.hip", "maint.hip", "embed.hip", "norm.hip", "attn.hip",
+           "rotary.hip", "paged.hip", "band_fwd.hip"]
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
     # packed fp32 instructions stay off: hipcc must not form v_pk_* fp32 ops
@@ -21,11 +22,12 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 
-# Per source.  attn.hip: matrix instructions take their accumulators in vector
+# Per source.  Attention: matrix instructions take their accumulators in vector
 # registers, where the softmax reads and scales them; by default a quarter of
 # the inner loops' instructions moved them to and from the accumulation
 # registers (both are one file on gfx950).
-EXTRA_FLAGS = {"attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+_MFMA_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA_FLAGS = {src: _MFMA_IN_VGPRS for src in ("attn.hip", "paged.hip", "band_fwd.hip")}
 
 
 def _compile(src: str) -> str:
@@ -39,7 +41,7 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(4, os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp]

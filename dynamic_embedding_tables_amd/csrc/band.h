@@ -1,0 +1,382 @@
+// band.h -- attention of a sequence to its own past: what the kernels for it share
+// (band_fwd.hip, band_bwd.hip over strided or packed keys, paged.hip over a paged
+// cache).
+//
+// The query at position p sees the keys j <= p with p - j < window or j < sinks
+// (and mask[j] != 0).  The q_heads / kv_heads query heads that share a key head are
+// folded into the rows of a pair (batch entry, key head): row = query * group + g.
+//
+// Matrix products are 32x32: an operand holds, per lane, 8 consecutive k of one row
+// (lane % 32), k from 8 * (lane / 32); a result holds column lane % 32 and rows
+// 8 * (i / 4) + 4 * (lane / 32) + i % 4 for i = 0 .. 15.  Scores are computed with
+// the side that is reduced over as rows, so two of a result's quarters are, after
+// rounding, the operand of the next product over 16 of them: slot j of lane half h
+// is row 4 h + j for j < 4, and 8 + 4 h + j - 4 above, and the other operand is read
+// in that order.
+#pragma once
+
+#include "attn.h"
+
+namespace recis {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct BandArgs {
+  const void *q, *k, *v, *o, *dout;
+  void *out, *dq, *dk, *dv;
+  float* lse;
+  const int* offsets;          // of packed queries (and, without pages, of the keys); or null
+  const int* lens;             // keys an entry has; or null
+  const int* table;            // paged: [batch][width] pages
+  const unsigned char* kv_mask;
+  unsigned* error;
+  long long mask_stride, total_rows, table_stride, pages;
+  long long qs[3], os[3], dos[3], dqs[3];      // batch, position, head
+  long long ks[3], vs[3], dks[3], dvs[3];      // the same, or page, slot, head
+  int batch, q_len, q_heads, kv_heads, group, head_dim;
+  int max_len;                 // most keys an entry has
+  int rows;                    // most rows a pair has: q_len * group
+  int causal, window, sinks;   // window: more than any length where there is none
+  int page_size, page_mul, page_shift;
+  int row_tiles, key_tiles, splits, q_splits, kv_splits, sink_tiles, sink_splits;
+  int dies, unit;              // `unit` pairs share a die, `dies` units lie side by side
+  float scale;
+  float *part_o, *part_ml;     // parts of key ranges: [pair][split][rows][head_dim], [..][2]
+  float* part_kv;              // parts of row ranges: [pair][slot][keys][2][dp]
+  f32x2* stats;                // [pair][rows]: L and delta, from dQ's kernel to dK and dV's
+};
+
+// Sizes a launch of one of the many-row kernels needs (band_fwd.hip, band_bwd.hip).
+constexpr int kBandWaves = 4, kBandRows = 32 * kBandWaves;
+constexpr int kLeastTiles = 2;      // tiles of keys a split has where there are so many
+inline int band_dp(int head_dim) { return (head_dim + 31) / 32 * 32; }
+inline int band_keys(int dtype, int head_dim) { return dtype == RECIS_DTYPE_F32 && head_dim > 64 ? 32 : 64; }
+inline dim3 band_grid(const BandArgs& a, int64_t per) {
+  return grid_of(round_up((int64_t)a.batch * a.kv_heads, (int64_t)a.dies * a.unit) * per);
+}
+void launch_band_fwd(int dtype, bool paged, bool aln, const BandArgs& a, hipStream_t s);
+
+namespace {
+
+// x / page_size for 0 <= x < 2^31.
+__device__ __forceinline__ int page_of(const BandArgs& a, int key) {
+  return a.page_size == 1 ? key : (int)(__umulhi((unsigned)key, (unsigned)a.page_mul) >> a.page_shift);
+}
+
+// --------------------------------------------------------------- an entry
+struct Entry {
+  long long row0;  // first packed row
+  int n;           // queries whose results are written
+  int len;         // keys
+  int step, shift; // position of query q: q * step + shift; not causal: the last key's, for all
+};
+
+template <bool PAGED>
+__device__ __forceinline__ Entry entry_at(const BandArgs& a, int b, bool tell = true) {
+  long long lo = 0, hi = a.q_len;
+  bool bad = false;
+  if (a.offsets) {
+    lo = a.offsets[b], hi = a.offsets[b + 1];
+    bad = lo < 0 || hi < lo || hi > a.total_rows || hi - lo > a.q_len;
+    if (bad) lo = hi = 0;
+  }
+  const int n = (int)(hi - lo);
+  int len = PAGED || !a.offsets ? a.max_len : n;
+  if (a.lens) {
+    len = a.lens[b];
+    if (len < 0 || len > a.max_len) {
+      bad = true;
+      len = 0;
+    }
+  }
+  if (bad && tell && a.error && threadIdx.x == 0) atomicOr(a.error, kErrInvalid);
+  const int causal = a.causal ? 1 : 0;
+  return Entry{lo, n, len, causal, causal ? (PAGED ? len - n : 0) : len - 1};
+}
+
+// Position of a query: below 0 it sees nothing (rows past the length among them).
+__device__ __forceinline__ int position(const BandArgs& a, Entry e, int query) {
+  const int p = query * e.step + e.shift;
+  return p < e.len ? p : -1;
+}
+
+// Positions of the rows row0 .. row1 of a pair, rows of the entry at most: the
+// lowest and the highest that see a key (high < low: none does).
+struct Reach {
+  int low, high;
+};
+__device__ __forceinline__ Reach reach_of(const BandArgs& a, Entry e, int row0, int row1) {
+  const int last = std::min(std::min(row1 / a.group, e.n - 1) * e.step + e.shift, e.len - 1);
+  return Reach{row0 / a.group * e.step + e.shift, last};
+}
+
+// The tiles of K keys that rows of a reach see, in order: tiles of sinks that lie
+// before the window, then the window's.
+struct Walk {
+  int sink_tiles, first, n;
+  __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : first + i - sink_tiles; }
+};
+template <int K>
+__device__ __forceinline__ Walk walk_of(const BandArgs& a, Reach r) {
+  Walk w{0, 0, 0};
+  if (r.high < r.low || r.high < 0) return w;
+  const int lo = std::max(0, r.low - a.window + 1);
+  w.sink_tiles = (std::min(a.sinks, lo) + K - 1) / K;
+  w.first = std::max(w.sink_tiles, lo / K);
+  w.n = w.sink_tiles + std::max(0, r.high / K - w.first + 1);
+  return w;
+}
+// Every row of the reach sees every one of K keys from `first`.
+template <int K>
+__device__ __forceinline__ bool all_seen(const BandArgs& a, Reach r, int first) {
+  return first + K - 1 <= r.low && (first > r.high - a.window || first + K <= a.sinks);
+}
+__device__ __forceinline__ bool seen(const BandArgs& a, int p, int key) {
+  return key <= p && (p - key < a.window || key < a.sinks);
+}
+
+// Bits of the keys first .. first + 63 that the row at position p sees.
+__device__ __forceinline__ unsigned long long seen_bits(const BandArgs& a, int p, int first) {
+  const int hi = p - first, lo = hi - a.window + 1, sinks = a.sinks - first;
+  const unsigned long long upto = hi < 0 ? 0 : hi >= 63 ? ~0ull : (2ull << hi) - 1;
+  const unsigned long long near = lo <= 0 ? ~0ull : lo >= 64 ? 0 : ~0ull << lo;
+  const unsigned long long sink = sinks <= 0 ? 0 : sinks >= 64 ? ~0ull : (1ull << sinks) - 1;
+  return upto & (near | sink);
+}
+
+// Split `s` of `splits` of a walk: `per` tiles, `least` where there are so many.
+__device__ __forceinline__ int split_size(int n, int splits, int least) {
+  if (splits == 1) return n > 0 ? n : 1;
+  const int per = (n + splits - 1) / splits;
+  return per > least ? per : least;
+}
+
+// Consecutive blocks go to the eight dies in turn; `unit` pairs, all `per` blocks of
+// each, share a die and its L2.
+constexpr int kDies = 8;
+__device__ __forceinline__ bool band_place(const BandArgs& a, int per, int* b, int* h, int* t) {
+  const int id = block_id(), slot = id / a.dies, across = per * a.unit, rest = slot % across;
+  const int pair = ((slot / across) * a.dies + id % a.dies) * a.unit + rest / per;
+  *t = rest % per;
+  *b = pair / a.kv_heads;
+  *h = pair % a.kv_heads;
+  return pair < a.batch * a.kv_heads;
+}
+
+// Offset of query q, head g of the group, in a tensor of queries.
+__device__ __forceinline__ long long query_at(const BandArgs& a, const long long (&st)[3], Entry e, int b,
+                                              int h, int r) {
+  const int q = r / a.group, g = r - q * a.group;
+  return (a.offsets ? e.row0 * st[1] : (long long)b * st[0]) + (long long)q * st[1] +
+         (long long)(h * a.group + g) * st[2];
+}
+__device__ __forceinline__ long long lse_at(const BandArgs& a, Entry e, int b, int h, int r) {
+  const int q = r / a.group, g = r - q * a.group;
+  return ((a.offsets ? e.row0 : (long long)b * a.q_len) + q) * a.q_heads + h * a.group + g;
+}
+
+// Offset of key head h of an entry in a tensor of keys that is not paged.
+__device__ __forceinline__ long long keys_at(const BandArgs& a, const long long (&st)[3], Entry e, int b,
+                                             int h) {
+  return (a.offsets ? e.row0 * st[1] : (long long)b * st[0]) + (long long)h * st[2];
+}
+
+// Bit i: key first + i is there and not masked (not paged).
+__device__ __forceinline__ unsigned long long band_bits(const BandArgs& a, Entry e, int b, int first,
+                                                        int lane) {
+  const int key = first + lane;
+  bool in = key < e.len;
+  if (in && a.kv_mask) in = a.kv_mask[(a.offsets ? e.row0 : (long long)b * a.mask_stride) + key] != 0;
+  return __ballot(in);
+}
+
+constexpr float kSlack = 8.f;
+template <typename T, int DP>
+constexpr int kBandKeys = sizeof(T) == 4 && DP > 64 ? 32 : 64;
+
+// ------------------------------------------------------------ 32x32 products
+__device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(f32x8 a, f32x8 b, f32x16 c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+__device__ __forceinline__ f32x16 zeros16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+// Row (of 32) that element i of a lane's result is.
+__device__ __forceinline__ int result_row(int lane, int i) { return 8 * (i / 4) + 4 * (lane >> 5) + i % 4; }
+
+__device__ __forceinline__ float halves_max(float x) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float halves_add(float x) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Half G of a result (its rows 16 G .. 16 G + 15) as the next product's operand.
+template <typename T, int G>
+__device__ __forceinline__ Frag<T> half_of(const f32x16& x) {
+  const f32x8 y = G == 0 ? __builtin_shufflevector(x, x, 0, 1, 2, 3, 4, 5, 6, 7)
+                         : __builtin_shufflevector(x, x, 8, 9, 10, 11, 12, 13, 14, 15);
+  return __builtin_convertvector(y, Frag<T>);
+}
+
+// A lane's operand for chunk c (16 elements) of a row of `dim`.
+template <typename T, bool ALN>
+__device__ __forceinline__ Frag<T> load_head16(const T* row, int c, int lane, int dim, bool in) {
+  return load8<T, ALN>(row, c * 16 + (lane >> 5) * 8, dim, in);
+}
+
+// The same for rows row0 .. row0 + 31 of a tile in LDS.
+template <int DP>
+__device__ __forceinline__ bf16x8 rows32(const __bf16* tile, int row0, int c, int lane) {
+  return *reinterpret_cast<const bf16x8*>(tile + row0 * kLd<__bf16, DP> +
+                                          chunk_at<__bf16, DP>(lane & 31, c * 2 + (lane >> 5)));
+}
+template <int DP>
+__device__ __forceinline__ f32x8 rows32(const float* tile, int row0, int c, int lane) {
+  const float* p = tile + (row0 + (lane & 31)) * kLd<float, DP> + c * 16 + (lane >> 5) * 8;
+  const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Column c0 + lane % 32 of the 16 rows from row0, in half_of()'s order.
+template <int DP>
+__device__ __forceinline__ bf16x8 cols32(const __bf16* tile, int row0, int c0, int lane) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const int row = (lane >> 5) * 4 + ((lane & 15) >> 2);
+  const __bf16* p = tile + row0 * kLd<__bf16, DP> +
+                    chunk_at<__bf16, DP>(row, c0 / 8 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) + (lane & 1) * 4;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * kLd<__bf16, DP>));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int DP>
+__device__ __forceinline__ f32x8 cols32(const float* tile, int row0, int c0, int lane) {
+  const float* p = tile + (row0 + (lane >> 5) * 4) * kLd<float, DP> + c0 + (lane & 31);
+  f32x8 x;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = p[(j < 4 ? j : j + 4) * kLd<float, DP>];
+  return x;
+}
+
+// -------------------------------------------------------------------- joins
+// Joins the key ranges of a row, V elements a thread; rows of one range are done.
+template <typename T, int V, bool PAGED, int K, int ROWS, int LEAST>
+__global__ __launch_bounds__(kThreads) void k_band_join(BandArgs a) {
+  const unsigned per_row = a.head_dim / V;
+  const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned row = id / per_row, d = (id - row * per_row) * V;
+  const unsigned pair = row / a.rows, r = row - pair * a.rows;
+  if (pair >= (unsigned)(a.batch * a.kv_heads)) return;
+  const int h = (int)pair % a.kv_heads, b = (int)pair / a.kv_heads;
+  const Entry e = entry_at<PAGED>(a, b, false);
+  if ((int)r >= e.n * a.group) return;
+  const int tile_row = r / ROWS * ROWS;
+  const int n = walk_of<K>(a, reach_of(a, e, tile_row, tile_row + ROWS - 1)).n, per = split_size(n, a.splits, LEAST);
+  if (n <= per) return;
+  const int used = (n + per - 1) / per;
+  const long long at = (long long)pair * a.splits * a.rows + r;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.part_ml);
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < used; ++s) top = fmaxf(top, ml[at + (long long)s * a.rows][0]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float o[V] = {}, l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < used; ++s) {
+    const long long p = at + (long long)s * a.rows;
+    const f32x2 x = ml[p];
+    const float weight = __builtin_amdgcn_exp2f(x[0] - ref);
+    l += weight * x[1];
+    float v[V];
+    load_f32<float, V>(a.part_o + p * a.head_dim + d, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] += weight * v[i];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(a.out) + query_at(a, a.os, e, b, h, r) + d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = (T)(o[i] * inv);
+  if (a.lse && d == 0) a.lse[lse_at(a, e, b, h, r)] = l == 0.f ? -INFINITY : top * kLn2 + __logf(l);
+}
+
+// The same for few rows and many ranges: a block a row, consecutive ranges for each
+// wave.
+template <typename T, bool PAGED, int K, int ROWS, int LEAST>
+__global__ __launch_bounds__(kThreads) void k_band_join_few(BandArgs a) {
+  constexpr int kParts = kMaxHeadDim / 64;
+  __shared__ float part[kBandWaves][kMaxHeadDim + 1];
+  const int lane = threadIdx.x & 63, wave = wave_of();
+  const int r = (int)(blockIdx.x % a.rows), pair = (int)(blockIdx.x / a.rows);
+  const int h = pair % a.kv_heads, b = pair / a.kv_heads;
+  const Entry e = entry_at<PAGED>(a, b, false);
+  if (r >= e.n * a.group) return;
+  const int tile_row = r / ROWS * ROWS;
+  const int n = walk_of<K>(a, reach_of(a, e, tile_row, tile_row + ROWS - 1)).n, per = split_size(n, a.splits, LEAST);
+  if (n <= per) return;
+  const int used = (n + per - 1) / per;
+  const long long at = (long long)pair * a.splits * a.rows + r;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.part_ml);
+  float top = -INFINITY, o[kParts] = {}, l = 0.f;
+  for (int s = lane; s < used; s += 64) top = fmaxf(top, ml[at + (long long)s * a.rows][0]);
+  top = group_max(top);
+#pragma unroll
+  for (int k = 1; k < 16; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+  const float ref = top == -INFINITY ? 0.f : top;
+  const int mine = (used + kBandWaves - 1) / kBandWaves, s1 = std::min(used, (wave + 1) * mine);
+#pragma unroll 4
+  for (int s = wave * mine; s < s1; ++s) {
+    const long long p = at + (long long)s * a.rows;
+    const f32x2 x = ml[p];
+    const float weight = __builtin_amdgcn_exp2f(x[0] - ref);
+    l += weight * x[1];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      if (lane + 64 * i < a.head_dim) o[i] += weight * a.part_o[p * a.head_dim + lane + 64 * i];
+  }
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) part[wave][lane + 64 * i] = o[i];
+  if (lane == 0) part[wave][kMaxHeadDim] = l;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int k = 1; k < kBandWaves; ++k) {
+    l += part[k][kMaxHeadDim];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) o[i] += part[k][lane + 64 * i];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(a.out) + query_at(a, a.os, e, b, h, r);
+#pragma unroll
+  for (int i = 0; i < kParts; ++i)
+    if (lane + 64 * i < a.head_dim) out[lane + 64 * i] = (T)(o[i] * inv);
+  if (a.lse && lane == 0) a.lse[lse_at(a, e, b, h, r)] = l == 0.f ? -INFINITY : top * kLn2 + __logf(l);
+}
+
+// A block a row where the rows alone do not fill the chip.
+template <typename T, bool PAGED, int K, int ROWS, int LEAST>
+void launch_join(const BandArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.batch * a.kv_heads * a.rows;
+  const int v = a.head_dim % 4 ? 1 : 4;
+  const int64_t threads = rows * (a.head_dim / v);
+  const dim3 blocks((unsigned)((threads + kThreads - 1) / kThreads));
+  if (rows <= 2048)
+    hipLaunchKernelGGL((k_band_join_few<T, PAGED, K, ROWS, LEAST>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
+  else if (v == 4)
+    hipLaunchKernelGGL((k_band_join<T, 4, PAGED, K, ROWS, LEAST>), blocks, dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_band_join<T, 1, PAGED, K, ROWS, LEAST>), blocks, dim3(kThreads), 0, s, a);
+}
+
+}  // namespace
+}  // namespace recis

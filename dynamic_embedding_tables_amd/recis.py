@@ -58,6 +58,7 @@ EXPORTED_SYMBOLS = (
     "recis_embed_fwd", "recis_embed_bwd_workspace_bytes", "recis_embed_bwd",
     "recis_layernorm_fwd", "recis_layernorm_bwd_workspace_bytes", "recis_layernorm_bwd",
     "recis_cross_attn_workspace_bytes", "recis_cross_attn_fwd", "recis_cross_attn_bwd",
+    "recis_rotary", "recis_cache_append", "recis_paged_attn_workspace_bytes", "recis_paged_attn_fwd",
 )
 
 
@@ -109,6 +110,32 @@ class recis_attn_desc(C.Structure):
                 ("dk_strides", C.c_int64 * 3), ("dv_strides", C.c_int64 * 3),
                 ("kv_lens", C.c_void_p), ("kv_offsets", C.c_void_p), ("kv_rows", C.c_int64),
                 ("kv_mask", C.c_void_p), ("mask_stride", C.c_int64), ("error", C.c_void_p)]
+
+
+class recis_rotary_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32), ("rot_dim", C.c_int32),
+                ("interleaved", C.c_int32), ("amplitude", C.c_float), ("batch", C.c_int64), ("seq", C.c_int64),
+                ("freqs", C.c_void_p), ("positions", C.c_void_p), ("pos_strides", C.c_int64 * 2),
+                ("x_strides", C.c_int64 * 3), ("out_strides", C.c_int64 * 3)]
+
+
+class recis_append_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("new_len", C.c_int32), ("q_heads", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("amplitude", C.c_float), ("page_size", C.c_int32), ("table_width", C.c_int32), ("pages", C.c_int64),
+                ("table_stride", C.c_int64), ("rows", C.c_int64), ("q_strides", C.c_int64 * 3),
+                ("q_out_strides", C.c_int64 * 3), ("k_strides", C.c_int64 * 3), ("v_strides", C.c_int64 * 3),
+                ("k_cache_strides", C.c_int64 * 3), ("v_cache_strides", C.c_int64 * 3), ("freqs", C.c_void_p),
+                ("q_offsets", C.c_void_p), ("kv_lens", C.c_void_p), ("page_table", C.c_void_p), ("error", C.c_void_p)]
+
+
+class recis_paged_attn_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("q_len", C.c_int32), ("q_heads", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("causal", C.c_int32), ("window", C.c_int32),
+                ("sinks", C.c_int32), ("page_size", C.c_int32), ("table_width", C.c_int32), ("scale", C.c_float),
+                ("pages", C.c_int64), ("table_stride", C.c_int64), ("q_rows", C.c_int64), ("q_strides", C.c_int64 * 3),
+                ("o_strides", C.c_int64 * 3), ("k_strides", C.c_int64 * 3), ("v_strides", C.c_int64 * 3),
+                ("q_offsets", C.c_void_p), ("kv_lens", C.c_void_p), ("page_table", C.c_void_p), ("error", C.c_void_p)]
 
 
 class RecisError(RuntimeError):
@@ -166,8 +193,12 @@ def load_library() -> C.CDLL:
     L.recis_cross_attn_workspace_bytes.argtypes = [p, i32]  # p first: a recis_attn_desc by reference
     L.recis_cross_attn_fwd.argtypes = [p, p, p, p, p, p, p, i64, p]
     L.recis_cross_attn_bwd.argtypes = [p, p, p, p, p, p, p, p, p, p, p, i64, p]
+    L.recis_rotary.argtypes = [p, i32, p, p, p]
+    L.recis_cache_append.argtypes = [p, p, p, p, p, p, p, p]
+    L.recis_paged_attn_workspace_bytes.argtypes = [p]
+    L.recis_paged_attn_fwd.argtypes = [p, p, p, p, p, p, p, i64, p]
     for name in ("recis_embed_bwd_workspace_bytes", "recis_layernorm_bwd_workspace_bytes",
-                 "recis_cross_attn_workspace_bytes"):
+                 "recis_cross_attn_workspace_bytes", "recis_paged_attn_workspace_bytes"):
         getattr(L, name).restype = i64
     L.recis_status_string.argtypes = [i32]
     L.recis_status_string.restype = C.c_char_p
@@ -178,7 +209,8 @@ def load_library() -> C.CDLL:
                  "recis_writeback", "recis_idmap_export", "recis_idmap_import", "recis_idmap_key_ages",
                  "recis_idmap_sketch", "recis_idmap_stats", "recis_get_error",
                  "recis_embed_fwd", "recis_embed_bwd", "recis_layernorm_fwd", "recis_layernorm_bwd",
-                 "recis_cross_attn_fwd", "recis_cross_attn_bwd"):
+                 "recis_cross_attn_fwd", "recis_cross_attn_bwd",
+                 "recis_rotary", "recis_cache_append", "recis_paged_attn_fwd"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -443,6 +475,28 @@ def recis_cross_attn_bwd(desc: recis_attn_desc, grad_out, q, k, v, out, lse, gra
         C.byref(desc), grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
         grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), workspace.data_ptr(), workspace_bytes,
         _stream(stream)), "recis_cross_attn_bwd")
+
+
+def recis_rotary(desc: recis_rotary_desc, backward: bool, x, out, stream=None):
+    _check(load_library().recis_rotary(C.byref(desc), 1 if backward else 0, x.data_ptr(), out.data_ptr(),
+                                       _stream(stream)), "recis_rotary")
+
+
+def recis_cache_append(desc: recis_append_desc, q, k, v, q_out, k_cache, v_cache, stream=None):
+    _check(load_library().recis_cache_append(
+        C.byref(desc), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+        _stream(stream)), "recis_cache_append")
+
+
+def recis_paged_attn_workspace_bytes(desc: recis_paged_attn_desc) -> int:
+    return int(load_library().recis_paged_attn_workspace_bytes(C.byref(desc)))
+
+
+def recis_paged_attn_fwd(desc: recis_paged_attn_desc, q, k_cache, v_cache, out, lse, workspace, workspace_bytes: int,
+                         stream=None):
+    _check(load_library().recis_paged_attn_fwd(
+        C.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse),
+        _ptr(workspace), workspace_bytes, _stream(stream)), "recis_paged_attn_fwd")
 
 
 # --------------------------------------------------------- conveniences

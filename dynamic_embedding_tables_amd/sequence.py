@@ -1,4 +1,6 @@
-"""The sequence operators on tensors: token embedding, layer norm, cross attention.
+"""The sequence operators on tensors: token embedding, layer norm, cross attention,
+and those of a growing history: rotary positions, causal self attention, and a
+paged cache of keys and values with its append and the attention that reads it.
 
 What reads and trains the rows a table gathers.  Each function checks its
 tensors, allocates what it returns and its workspace from torch's caching
@@ -20,6 +22,7 @@ raises for what it holds.
 from __future__ import annotations
 
 import contextlib
+import math
 import warnings
 from typing import Optional
 
@@ -342,3 +345,248 @@ def cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens=None, kv_offse
     workspace = q.new_empty(max(nbytes, 0), dtype=torch.uint8)
     recis.recis_cross_attn_bwd(d, grad_out, q, k, v, out, lse, dq, dk, dv, workspace, nbytes)
     return dq, dk, dv
+
+
+# --------------------------------------------------------- rotary positions
+def _st(t):
+    """Strides of (batch entry, position, head) or (page, slot, head); axes of one element have none."""
+    s = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
+
+
+def _serves(name: str, *tensors):
+    """Checks of a call that serves only: it has no backward pass."""
+    _on_gpu(*tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"sequence.{name} is for serving and has no backward pass: pass detached tensors or work "
+                          "under torch.no_grad()", stacklevel=3)
+            return
+
+
+def _head_tensor(name: str, t, shape, dtype):
+    """An output or a cache given by the caller: head vectors contiguous, no element twice."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    if (t.shape[-1] > 1 and t.stride(-1) != 1) or any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+        raise ValueError(f"{name} is written in place: its head vectors must be contiguous and no axis expanded")
+    return t
+
+
+def _freqs(freqs, head_dim: int) -> int:
+    """Elements of a head that turn."""
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be contiguous float64 [rotated elements / 2]")
+    if 2 * freqs.numel() > head_dim:
+        raise ValueError(f"{freqs.numel()} pairs are more than a head of {head_dim} has")
+    return 2 * freqs.numel()
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_len: Optional[int] = None, slow: float = 1.0, fast: float = 4.0, device=None):
+    """Radians a position for the pairs of the first rot_dim elements of a head: f[i] = base ** (-2 i / rot_dim), as
+    a float64 tensor on the GPU that is made once and given to ``rotary`` and ``cache_append``.  For histories
+    longer than a model was trained on, scaling
+
+    * "linear": every f / factor;
+    * "base": base * factor ** (rot_dim / (rot_dim - 2)) in place of base, so that the first pair turns as before and
+      the last 1 / factor as fast;
+    * "parts": a pair that turns n = original_len * f / 2 pi times over the original length keeps its f where n >=
+      fast, gets f / factor where n <= slow, and in between the mean of the two with weights (n - slow) / (fast -
+      slow) and the rest."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if scaling not in ("none", "linear", "base", "parts") or not factor > 0 or not base > 0:
+        raise ValueError("scaling is 'none', 'linear', 'base' or 'parts', factor and base are above 0")
+    if scaling == "base":
+        if rot_dim <= 2:
+            raise ValueError("scaling the base takes more than one pair")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = torch.tensor([base ** (-2 * i / rot_dim) for i in range(rot_dim // 2)], dtype=torch.float64)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original_len is None or not fast > slow:
+            raise ValueError("scaling by parts takes original_len, and fast above slow")
+        keep = ((original_len * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    return f.to("cuda" if device is None else device)
+
+
+def _rotary(x, freqs, positions, interleaved, amplitude, out, backward):
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [seq, heads, head_dim] or [batch, seq, heads, head_dim]")
+    d = recis.recis_rotary_desc()
+    d.dtype = _dtype("x", x)
+    heads, head_dim = x.shape[-2:]
+    d.rot_dim = _freqs(freqs, head_dim)
+    x = _heads(x)
+    if out is None:
+        out = _like(x)
+    else:
+        _head_tensor("out", out, x.shape, x.dtype)
+    d.heads, d.head_dim = recis.int32(heads), recis.int32(head_dim)
+    d.batch, d.seq = (x.shape[0] if x.dim() == 4 else 1), x.shape[-3]
+    d.interleaved, d.amplitude = 1 if interleaved else 0, amplitude
+    if d.rot_dim:
+        d.freqs = freqs.data_ptr()
+    if positions is not None:
+        if positions.dtype != torch.int64 or tuple(positions.shape) not in (tuple(x.shape[:-2]), (d.seq,)):
+            raise ValueError(f"positions must be int64 {list(x.shape[:-2])} or [{d.seq}]")
+        d.positions = positions.data_ptr()
+        d.pos_strides[:] = positions.stride() if positions.dim() == 2 else (0, *positions.stride())
+    d.x_strides[:], d.out_strides[:] = _st(x), _st(out)
+    if x.numel():
+        recis.recis_rotary(d, backward, x, out)
+    return out
+
+
+def rotary(x, freqs, positions=None, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """Rotary positions of heads x [seq, heads, head_dim] or [batch, seq, heads, head_dim]: pair i of each head turned
+    by positions * freqs[i], the elements past 2 * len(freqs) copied.  Pairs are (i, i + len(freqs)), or (2i, 2i + 1)
+    interleaved.  positions: int64 over x's leading axes or [seq] (default: 0 .. seq - 1); freqs: float64, as
+    ``rotary_frequencies`` makes them; amplitude multiplies what is turned.  out may be x."""
+    if stream is not None:
+        with _on(stream, x, freqs, positions, out):
+            return rotary(x, freqs, positions, interleaved, amplitude, out)
+    _forward_of("rotary", x, freqs, positions, out)
+    return _rotary(x, freqs, positions, interleaved, amplitude, out, False)
+
+
+def rotary_backward(grad_out, freqs, positions=None, interleaved: bool = False, amplitude: float = 1.0, out=None,
+                    stream=None):
+    """The gradient of rotary's x: grad_out turned back.  Arguments as there; out may be grad_out."""
+    if stream is not None:
+        with _on(stream, grad_out, freqs, positions, out):
+            return rotary_backward(grad_out, freqs, positions, interleaved, amplitude, out)
+    _on_gpu(grad_out, freqs, positions, out)
+    return _rotary(grad_out, freqs, positions, interleaved, amplitude, out, True)
+
+
+# -------------------------------------------------------------- paged cache
+def _paged(d, k_cache, v_cache, page_table, kv_lens, q_offsets, batch, rows, error):
+    """What both calls on a cache check and describe alike; returns what has to stay."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be [pages, page_size, kv_heads, head_dim] of one type")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError(f"page_table must be int32 [{batch}, pages an entry may have]")
+    keep = [page_table if page_table.shape[1] <= 1 or page_table.stride(1) == 1 else page_table.contiguous(),
+            _index("kv_lens", kv_lens, torch.int32, (batch,))]
+    d.batch = recis.int32(batch)
+    d.page_size, d.pages = recis.int32(k_cache.shape[1]), k_cache.shape[0]
+    d.table_width = recis.int32(page_table.shape[1])
+    d.table_stride = keep[0].stride(0) if batch > 1 else page_table.shape[1]
+    d.page_table, d.kv_lens = keep[0].data_ptr(), keep[1].data_ptr()
+    if q_offsets is not None:
+        keep.append(_index("q_offsets", q_offsets, torch.int32, (batch + 1,)))
+        d.q_offsets = keep[-1].data_ptr()
+    if error is not None:
+        d.error = _error_word(error).data_ptr()
+    return keep
+
+
+def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, q_offsets=None, freqs=None,
+                 interleaved: bool = False, amplitude: float = 1.0, error=None, stream=None):
+    """Stores the keys and values of new events in a paged cache, in place, in one launch.
+
+    k and v [batch, new, kv_heads, head_dim], or packed [rows, kv_heads, head_dim] with q_offsets (int32 [batch + 1]:
+    entry b has rows q_offsets[b] .. q_offsets[b + 1] - 1).  k_cache and v_cache [pages, page_size, kv_heads,
+    head_dim]; page_table int32 [batch, width]: key j of entry b lies in slot j % page_size of page page_table[b, j //
+    page_size].  kv_lens int32 [batch] counts each entry's keys with the new ones, whose last is at position kv_lens[b]
+    - 1; rows that fall at negative positions are padding and are not stored (an entry of kv_lens 0 is idle).
+
+    With freqs the keys are turned by their positions on the way (``rotary``), and with q [.., q_heads, head_dim], the
+    queries of the same rows, the call returns those turned (rows of no entry zero); without q it returns None."""
+    if stream is not None:
+        with _on(stream, k, v, k_cache, v_cache, page_table, kv_lens, q, q_offsets, freqs, error):
+            return cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q, q_offsets, freqs, interleaved,
+                                amplitude, error)
+    _serves("cache_append", k, v, k_cache, v_cache, page_table, kv_lens, q, q_offsets, freqs, error)
+    if k.dim() != (4 if q_offsets is None else 3) or v.shape != k.shape:
+        raise ValueError("k and v must both be [batch, new, kv_heads, head_dim], or [rows, kv_heads, head_dim] with "
+                         "q_offsets")
+    if q is not None and (q.shape[:-2] != k.shape[:-2] or q.dim() != k.dim() or q.shape[-1] != k.shape[-1]):
+        raise ValueError("q must have k's rows and head_dim")
+    if q is not None and freqs is None:
+        raise ValueError("q is turned by its positions: it takes freqs")
+    _head_tensor("k_cache", k_cache, (*k_cache.shape[:2], *k.shape[-2:]), k.dtype)
+    _head_tensor("v_cache", v_cache, k_cache.shape, k.dtype)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k, v and the caches must be of one type")
+    d = recis.recis_append_desc()
+    d.dtype = _dtype("k", k)
+    k, v, q = _heads(k), _heads(v), None if q is None else _heads(q)
+    batch = k.shape[0] if q_offsets is None else q_offsets.numel() - 1
+    keep = _paged(d, k_cache, v_cache, page_table, kv_lens, q_offsets, batch, k.shape[0], error)
+    d.new_len, d.rows = (recis.int32(k.shape[1]), 0) if q_offsets is None else (0, k.shape[0])
+    d.kv_heads, d.head_dim = recis.int32(k.shape[-2]), recis.int32(k.shape[-1])
+    d.interleaved, d.amplitude = 1 if interleaved else 0, amplitude
+    if freqs is not None:
+        d.rot_dim = _freqs(freqs, k.shape[-1])
+        d.freqs = freqs.data_ptr() if d.rot_dim else None
+    out = None
+    if q is not None:
+        out = _like(q) if batch else torch.zeros_like(q)
+        d.q_heads = recis.int32(q.shape[-2])
+        d.q_strides[:], d.q_out_strides[:] = _st(q), _st(out)
+    d.k_strides[:], d.v_strides[:] = _st(k), _st(v)
+    d.k_cache_strides[:], d.v_cache_strides[:] = _st(k_cache), _st(v_cache)
+    recis.recis_cache_append(d, q, k, v, out, k_cache, v_cache)
+    return out
+
+
+def _band(window, sinks: int):
+    """(window, sinks) as the C ABI has them."""
+    if window is not None and window < 1:
+        raise ValueError("window counts the positions a row sees, itself among them: at least 1")
+    if sinks < 0:
+        raise ValueError("sinks must not be negative")
+    return 0 if window is None else recis.int32(window), recis.int32(sinks)
+
+
+def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, max_q_len: Optional[int] = None,
+                    causal: bool = True, window: Optional[int] = None, sinks: int = 0, scale: Optional[float] = None,
+                    return_lse: bool = False, out=None, error=None, stream=None):
+    """Attention of new events to the paged cache that ``cache_append`` fills, their own keys among it.
+
+    q [batch, new, q_heads, head_dim], or packed [rows, q_heads, head_dim] with q_offsets (int32 [batch + 1]), no entry
+    having more than max_q_len rows; q_heads is a multiple of the cache's kv_heads.  Causal, the last row of entry b is
+    at position kv_lens[b] - 1 and each row sees the keys up to its position: with window the latest `window` of them,
+    itself among them, and the first `sinks` ones.  Not causal (candidates reading a history), every row sees all
+    kv_lens[b] keys.  Returns q's shape (in out, if given) and with return_lse the float32 log of the sums of
+    exponentials [.., q_heads].  Rows that see no key, at negative positions or of an entry without keys, give zeros
+    and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf."""
+    if stream is not None:
+        with _on(stream, q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, error):
+            return paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal, window,
+                                   sinks, scale, return_lse, out, error)
+    _serves("paged_attention", q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, error)
+    packed = q_offsets is not None
+    if q.dim() != (3 if packed else 4) or packed != (max_q_len is not None):
+        raise ValueError("q must be [batch, new, q_heads, head_dim], or [rows, q_heads, head_dim] with q_offsets and "
+                         "max_q_len")
+    if k_cache.dim() != 4 or not q.dtype == k_cache.dtype or q.shape[-1] != k_cache.shape[-1]:
+        raise ValueError("q and the caches must be of one type and head_dim")
+    q, k_cache, v_cache = _heads(q), _heads(k_cache), _heads(v_cache)
+    d = recis.recis_paged_attn_desc()
+    d.dtype = _dtype("q", q)
+    batch = q_offsets.numel() - 1 if packed else q.shape[0]
+    keep = _paged(d, k_cache, v_cache, page_table, kv_lens, q_offsets, batch, q.shape[0], error)
+    d.q_len, d.q_rows = (recis.int32(max_q_len), q.shape[0]) if packed else (recis.int32(q.shape[1]), 0)
+    d.q_heads, d.kv_heads, d.head_dim = map(recis.int32, (q.shape[-2], k_cache.shape[-2], q.shape[-1]))
+    if not causal and (window is not None or sinks):
+        raise ValueError("a window takes causal rows")
+    d.causal = 1 if causal else 0
+    d.window, d.sinks = _band(window, sinks)
+    d.scale = max(q.shape[-1], 1) ** -0.5 if scale is None else scale
+    if out is None:
+        out = q.new_zeros(q.shape) if packed else _like(q)
+    else:
+        _head_tensor("out", out, q.shape, q.dtype)
+    lse = q.new_full(q.shape[:-1], -math.inf, dtype=torch.float32) if return_lse else None
+    d.q_strides[:], d.o_strides[:] = _st(q), _st(out)
+    d.k_strides[:], d.v_strides[:] = _st(k_cache), _st(v_cache)
+    nbytes = recis.recis_paged_attn_workspace_bytes(d)
+    workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
+    recis.recis_paged_attn_fwd(d, q, k_cache, v_cache, out, lse, workspace, nbytes)
+    return (out, lse) if return_lse else out

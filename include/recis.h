@@ -597,6 +597,123 @@ recis_status recis_cross_attn_bwd(const recis_attn_desc* desc, const void* grad_
                                   const void* v, const void* out, const float* lse, void* grad_q, void* grad_k,
                                   void* grad_v, void* workspace, int64_t workspace_bytes, hipStream_t s);
 
+/* ------------------------------------------------- operators of a growing history
+ * Positions, and attention of a history to its own past: whole histories for
+ * training, and new events over a cache of the keys and values of those before
+ * them for serving.  Conventions as above.  Passage: as recis_embed_fwd. */
+
+/* Rotary positions: each head's first rot_dim elements are taken as pairs --
+ * element i with i + rot_dim / 2, or 2i with 2i + 1 where interleaved -- and pair
+ * i of position p is turned by the angle t = p * freqs[i]:
+ *   (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t);
+ * the rest of the head is copied.  The angle is a product in 64 bits, reduced to
+ * one turn there; the rest is float32, rounded once to dtype.  Strides are those
+ * of (batch entry, position, head).  Limits (else UNSUPPORTED): head_dim 1024,
+ * heads * head_dim 2^18, batch * seq 2^40 and blocks 2^31 - 2^22. */
+typedef struct {
+  int32_t dtype;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t rot_dim;            /* even, 0 .. head_dim */
+  int32_t interleaved;
+  float amplitude;            /* finite */
+  int64_t batch;
+  int64_t seq;
+  const double* freqs;        /* device [rot_dim / 2]: radians a position */
+  const int64_t* positions;   /* device; NULL: the place in the sequence, 0 .. seq - 1 */
+  int64_t pos_strides[2];     /* of (batch entry, place) in positions; 0 repeats */
+  int64_t x_strides[3];
+  int64_t out_strides[3];
+} recis_rotary_desc;
+
+/* backward 0: out = the turned x.  Else x is a gradient and out that of what was
+ * turned: the same with t negative.  out may be x (with equal strides). */
+recis_status recis_rotary(const recis_rotary_desc* desc, int32_t backward, const void* x, void* out, hipStream_t s);
+
+/* A paged cache: key j of batch entry b lies in slot j % page_size of page
+ * page_table[b * table_stride + j / page_size] of k_cache and v_cache, whose
+ * strides are those of (page, slot, head).  kv_lens[b] counts the entry's keys,
+ * new ones included.  An entry's new rows are rows b * new_len (q_len) .. of a
+ * padded batch, or rows q_offsets[b] .. q_offsets[b + 1] - 1 of a packed one; the
+ * last of them is at position kv_lens[b] - 1, and rows that fall at negative
+ * positions are padding.  On the GPU, a length, offset or page out of range
+ * records RECIS_ERR_INVALID_ARG.  Limits (else UNSUPPORTED): table_width *
+ * page_size 2^30, 2^31 pages.
+ *
+ * recis_cache_append stores the new keys (turned by their positions, where
+ * rot_dim > 0: recis_rotary) and values, and, where q_heads > 0, writes the turned
+ * queries of the same rows to q_out (which may be q).  Padding rows, rows of no
+ * entry and rows whose page is out of range are not stored; rows of no entry get
+ * zeros in q_out.  Entries must not share the slots that they append to. */
+typedef struct {
+  int32_t dtype;              /* of q, k, v and the caches */
+  int32_t batch;
+  int32_t new_len;            /* padded: new rows an entry */
+  int32_t q_heads;            /* 0: no queries */
+  int32_t kv_heads;
+  int32_t head_dim;           /* 1 .. 1024, (q_heads + 2 kv_heads) * head_dim <= 2^18 (else UNSUPPORTED) */
+  int32_t rot_dim;
+  int32_t interleaved;
+  float amplitude;
+  int32_t page_size;
+  int32_t table_width;        /* pages an entry may have */
+  int64_t pages;              /* of the caches */
+  int64_t table_stride;
+  int64_t rows;               /* packed: rows of q, k and v */
+  int64_t q_strides[3];       /* (batch entry, row, head); packed: the first is not read */
+  int64_t q_out_strides[3];
+  int64_t k_strides[3];
+  int64_t v_strides[3];
+  int64_t k_cache_strides[3]; /* (page, slot, head) */
+  int64_t v_cache_strides[3];
+  const double* freqs;
+  const int32_t* q_offsets;   /* device [batch + 1], or NULL: padded */
+  const int32_t* kv_lens;     /* device [batch] */
+  const int32_t* page_table;  /* device */
+  uint32_t* error;
+} recis_append_desc;
+
+recis_status recis_cache_append(const recis_append_desc* desc, const void* q, const void* k, const void* v, void* q_out,
+                                void* k_cache, void* v_cache, hipStream_t s);
+
+/* Attention of new rows to a paged cache that holds their own keys already.
+ * Causal: the row at position p sees the keys j <= p with p - j < window (window >
+ * 0) or j < sinks; else every row sees all kv_lens[b] keys.  out and lse as
+ * recis_cross_attn_fwd, lse [rows of q, q_heads]; a row that sees no key gives 0
+ * and -infinity, rows of no entry are left as they were.  What the cache holds
+ * past an entry's length is not looked at.  A value that is not finite may reach
+ * rows of its own entry that do not see it. */
+typedef struct {
+  int32_t dtype;
+  int32_t batch;
+  int32_t q_len;              /* padded: new rows an entry; packed: the most any entry has */
+  int32_t q_heads;            /* a multiple of kv_heads */
+  int32_t kv_heads;
+  int32_t head_dim;           /* 1 .. 128 (else UNSUPPORTED) */
+  int32_t causal;
+  int32_t window;             /* 0: none; needs causal */
+  int32_t sinks;
+  int32_t page_size;
+  int32_t table_width;
+  float scale;                /* of the scores, > 0 */
+  int64_t pages;
+  int64_t table_stride;
+  int64_t q_rows;             /* packed: rows of q and out */
+  int64_t q_strides[3];       /* (batch entry, row, head); packed: the first is not read */
+  int64_t o_strides[3];
+  int64_t k_strides[3];       /* (page, slot, head) */
+  int64_t v_strides[3];
+  const int32_t* q_offsets;   /* device [batch + 1], or NULL: padded */
+  const int32_t* kv_lens;     /* device [batch] */
+  const int32_t* page_table;  /* device */
+  uint32_t* error;
+} recis_paged_attn_desc;
+
+int64_t recis_paged_attn_workspace_bytes(const recis_paged_attn_desc* desc);
+recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* desc, const void* q, const void* k_cache,
+                                  const void* v_cache, void* out, float* lse, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t s);
+
 #ifdef __cplusplus
 }
 #endif
