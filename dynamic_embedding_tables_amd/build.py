@@ -13,7 +13,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librecis.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["table.hip", "lookup.hip", "fwd_bwd.hip", "maint.hip", "embed.hip", "norm.hip", "attn.hip",
-           "rotary.hip", "paged.hip", "band_fwd.hip"]
+           "rotary.hip", "paged.hip", "band_fwd.hip", "band_bwd.hip"]
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
     # packed fp32 instructions stay off: hipcc must not form v_pk_* fp32 ops
@@ -27,7 +27,7 @@ FLAGS = [
 # the inner loops' instructions moved them to and from the accumulation
 # registers (both are one file on gfx950).
 _MFMA_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-EXTRA_FLAGS = {src: _MFMA_IN_VGPRS for src in ("attn.hip", "paged.hip", "band_fwd.hip")}
+EXTRA_FLAGS = {src: _MFMA_IN_VGPRS for src in ("attn.hip", "paged.hip", "band_fwd.hip", "band_bwd.hip")}
 
 
 def _compile(src: str) -> str:

@@ -38,11 +38,12 @@ struct BandArgs {
   int rows;                    // most rows a pair has: q_len * group
   int causal, window, sinks;   // window: more than any length where there is none
   int page_size, page_mul, page_shift;
-  int row_tiles, key_tiles, splits, q_splits, kv_splits, sink_tiles, sink_splits;
+  int row_tiles, key_tiles, splits, q_splits, kv_splits, sink_splits;
+  int part_keys, far_keys;     // keys that have parts of dK and dV, and sinks in whole blocks of 32
   int dies, unit;              // `unit` pairs share a die, `dies` units lie side by side
   float scale;
   float *part_o, *part_ml;     // parts of key ranges: [pair][split][rows][head_dim], [..][2]
-  float* part_kv;              // parts of row ranges: [pair][slot][keys][2][dp]
+  float* part_kv;              // parts of row ranges: [pair][split][part_keys][2][head_dim], then far ones
   f32x2* stats;                // [pair][rows]: L and delta, from dQ's kernel to dK and dV's
 };
 
@@ -131,6 +132,11 @@ template <int K>
 __device__ __forceinline__ bool all_seen(const BandArgs& a, Reach r, int first) {
   return first + K - 1 <= r.low && (first > r.high - a.window || first + K <= a.sinks);
 }
+// No row of the reach sees any of them.
+template <int K>
+__device__ __forceinline__ bool none_seen(const BandArgs& a, Reach r, int first) {
+  return first > r.high || (first + K - 1 <= r.low - a.window && first >= a.sinks);
+}
 __device__ __forceinline__ bool seen(const BandArgs& a, int p, int key) {
   return key <= p && (p - key < a.window || key < a.sinks);
 }
@@ -193,6 +199,30 @@ __device__ __forceinline__ unsigned long long band_bits(const BandArgs& a, Entry
 constexpr float kSlack = 8.f;
 template <typename T, int DP>
 constexpr int kBandKeys = sizeof(T) == 4 && DP > 64 ? 32 : 64;
+
+// Zeros for `heads` heads from h of the packed rows that no entry writes: those before
+// the first and after the last, a part of them from each of the head's blocks, and those
+// of an entry of too many, from its own `per` blocks (t of them).
+template <typename T>
+__device__ __forceinline__ void zero_rows(T* to, const long long (&st)[3], int h, int heads, int dim, long long lo,
+                                          long long hi, long long end, int block, int blocks) {
+  const long long per = (long long)heads * dim, n = (lo + end - hi) * per;
+  for (long long i = (long long)block * kThreads + threadIdx.x; i < n; i += (long long)blocks * kThreads) {
+    const long long at = i / per, in = i - at * per, row = at < lo ? at : hi + (at - lo);
+    to[row * st[1] + (h + in / dim) * st[2] + in % dim] = (T)0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void zero_spare(const BandArgs& a, void* to, const long long (&st)[3], int h, int heads,
+                                           int b, int t, int per) {
+  if (!a.offsets) return;
+  auto at = [&](int i) { return std::min<long long>(std::max(a.offsets[i], 0), a.total_rows); };
+  const long long first = at(0), last = at(a.batch), lo = at(b), hi = at(b + 1);
+  if (first > 0 || last < a.total_rows)
+    zero_rows(static_cast<T*>(to), st, h, heads, a.head_dim, first, std::max(first, last), a.total_rows, b * per + t,
+              a.batch * per);
+  if (hi - lo > a.q_len) zero_rows(static_cast<T*>(to), st, h, heads, a.head_dim, 0, lo, hi, t, per);
+}
 
 // ------------------------------------------------------------ 32x32 products
 __device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {

@@ -1,0 +1,771 @@
+// band_bwd.hip -- attention of a sequence to its own past: the backward pass, and the
+// host side of both passes.
+//
+//   P = exp(S - L),  dV = P^T dO,  dP = dO V^T,  delta = sum dO O,  dS = P (dP - delta)
+//   dQ = scale dS K,  dK = scale dS^T Q,  over the pairs (row, key) that see each other
+//
+// Sums are float32; with bfloat16, P and dS are rounded to bfloat16 where they enter a
+// matrix product.  dQ has a kernel of its own, which walks the keys of 128 rows; dK and
+// dV's walks the rows of 128 keys.  So S and dP are computed twice, 7 products for 5:
+// a single kernel would add up dQ over its blocks, by atomics, whose order would change
+// the result, or through memory.
+//
+// The sinks' keys are seen by all later rows, many times a window.  Their rows past the
+// window are walked by blocks of their own (FAR), split over the rows, whose four waves
+// share 32 keys; the parts are added in order at the end.
+#include <algorithm>
+#include <cmath>
+
+#include "band.h"
+
+namespace recis {
+namespace {
+
+// A tile of K keys of K and V in registers on its way to LDS (keys that are not paged).
+template <typename T, int DP, int K, bool ALN>
+struct PairStage {
+  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross;
+  static constexpr int kPer = (K + kStep - 1) / kStep;
+  Frag<T> fk[kPer], fv[kPer];
+  int row, d0;
+  __device__ __forceinline__ void start() {
+    row = threadIdx.x / kAcross;
+    d0 = (threadIdx.x % kAcross) * 8;
+  }
+  // rows whose bit is clear are zero, whatever memory holds there
+  __device__ __forceinline__ void load(const BandArgs& a, const T* kb, const T* vb, int first,
+                                       unsigned long long bits) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int in_tile = row + i * kStep;
+      const bool in = in_tile < K && (bits >> in_tile & 1);
+      fk[i] = load8<T, ALN>(kb + (long long)(first + in_tile) * a.ks[1], d0, a.head_dim, in);
+      fv[i] = load8<T, ALN>(vb + (long long)(first + in_tile) * a.vs[1], d0, a.head_dim, in);
+    }
+  }
+  __device__ __forceinline__ void store(T* tk, T* tv) const {
+    if (d0 >= DP) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (K == kPer * kStep || row + i * kStep < K) {
+        const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
+        *reinterpret_cast<Frag<T>*>(tk + at) = fk[i];
+        *reinterpret_cast<Frag<T>*>(tv + at) = fv[i];
+      }
+  }
+};
+
+// dQ, and each row's L (in log2 of the weight) and delta for dK and dV.
+template <typename T, int DP, bool ALN>
+__global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
+  constexpr int KK = DP / 16, DB = DP / 32, K = kBandKeys<T, DP>, KB = K / 32;
+  constexpr int kTile = K * kLd<T, DP>;
+  __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
+  int b, h, t;
+  if (!band_place(a, a.row_tiles * a.q_splits, &b, &h, &t)) return;
+  zero_spare<T>(a, a.dq, a.dqs, h * a.group, a.group, b, t, a.row_tiles * a.q_splits);
+  const int split = t % a.q_splits, tile = a.row_tiles - 1 - t / a.q_splits;
+  const Entry e = entry_at<false>(a, b);
+  const int tile_row = tile * kBandRows, rows = e.n * a.group;
+  if (tile_row >= rows) return;
+  const int lane = threadIdx.x & 63, wave = wave_of();
+  const Walk walk = walk_of<K>(a, reach_of(a, e, tile_row, tile_row + kBandRows - 1));
+  const int per = split_size(walk.n, a.q_splits, kLeastTiles);
+  const int i0 = split * per, i1 = std::min(walk.n, i0 + per);
+  if (split > 0 && i0 >= walk.n) return;
+  const Reach reach = reach_of(a, e, tile_row + wave * 32, tile_row + wave * 32 + 31);
+  const T* kb = static_cast<const T*>(a.k) + keys_at(a, a.ks, e, b, h);
+  const T* vb = static_cast<const T*>(a.v) + keys_at(a, a.vs, e, b, h);
+  const int r = tile_row + wave * 32 + (lane & 31);
+  const bool exists = r < rows;
+  const int p = exists ? position(a, e, r / a.group) : -1;
+  const float c2 = a.scale * kLog2e;
+  Frag<T> q[KK], g[KK];
+  float delta = 0.f;
+  {
+    const T* pq = static_cast<const T*>(a.q) + (exists ? query_at(a, a.qs, e, b, h, r) : 0);
+    const T* pg = static_cast<const T*>(a.dout) + (exists ? query_at(a, a.dos, e, b, h, r) : 0);
+    const T* po = static_cast<const T*>(a.o) + (exists ? query_at(a, a.os, e, b, h, r) : 0);
+#pragma unroll
+    for (int c = 0; c < KK; ++c) {
+      q[c] = load_head16<T, ALN>(pq, c, lane, a.head_dim, p >= 0);
+      g[c] = load_head16<T, ALN>(pg, c, lane, a.head_dim, p >= 0);
+      const Frag<T> o = load_head16<T, ALN>(po, c, lane, a.head_dim, p >= 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta += (float)g[c][i] * (float)o[i];
+    }
+    delta = halves_add(delta);
+  }
+  const float lse = p >= 0 ? a.lse[lse_at(a, e, b, h, r)] : -INFINITY;
+  const float lse2 = lse != -INFINITY ? lse * kLog2e : INFINITY;  // exp2(s - inf) = 0
+  f32x16 dq[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) dq[d] = zeros16();
+  PairStage<T, DP, K, ALN> st;
+  st.start();
+  unsigned long long bits = 0;
+  if (i0 < i1) {
+    const int first = walk.tile(i0) * K;
+    bits = band_bits(a, e, b, first, lane);
+    st.load(a, kb, vb, first, bits);
+  }
+  int buffer = 0;
+  for (int i = i0; i < i1; ++i, buffer ^= 1) {
+    const int first = walk.tile(i) * K;
+    T* tk = tiles + buffer * 2 * kTile;
+    T* tv = tk + kTile;
+    st.store(tk, tv);
+    __syncthreads();
+    const unsigned long long now = bits;
+    if (i + 1 < i1) {
+      const int next = walk.tile(i + 1) * K;
+      bits = band_bits(a, e, b, next, lane);
+      st.load(a, kb, vb, next, bits);
+    }
+    if (none_seen<K>(a, reach, first)) continue;
+    const bool whole = (K == 64 ? now == ~0ull : (unsigned)now == ~0u) && all_seen<K>(a, reach, first);
+    const unsigned long long mine = whole ? ~0ull : (seen_bits(a, p, first) & now) >> (4 * (lane >> 5));
+    // delta from out carries out's rounding, which a key with nearly all the weight
+    // sees whole: rows that see one tile of keys get it from P and dP
+    if (sizeof(T) == 2 && walk.n == 1) {
+      delta = 0.f;
+#pragma unroll
+      for (int n = 0; n < KB; ++n) {
+        f32x16 s = zeros16(), dp = zeros16();
+#pragma unroll
+        for (int c = 0; c < KK; ++c) {
+          s = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s);
+          dp = mma32(rows32<DP>(tv, n * 32, c, lane), g[c], dp);
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if ((mine >> (n * 32 + 8 * (x / 4) + x % 4)) & 1) delta += __builtin_amdgcn_exp2f(s[x] * c2 - lse2) * dp[x];
+      }
+      delta = halves_add(delta);
+    }
+#pragma unroll
+    for (int n = 0; n < KB; ++n) {
+      f32x16 s = zeros16(), dp;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) dp[x] = -delta;
+#pragma unroll
+      for (int c = 0; c < KK; ++c) {
+        s = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s);
+        dp = mma32(rows32<DP>(tv, n * 32, c, lane), g[c], dp);
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) s[x] = __builtin_amdgcn_exp2f(s[x] * c2 - lse2) * dp[x];
+      if (!whole) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (!((mine >> (n * 32 + 8 * (x / 4) + x % 4)) & 1)) s[x] = 0.f;
+      }
+      const Frag<T> d0 = half_of<T, 0>(s), d1 = half_of<T, 1>(s);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        dq[d] = mma32(cols32<DP>(tk, n * 32, d * 32, lane), d0, dq[d]);
+        dq[d] = mma32(cols32<DP>(tk, n * 32 + 16, d * 32, lane), d1, dq[d]);
+      }
+    }
+  }
+  if (!exists) return;
+  if (lane < 32 && split == 0) a.stats[((long long)b * a.kv_heads + h) * a.rows + r] = f32x2{lse2, delta};
+  if (p < 0) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) dq[d] = zeros16();
+  }
+  if (walk.n > per) {
+    float* to = a.part_o + ((((long long)b * a.kv_heads + h) * a.q_splits + split) * a.rows + r) * a.head_dim;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; x += 4)
+        store4<float, false>(to, d * 32 + result_row(lane, x), a.head_dim,
+                             f32x4{dq[d][x], dq[d][x + 1], dq[d][x + 2], dq[d][x + 3]});
+    return;
+  }
+  T* to = static_cast<T*>(a.dq) + query_at(a, a.dqs, e, b, h, r);
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int x = 0; x < 16; x += 4)
+      store4<T, ALN>(to, d * 32 + result_row(lane, x), a.head_dim,
+                     f32x4{dq[d][x] * a.scale, dq[d][x + 1] * a.scale, dq[d][x + 2] * a.scale, dq[d][x + 3] * a.scale});
+}
+
+// Adds the key ranges' parts of dQ, in order: V elements of a row a thread.
+template <typename T, int V, int K>
+__global__ __launch_bounds__(kThreads) void k_band_join_q(BandArgs a) {
+  const unsigned per_row = a.head_dim / V;
+  const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned row = id / per_row, d = (id - row * per_row) * V;
+  const unsigned pair = row / a.rows, r = row - pair * a.rows;
+  if (pair >= (unsigned)(a.batch * a.kv_heads)) return;
+  const int h = (int)pair % a.kv_heads, b = (int)pair / a.kv_heads;
+  const Entry e = entry_at<false>(a, b, false);
+  if ((int)r >= e.n * a.group) return;
+  const int tile_row = r / kBandRows * kBandRows;
+  const int n = walk_of<K>(a, reach_of(a, e, tile_row, tile_row + kBandRows - 1)).n;
+  const int per = split_size(n, a.q_splits, kLeastTiles);
+  if (n <= per) return;
+  const int used = (n + per - 1) / per;
+  const float* from = a.part_o + ((long long)pair * a.q_splits * a.rows + r) * a.head_dim + d;
+  float sum[V] = {};
+#pragma unroll 4
+  for (int s = 0; s < used; ++s) {
+    float v[V];
+    load_f32<float, V>(from + (long long)s * a.rows * a.head_dim, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] += v[i];
+  }
+  T* out = static_cast<T*>(a.dq) + query_at(a, a.dqs, e, b, h, r) + d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) out[i] = (T)(sum[i] * a.scale);
+}
+
+// ------------------------------------------------------------------ dK, dV
+// Rows of a tile: of the near walk, and of the far one, where each wave has 32 of its own.
+template <int DP, bool FAR>
+constexpr int kWalkRows = FAR ? 128 : DP <= 64 ? 64 : 32;
+
+// Walks a thread's chunks of the folded rows of Q and dO, from row `first` on.
+template <typename T, int DP, int R, bool ALN>
+struct RowStage {
+  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = (R + kStep - 1) / kStep;
+  Frag<T> fq[kPer], fg[kPer];
+  const T *pq[kPer], *pg[kPer];  // of the row that comes next
+  int head[kPer];                // its head in the group
+  int row, d0;
+  __device__ __forceinline__ void start(const BandArgs& a, Entry e, int b, int h, int first) {
+    row = threadIdx.x / kAcross;
+    d0 = (threadIdx.x % kAcross) * 8;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = first + row + i * kStep;
+      head[i] = r % a.group;
+      pq[i] = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, r);
+      pg[i] = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, r);
+    }
+  }
+  // `left` rows from the next one on exist; the others are zero
+  __device__ __forceinline__ void load(const BandArgs& a, int left) {
+    const int dq = R / a.group, dh = R % a.group;  // R rows on
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const bool in = row + i * kStep < std::min(left, R);
+      fq[i] = load8<T, ALN>(pq[i], d0, a.head_dim, in);
+      fg[i] = load8<T, ALN>(pg[i], d0, a.head_dim, in);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      pq[i] += dq * a.qs[1] + dh * a.qs[2];
+      pg[i] += dq * a.dos[1] + dh * a.dos[2];
+      if (dh) {
+        head[i] += dh;
+        if (head[i] >= a.group) {
+          head[i] -= a.group;
+          pq[i] += a.qs[1] - a.group * a.qs[2];
+          pg[i] += a.dos[1] - a.group * a.dos[2];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* tq, T* tg) const {
+    if (d0 >= DP) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (R == kPer * kStep || row + i * kStep < R) {
+        const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
+        *reinterpret_cast<Frag<T>*>(tq + at) = fq[i];
+        *reinterpret_cast<Frag<T>*>(tg + at) = fg[i];
+      }
+  }
+};
+
+constexpr int kTileKeys128 = 32 * kBandWaves;  // keys of a near block
+constexpr int kMostFarSinks = 128;             // more sinks: their tiles walk all rows themselves
+
+// Where a key's part of dK and dV lies: near parts first, [pair][split][keys], then far.
+__device__ __forceinline__ float* part_near(const BandArgs& a, long long pair, int split, int key) {
+  return a.part_kv + ((pair * a.kv_splits + split) * a.part_keys + key) * 2 * a.head_dim;
+}
+__device__ __forceinline__ float* part_far(const BandArgs& a, long long pair, int split, int key) {
+  const long long near = (long long)a.batch * a.kv_heads * a.kv_splits * a.part_keys;
+  return a.part_kv + (near + (pair * a.sink_splits + split) * a.far_keys + key) * 2 * a.head_dim;
+}
+
+template <typename T, int DP, bool ALN, bool FAR>
+__global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(BandArgs a) {
+  constexpr int KK = DP / 16, DB = DP / 32;
+  constexpr int R = kWalkRows<DP, FAR>, kTile = R * kLd<T, DP>;
+  // (the far walk's 128 rows fit once; they are staged between two barriers)
+  constexpr int kBuffers = FAR ? 1 : 2;
+  constexpr int kTileBytes = kBuffers * 2 * kTile * (int)sizeof(T);
+  constexpr int kJoinBytes = FAR ? 32 * DP * 4 : 0;
+  __shared__ __attribute__((aligned(128))) char tile_bytes[kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes];
+  T* const tiles = reinterpret_cast<T*>(tile_bytes);
+  __shared__ __attribute__((aligned(16))) float stat_l[kBuffers][R], stat_d[kBuffers][R];
+  __shared__ __attribute__((aligned(16))) int stat_p[kBuffers][R];
+  int b, h, t;
+  const int key_blocks = FAR ? a.far_keys / 32 : a.key_tiles, splits = FAR ? a.sink_splits : a.kv_splits;
+  if (!band_place(a, key_blocks * splits, &b, &h, &t)) return;
+  const long long pair = (long long)b * a.kv_heads + h;
+  const int split = t % splits, tile = t / splits;
+  const int lane = threadIdx.x & 63, wave = wave_of();
+  if constexpr (!FAR) {
+    zero_spare<T>(a, a.dk, a.dks, h, 1, b, t, key_blocks * splits);
+    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, t, key_blocks * splits);
+  }
+  const Entry e = entry_at<false>(a, b);
+  const int block_key = FAR ? tile * 32 : tile * kTileKeys128;
+  // padded keys past the length still get their (zero) gradient
+  const int end = a.offsets ? e.len : a.max_len;
+  if (block_key >= (FAR ? std::min(e.len, a.sinks) : end)) return;
+  // rows that see a key of the tile: near, from the first key's to the last one's
+  // window's end; far, the rest
+  const int tile_end = std::min(e.len, (block_key / kTileKeys128 + 1) * kTileKeys128);  // of the near tile
+  const int near_end = (int)std::min<long long>(e.len, (long long)tile_end - 1 + a.window);
+  const bool all_rows = !FAR && block_key < a.sinks && a.sink_splits == 0;
+  const int from = (FAR ? near_end : block_key) * a.group;
+  const int until = (FAR || all_rows ? e.len : near_end) * a.group;
+  const int steps = until > from ? (until - from + R - 1) / R : 0;
+  const int per = split_size(steps, splits, 1);
+  const int s0 = split * per, s1 = std::min(steps, s0 + per);
+  const T* kb = static_cast<const T*>(a.k) + keys_at(a, a.ks, e, b, h);
+  const T* vb = static_cast<const T*>(a.v) + keys_at(a, a.vs, e, b, h);
+  const float c2 = a.scale * kLog2e;
+  const int key_lo = FAR ? block_key : block_key + wave * 32, key = key_lo + (lane & 31);
+  bool in = key < e.len;
+  if (in && a.kv_mask) in = a.kv_mask[(a.offsets ? e.row0 : (long long)b * a.mask_stride) + key] != 0;
+  Frag<T> k[KK], v[KK];
+  f32x16 dk[DB], dv[DB];
+#pragma unroll
+  for (int c = 0; c < KK; ++c) {
+    k[c] = load_head16<T, ALN>(kb + (long long)key * a.ks[1], c, lane, a.head_dim, in);
+    v[c] = load_head16<T, ALN>(vb + (long long)key * a.vs[1], c, lane, a.head_dim, in);
+  }
+#pragma unroll
+  for (int d = 0; d < DB; ++d) dk[d] = dv[d] = zeros16();
+  const f32x2* row_stats = a.stats + pair * a.rows;
+  const f32x2 none{INFINITY, 0.f};  // rows that do not exist: weight 0
+  RowStage<T, DP, R, ALN> st;
+  f32x2 stat = none;
+  auto load = [&](int first) {
+    st.load(a, until - first);
+    stat = none;
+    if ((int)threadIdx.x < std::min(until - first, R)) stat = row_stats[first + threadIdx.x];
+  };
+  if (s0 < s1) {
+    st.start(a, e, b, h, from + s0 * R);
+    load(from + s0 * R);
+  }
+  int buffer = 0;
+  for (int step = s0; step < s1; ++step, buffer ^= kBuffers - 1) {
+    const int first = from + step * R;
+    T* tq = tiles + buffer * 2 * kTile;
+    T* tg = tq + kTile;
+    if (FAR && step > s0) __syncthreads();
+    st.store(tq, tg);
+    if (threadIdx.x < R) {
+      stat_l[buffer][threadIdx.x] = stat[0];
+      stat_d[buffer][threadIdx.x] = -stat[1];
+      stat_p[buffer][threadIdx.x] = (first + (int)threadIdx.x) / a.group;
+    }
+    __syncthreads();
+    if (step + 1 < s1) load(first + R);
+#pragma unroll
+    for (int n0 = 0; n0 < (FAR ? 32 : R); n0 += 32) {
+      const int n = FAR ? wave * 32 : n0;
+      const int p_lo = (first + n) / a.group, p_hi = (first + n + 31) / a.group;
+      // (of the far walk's rows every one sees every sink)
+      const bool far_sinks = key_lo < a.sinks;
+      if (!FAR && (p_hi < key_lo || (p_lo - (key_lo + 31) >= a.window && !far_sinks))) continue;
+      const bool whole = FAR ? key_lo + 32 <= a.sinks
+                             : p_lo >= key_lo + 31 && (p_hi - key_lo < a.window || key_lo + 32 <= a.sinks);
+      f32x16 s = zeros16(), dp;
+#pragma unroll
+      for (int x = 0; x < 16; x += 4) {
+        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&stat_d[buffer][n + result_row(lane, x)]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) dp[x + y] = d4[y];
+      }
+#pragma unroll
+      for (int c = 0; c < KK; ++c) {
+        s = mma32(rows32<DP>(tq, n, c, lane), k[c], s);
+        dp = mma32(rows32<DP>(tg, n, c, lane), v[c], dp);
+      }
+#pragma unroll
+      for (int x = 0; x < 16; x += 4) {
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&stat_l[buffer][n + result_row(lane, x)]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[x + y] = __builtin_amdgcn_exp2f(s[x + y] * c2 - l4[y]);
+      }
+      if (!whole) {
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int x = 0; x < 16; x += 4) {
+          const i32x4 p4 = *reinterpret_cast<const i32x4*>(&stat_p[buffer][n + result_row(lane, x)]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (!seen(a, p4[y], key)) s[x + y] = dp[x + y] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) dp[x] *= s[x];
+      const Frag<T> p0 = half_of<T, 0>(s), p1 = half_of<T, 1>(s), d0 = half_of<T, 0>(dp), d1 = half_of<T, 1>(dp);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        dv[d] = mma32(cols32<DP>(tg, n, d * 32, lane), p0, dv[d]);
+        dk[d] = mma32(cols32<DP>(tq, n, d * 32, lane), d0, dk[d]);
+        dv[d] = mma32(cols32<DP>(tg, n + 16, d * 32, lane), p1, dv[d]);
+        dk[d] = mma32(cols32<DP>(tq, n + 16, d * 32, lane), d1, dk[d]);
+      }
+    }
+  }
+  if constexpr (FAR) {
+    // the waves' sums, one wave after the other, dK and then dV
+    float* sums = reinterpret_cast<float*>(tile_bytes);
+    for (int half = 0; half < 2; ++half) {
+      for (int w = 0; w < kBandWaves; ++w) {
+        __syncthreads();
+        if (wave != w) continue;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float* at = sums + (d * 32 + result_row(lane, x)) * 32 + (lane & 31);
+            const float mine = half ? dv[d][x] : dk[d][x];
+            *at = w ? *at + mine : mine;
+          }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 32 * a.head_dim; i += kThreads) {
+        const int at_key = i / a.head_dim, d = i - at_key * a.head_dim;
+        part_far(a, pair, split, block_key + at_key)[half * a.head_dim + d] = sums[d * 32 + at_key];
+      }
+    }
+    return;
+  } else {
+    if (key >= end) return;
+    const bool sink = key < a.sinks && a.sink_splits > 0 && key < e.len;
+    if (a.kv_splits > 1 || sink) {
+      float* to = part_near(a, pair, split, key);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; x += 4) {
+          const int d0 = d * 32 + result_row(lane, x);
+          store4<float, false>(to, d0, a.head_dim, f32x4{dk[d][x], dk[d][x + 1], dk[d][x + 2], dk[d][x + 3]});
+          store4<float, false>(to + a.head_dim, d0, a.head_dim, f32x4{dv[d][x], dv[d][x + 1], dv[d][x + 2], dv[d][x + 3]});
+        }
+      return;
+    }
+    T* tk = static_cast<T*>(a.dk) + keys_at(a, a.dks, e, b, h) + (long long)key * a.dks[1];
+    T* tv = static_cast<T*>(a.dv) + keys_at(a, a.dvs, e, b, h) + (long long)key * a.dvs[1];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; x += 4) {
+        const int d0 = d * 32 + result_row(lane, x);
+        f32x4 xk{dk[d][x], dk[d][x + 1], dk[d][x + 2], dk[d][x + 3]};
+        f32x4 xv{dv[d][x], dv[d][x + 1], dv[d][x + 2], dv[d][x + 3]};
+        store4<T, ALN>(tk, d0, a.head_dim, in ? xk * a.scale : f32x4{0.f, 0.f, 0.f, 0.f});
+        store4<T, ALN>(tv, d0, a.head_dim, in ? xv : f32x4{0.f, 0.f, 0.f, 0.f});
+      }
+  }
+}
+
+// Adds a key's parts of dK and dV, near ones and then far ones, in order: V elements a
+// thread, of the keys 0 .. part_keys - 1.
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void k_band_join_kv(BandArgs a) {
+  const unsigned per_key = 2 * a.head_dim / V;
+  const long long id = (long long)block_id() * kThreads + threadIdx.x;
+  const long long at = id / per_key;
+  const int d = (int)(id - at * per_key) * V;
+  const long long pair = at / a.part_keys;
+  const int key = (int)(at - pair * a.part_keys);
+  if (pair >= (long long)a.batch * a.kv_heads) return;
+  const int h = (int)(pair % a.kv_heads), b = (int)(pair / a.kv_heads);
+  const Entry e = entry_at<false>(a, b, false);
+  const bool sink = key < a.sinks && a.sink_splits > 0 && key < e.len;
+  if (key >= (a.offsets ? e.len : a.max_len) || !(a.kv_splits > 1 || sink)) return;
+  float sum[V] = {};
+  bool in = key < e.len;
+  if (in && a.kv_mask) in = a.kv_mask[(a.offsets ? e.row0 : (long long)b * a.mask_stride) + key] != 0;
+  if (in) {
+#pragma unroll 4
+    for (int s = 0; s < a.kv_splits; ++s) {
+      float v[V];
+      load_f32<float, V>(part_near(a, pair, s, key) + d, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += v[i];
+    }
+    if (sink) {
+#pragma unroll 4
+      for (int s = 0; s < a.sink_splits; ++s) {
+        float v[V];
+        load_f32<float, V>(part_far(a, pair, s, key) + d, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += v[i];
+      }
+    }
+  }
+  T* to;
+  if (d < a.head_dim) {
+    to = static_cast<T*>(a.dk) + keys_at(a, a.dks, e, b, h) + (long long)key * a.dks[1] + d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] *= a.scale;
+  } else {
+    to = static_cast<T*>(a.dv) + keys_at(a, a.dvs, e, b, h) + (long long)key * a.dvs[1] + (d - a.head_dim);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) to[i] = (T)sum[i];
+}
+
+// ----------------------------------------------------------- sizes, launches
+template <typename T, int DP, bool ALN>
+void launch_bwd(const BandArgs& a, hipStream_t s) {
+  constexpr int K = kBandKeys<T, DP>;
+  const int64_t pairs = (int64_t)a.batch * a.kv_heads;
+  const int v = a.head_dim % 4 ? 1 : 4;
+  hipLaunchKernelGGL((k_band_bwd_q<T, DP, ALN>), band_grid(a, (int64_t)a.row_tiles * a.q_splits), dim3(kThreads), 0, s,
+                     a);
+  if (a.q_splits > 1) {
+    const dim3 blocks((unsigned)((pairs * a.rows * (a.head_dim / v) + kThreads - 1) / kThreads));
+    if (v == 4)
+      hipLaunchKernelGGL((k_band_join_q<T, 4, K>), blocks, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_band_join_q<T, 1, K>), blocks, dim3(kThreads), 0, s, a);
+  }
+  hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, false>), band_grid(a, (int64_t)a.key_tiles * a.kv_splits),
+                     dim3(kThreads), 0, s, a);
+  if (a.sink_splits)
+    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, true>), band_grid(a, (int64_t)(a.far_keys / 32) * a.sink_splits),
+                       dim3(kThreads), 0, s, a);
+  if (a.sink_splits || a.kv_splits > 1) {
+    const dim3 blocks = grid_of((pairs * a.part_keys * 2 * (a.head_dim / v) + kThreads - 1) / kThreads);
+    if (v == 4)
+      hipLaunchKernelGGL((k_band_join_kv<T, 4>), blocks, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_band_join_kv<T, 1>), blocks, dim3(kThreads), 0, s, a);
+  }
+}
+
+template <typename T>
+void launch_bwd_dp(bool aln, const BandArgs& a, hipStream_t s) {
+  switch (band_dp(a.head_dim)) {
+    case 32: return aln ? launch_bwd<T, 32, true>(a, s) : launch_bwd<T, 32, false>(a, s);
+    case 64: return aln ? launch_bwd<T, 64, true>(a, s) : launch_bwd<T, 64, false>(a, s);
+    case 96: return aln ? launch_bwd<T, 96, true>(a, s) : launch_bwd<T, 96, false>(a, s);
+    default: return aln ? launch_bwd<T, 128, true>(a, s) : launch_bwd<T, 128, false>(a, s);
+  }
+}
+
+constexpr int kMaxSplits = 256, kPairsForDies = 128;
+
+recis_status check_self(const recis_self_attn_desc* d) {
+  if (!d || !dtype_known(d->dtype) || d->batch < 0 || d->len < 0 || d->q_heads < 1 || d->kv_heads < 1 ||
+      d->head_dim < 1 || d->q_heads % d->kv_heads || !(d->scale > 0.f) || !std::isfinite(d->scale) || d->window < 0 ||
+      d->sinks < 0)
+    return RECIS_ERR_INVALID_ARG;
+  if (d->offsets && (d->lens || d->rows < 0)) return RECIS_ERR_INVALID_ARG;
+  if (!aligned_to(d->offsets, 4) || !aligned_to(d->lens, 4) || !aligned_to(d->error, 4)) return RECIS_ERR_INVALID_ARG;
+  if (d->head_dim > kMaxHeadDim) return RECIS_ERR_UNSUPPORTED;
+  if ((int64_t)d->len * (d->q_heads / d->kv_heads) > (1 << 30) || (int64_t)d->batch * d->kv_heads > (1 << 24))
+    return RECIS_ERR_UNSUPPORTED;
+  return RECIS_OK;
+}
+
+struct SelfPlan {
+  int window, sinks;
+  int row_tiles, key_tiles, splits, q_splits, kv_splits, sink_splits;
+  int64_t part_keys, far_keys;
+  int64_t ml_at, fwd_bytes, dq_at, kv_at, bwd_bytes;
+  bool launchable[2];
+};
+
+SelfPlan self_plan(const recis_self_attn_desc* d) {
+  SelfPlan p;
+  const int group = d->q_heads / d->kv_heads;
+  const int64_t rows = (int64_t)d->len * group, pairs = (int64_t)d->batch * d->kv_heads;
+  const int keys = band_keys(d->dtype, d->head_dim);
+  // a window that no row fills: none, and nothing for sinks to add
+  const bool band = d->window && d->window < d->len;
+  p.window = band ? d->window : 1 << 30;
+  p.sinks = band ? std::min(d->sinks, d->len) : 0;
+  p.row_tiles = std::max<int64_t>(1, (rows + kBandRows - 1) / kBandRows);
+  p.key_tiles = std::max(1, (d->len + kTileKeys128 - 1) / kTileKeys128);
+  const int64_t near = band ? (int64_t)d->window + kBandRows / group + 1 + p.sinks : d->len;
+  const int64_t walk = std::min<int64_t>(d->len, near) / keys + 2;
+  // keys (rows) are split until there are `want` blocks
+  auto split = [&](int64_t blocks, int64_t want, int64_t most) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, want / std::max<int64_t>(1, blocks), most}));
+  };
+  p.splits = p.q_splits = split(pairs * p.row_tiles, 1024, (walk + kLeastTiles - 1) / kLeastTiles);
+  const int64_t row_steps = (std::min<int64_t>(d->len, band ? d->window + kTileKeys128 : d->len) * group + 63) / 64;
+  p.kv_splits = split(pairs * p.key_tiles, 512, (row_steps + 1) / 2);
+  p.sink_splits = 0;
+  p.far_keys = p.part_keys = 0;
+  if (p.sinks > 0 && p.sinks <= kMostFarSinks) {
+    p.far_keys = round_up(p.sinks, 32);
+    p.part_keys = p.far_keys;
+    // 8 steps of 128 rows a part, more where that leaves the chip empty
+    const int64_t steps = std::max<int64_t>(1, rows / 128);
+    p.sink_splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>({64, steps, std::max<int64_t>(steps / 8, 512 / std::max<int64_t>(1, pairs))}));
+  }
+  if (p.kv_splits > 1) p.part_keys = (int64_t)p.key_tiles * kTileKeys128;
+  const int64_t cells = std::max<int64_t>(pairs * rows, 1);
+  p.ml_at = p.splits > 1 ? round_up(cells * p.splits * d->head_dim * 4, 256) : 0;
+  p.fwd_bytes = p.splits > 1 ? p.ml_at + round_up(cells * p.splits * 8, 256) : 0;
+  p.dq_at = round_up(cells * 8, 256);
+  p.kv_at = p.dq_at + (p.q_splits > 1 ? round_up(cells * p.q_splits * d->head_dim * 4, 256) : 0);
+  p.bwd_bytes = p.kv_at;
+  if (p.part_keys)
+    p.bwd_bytes += round_up(std::max<int64_t>(pairs, 1) * (p.kv_splits * p.part_keys + p.sink_splits * p.far_keys) * 2 *
+                                d->head_dim * 4, 256);
+  auto fits = [&](int64_t per) { return round_up(pairs, kDies) * per <= kMaxBlocks; };
+  p.launchable[0] = fits((int64_t)p.row_tiles * p.splits);
+  p.launchable[1] = p.launchable[0] && fits((int64_t)p.key_tiles * p.kv_splits) &&
+                    fits(std::max<int64_t>(1, p.far_keys / 32) * std::max(1, p.sink_splits)) &&
+                    pairs * p.part_keys * 2 * d->head_dim / kThreads < kMaxBlocks;
+  return p;
+}
+
+void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
+  *a = BandArgs{};
+  a->offsets = d->offsets;
+  a->lens = d->lens;
+  a->kv_mask = d->kv_mask;
+  a->error = d->error;
+  a->mask_stride = d->mask_stride;
+  a->total_rows = d->rows;
+  for (int i = 0; i < 3; ++i) {
+    a->qs[i] = d->q_strides[i];
+    a->ks[i] = d->k_strides[i];
+    a->vs[i] = d->v_strides[i];
+    a->os[i] = d->o_strides[i];
+    a->dos[i] = d->do_strides[i];
+    a->dqs[i] = d->dq_strides[i];
+    a->dks[i] = d->dk_strides[i];
+    a->dvs[i] = d->dv_strides[i];
+  }
+  a->batch = d->batch;
+  a->q_len = a->max_len = d->len;
+  a->q_heads = d->q_heads;
+  a->kv_heads = d->kv_heads;
+  a->group = d->q_heads / d->kv_heads;
+  a->head_dim = d->head_dim;
+  a->rows = d->len * a->group;
+  a->causal = 1;
+  a->window = p.window;
+  a->sinks = p.sinks;
+  a->page_size = 1;
+  a->row_tiles = p.row_tiles;
+  a->key_tiles = p.key_tiles;
+  a->splits = p.splits;
+  a->q_splits = p.q_splits;
+  a->kv_splits = p.kv_splits;
+  a->sink_splits = p.sink_splits;
+  a->part_keys = (int)p.part_keys;
+  a->far_keys = (int)p.far_keys;
+  a->unit = 1;
+  a->dies = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDies : 1;
+  a->scale = d->scale;
+}
+
+// Rows can be moved 16 bytes at a time.
+bool self_aligned(const recis_self_attn_desc* d, std::initializer_list<const void*> ptrs,
+                  std::initializer_list<const int64_t*> strides) {
+  const int per = 16 / dtype_size(d->dtype);
+  if (d->head_dim % 8) return false;
+  for (const void* p : ptrs)
+    if (!aligned_to(p, 16)) return false;
+  for (const int64_t* s : strides)
+    for (int i = 0; i < 3; ++i)
+      if (s[i] % per) return false;
+  return true;
+}
+
+bool all_there(const recis_self_attn_desc* d, std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!p || !aligned_to(p, dtype_size(d->dtype))) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace recis
+
+using namespace recis;
+
+extern "C" {
+
+int64_t recis_self_attn_workspace_bytes(const recis_self_attn_desc* desc, int32_t backward) {
+  if (check_self(desc) != RECIS_OK) return -1;
+  const SelfPlan p = self_plan(desc);
+  if (!p.launchable[backward ? 1 : 0]) return -1;
+  return backward ? p.bwd_bytes : p.fwd_bytes;
+}
+
+recis_status recis_self_attn_fwd(const recis_self_attn_desc* desc, const void* q, const void* k, const void* v,
+                                 void* out, float* lse, void* workspace, int64_t workspace_bytes, hipStream_t s) {
+  const recis_status st = check_self(desc);
+  if (st != RECIS_OK) return st;
+  if (desc->batch == 0 || (desc->offsets ? desc->rows : desc->len) == 0) return RECIS_OK;
+  if (!all_there(desc, {q, k, v, out}) || !aligned_to(lse, 4)) return RECIS_ERR_INVALID_ARG;
+  const SelfPlan p = self_plan(desc);
+  if (!p.launchable[0]) return RECIS_ERR_UNSUPPORTED;
+  if (p.fwd_bytes && (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.fwd_bytes))
+    return RECIS_ERR_INVALID_ARG;
+  BandArgs a;
+  fill_self(desc, p, &a);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
+  const bool aln = self_aligned(desc, {q, k, v, out},
+                                {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides});
+  launch_band_fwd(desc->dtype, false, aln, a, s);
+  return launch_status();
+}
+
+recis_status recis_self_attn_bwd(const recis_self_attn_desc* desc, const void* grad_out, const void* q, const void* k,
+                                 const void* v, const void* out, const float* lse, void* grad_q, void* grad_k,
+                                 void* grad_v, void* workspace, int64_t workspace_bytes, hipStream_t s) {
+  const recis_status st = check_self(desc);
+  if (st != RECIS_OK) return st;
+  if (desc->batch == 0 || (desc->offsets ? desc->rows : desc->len) == 0) return RECIS_OK;
+  if (!all_there(desc, {grad_out, q, k, v, out, grad_q, grad_k, grad_v}) || !lse || !aligned_to(lse, 4))
+    return RECIS_ERR_INVALID_ARG;
+  const SelfPlan p = self_plan(desc);
+  if (!p.launchable[1]) return RECIS_ERR_UNSUPPORTED;
+  if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < p.bwd_bytes) return RECIS_ERR_INVALID_ARG;
+  BandArgs a;
+  fill_self(desc, p, &a);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = out;
+  a.dout = grad_out;
+  a.lse = const_cast<float*>(lse);
+  a.dq = grad_q;
+  a.dk = grad_k;
+  a.dv = grad_v;
+  a.stats = static_cast<f32x2*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.dq_at);
+  a.part_kv = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.kv_at);
+  const bool aln = self_aligned(desc, {q, k, v, out, grad_out, grad_q, grad_k, grad_v},
+                                {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides,
+                                 desc->do_strides, desc->dq_strides, desc->dk_strides, desc->dv_strides});
+  if (desc->dtype == RECIS_DTYPE_BF16)
+    launch_bwd_dp<__bf16>(aln, a, s);
+  else
+    launch_bwd_dp<float>(aln, a, s);
+  return launch_status();
+}
+
+}  // extern "C"

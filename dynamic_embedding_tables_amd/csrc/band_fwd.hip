@@ -85,14 +85,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, t;
   if (!band_place(a, a.row_tiles * a.splits, &b, &h, &t)) return;
+  if constexpr (!PAGED) zero_spare<T>(a, a.out, a.os, h * a.group, a.group, b, t, a.row_tiles * a.splits);
   // the last rows see the most keys: they start first
   const int split = t % a.splits, tile = a.row_tiles - 1 - t / a.splits;
   const Entry e = entry_at<PAGED>(a, b);
   const int tile_row = tile * kBandRows, rows = e.n * a.group;
   if (tile_row >= rows) return;
   const int lane = threadIdx.x & 63, wave = wave_of();
-  const Reach reach = reach_of(a, e, tile_row, tile_row + kBandRows - 1);
-  const Walk walk = walk_of<K>(a, reach);
+  const Walk walk = walk_of<K>(a, reach_of(a, e, tile_row, tile_row + kBandRows - 1));
+  const Reach reach = reach_of(a, e, tile_row + wave * 32, tile_row + wave * 32 + 31);
   const int per = split_size(walk.n, a.splits, kLeastTiles);
   const int i0 = split * per, i1 = std::min(walk.n, i0 + per);
   if (split > 0 && i0 >= walk.n) return;
@@ -150,6 +151,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
       if constexpr (PAGED)
         if (i + 2 < i1) st.ask_pages(a, table, walk.tile(i + 2) * K, e.len);
     }
+    if (none_seen<K>(a, reach, first)) continue;
     f32x16 s[KB];
 #pragma unroll
     for (int n = 0; n < KB; ++n) {

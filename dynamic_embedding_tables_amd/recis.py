@@ -59,6 +59,7 @@ EXPORTED_SYMBOLS = (
     "recis_layernorm_fwd", "recis_layernorm_bwd_workspace_bytes", "recis_layernorm_bwd",
     "recis_cross_attn_workspace_bytes", "recis_cross_attn_fwd", "recis_cross_attn_bwd",
     "recis_rotary", "recis_cache_append", "recis_paged_attn_workspace_bytes", "recis_paged_attn_fwd",
+    "recis_self_attn_workspace_bytes", "recis_self_attn_fwd", "recis_self_attn_bwd",
 )
 
 
@@ -138,6 +139,16 @@ class recis_paged_attn_desc(C.Structure):
                 ("q_offsets", C.c_void_p), ("kv_lens", C.c_void_p), ("page_table", C.c_void_p), ("error", C.c_void_p)]
 
 
+class recis_self_attn_desc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("len", C.c_int32), ("q_heads", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("window", C.c_int32), ("sinks", C.c_int32),
+                ("scale", C.c_float), ("rows", C.c_int64), ("q_strides", C.c_int64 * 3), ("k_strides", C.c_int64 * 3),
+                ("v_strides", C.c_int64 * 3), ("o_strides", C.c_int64 * 3), ("do_strides", C.c_int64 * 3),
+                ("dq_strides", C.c_int64 * 3), ("dk_strides", C.c_int64 * 3), ("dv_strides", C.c_int64 * 3),
+                ("lens", C.c_void_p), ("offsets", C.c_void_p), ("kv_mask", C.c_void_p), ("mask_stride", C.c_int64),
+                ("error", C.c_void_p)]
+
+
 class RecisError(RuntimeError):
     def __init__(self, status: int, where: str = ""):
         self.status = int(status)
@@ -197,8 +208,12 @@ def load_library() -> C.CDLL:
     L.recis_cache_append.argtypes = [p, p, p, p, p, p, p, p]
     L.recis_paged_attn_workspace_bytes.argtypes = [p]
     L.recis_paged_attn_fwd.argtypes = [p, p, p, p, p, p, p, i64, p]
+    L.recis_self_attn_workspace_bytes.argtypes = [p, i32]
+    L.recis_self_attn_fwd.argtypes = [p, p, p, p, p, p, p, i64, p]
+    L.recis_self_attn_bwd.argtypes = [p, p, p, p, p, p, p, p, p, p, p, i64, p]
     for name in ("recis_embed_bwd_workspace_bytes", "recis_layernorm_bwd_workspace_bytes",
-                 "recis_cross_attn_workspace_bytes", "recis_paged_attn_workspace_bytes"):
+                 "recis_cross_attn_workspace_bytes", "recis_paged_attn_workspace_bytes",
+                 "recis_self_attn_workspace_bytes"):
         getattr(L, name).restype = i64
     L.recis_status_string.argtypes = [i32]
     L.recis_status_string.restype = C.c_char_p
@@ -210,7 +225,8 @@ def load_library() -> C.CDLL:
                  "recis_idmap_sketch", "recis_idmap_stats", "recis_get_error",
                  "recis_embed_fwd", "recis_embed_bwd", "recis_layernorm_fwd", "recis_layernorm_bwd",
                  "recis_cross_attn_fwd", "recis_cross_attn_bwd",
-                 "recis_rotary", "recis_cache_append", "recis_paged_attn_fwd"):
+                 "recis_rotary", "recis_cache_append", "recis_paged_attn_fwd", "recis_self_attn_fwd",
+                 "recis_self_attn_bwd"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -497,6 +513,24 @@ def recis_paged_attn_fwd(desc: recis_paged_attn_desc, q, k_cache, v_cache, out, 
     _check(load_library().recis_paged_attn_fwd(
         C.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse),
         _ptr(workspace), workspace_bytes, _stream(stream)), "recis_paged_attn_fwd")
+
+
+def recis_self_attn_workspace_bytes(desc: recis_self_attn_desc, backward: bool) -> int:
+    return int(load_library().recis_self_attn_workspace_bytes(C.byref(desc), 1 if backward else 0))
+
+
+def recis_self_attn_fwd(desc: recis_self_attn_desc, q, k, v, out, lse, workspace, workspace_bytes: int, stream=None):
+    _check(load_library().recis_self_attn_fwd(
+        C.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _stream(stream)), "recis_self_attn_fwd")
+
+
+def recis_self_attn_bwd(desc: recis_self_attn_desc, grad_out, q, k, v, out, lse, grad_q, grad_k, grad_v, workspace,
+                        workspace_bytes: int, stream=None):
+    _check(load_library().recis_self_attn_bwd(
+        C.byref(desc), grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), workspace.data_ptr(), workspace_bytes,
+        _stream(stream)), "recis_self_attn_bwd")
 
 
 # --------------------------------------------------------- conveniences

@@ -590,3 +590,97 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
     workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
     recis.recis_paged_attn_fwd(d, q, k_cache, v_cache, out, lse, workspace, nbytes)
     return (out, lse) if return_lse else out
+
+
+# ----------------------------------------------------------- self attention
+def _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error):
+    packed = offsets is not None
+    if q.dim() != (3 if packed else 4) or k.dim() != q.dim() or v.shape != k.shape or q.shape[:-2] != k.shape[:-2] \
+            or q.shape[-1] != k.shape[-1]:
+        raise ValueError("q must be [batch, len, q_heads, head_dim], or [rows, q_heads, head_dim] with offsets, and k "
+                         "and v the same with kv_heads")
+    if not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q, k and v must be of one type")
+    if packed != (max_len is not None) or (packed and lens is not None):
+        raise ValueError("packed histories (offsets) take max_len, and no lens; padded ones no max_len")
+    d = recis.recis_self_attn_desc()
+    d.dtype = _dtype("q", q)
+    batch, length = (offsets.numel() - 1, max_len) if packed else q.shape[:2]
+    d.batch, d.len, d.rows = recis.int32(batch), recis.int32(length), q.shape[0] if packed else 0
+    d.q_heads, d.kv_heads, d.head_dim = map(recis.int32, (q.shape[-2], k.shape[-2], q.shape[-1]))
+    d.window, d.sinks = _band(window, sinks)
+    d.scale = max(q.shape[-1], 1) ** -0.5 if scale is None else scale
+    keep = []
+    if packed:
+        keep.append(_index("offsets", offsets, torch.int32, (batch + 1,)))
+        d.offsets = keep[-1].data_ptr()
+    elif lens is not None:
+        keep.append(_index("lens", lens, torch.int32, (batch,)))
+        d.lens = keep[-1].data_ptr()
+    if kv_mask is not None:
+        if kv_mask.dtype not in (torch.bool, torch.uint8) or kv_mask.shape != k.shape[:-2]:
+            raise ValueError(f"kv_mask must be bool or uint8 {list(k.shape[:-2])}")
+        keep.append(kv_mask if kv_mask.stride(-1) == 1 else kv_mask.contiguous())
+        d.kv_mask, d.mask_stride = keep[-1].data_ptr(), 0 if packed else keep[-1].stride(0)
+    if error is not None:
+        d.error = _error_word(error).data_ptr()
+    d.q_strides[:], d.k_strides[:], d.v_strides[:] = _st(q), _st(k), _st(v)
+    return d, keep
+
+
+def self_attention(q, k, v, lens=None, offsets=None, kv_mask=None, max_len: Optional[int] = None,
+                   window: Optional[int] = None, sinks: int = 0, scale: Optional[float] = None,
+                   return_lse: bool = False, error=None, stream=None):
+    """Causal attention of histories to themselves: position p sees the positions up to p, with window the latest
+    `window` of them, itself among them, and the first `sinks` ones.
+
+    q [batch, len, q_heads, head_dim], k and v [batch, len, kv_heads, head_dim], entry b having its first lens[b]
+    positions (int32, default: all); or packed, [rows, heads, head_dim], entry b having rows offsets[b] .. offsets[b +
+    1] - 1 (int32 [batch + 1], as the lookup's bag offsets), none more than max_len.  kv_mask (bool or uint8, [batch,
+    len] or [rows]) leaves further positions out as keys where it is zero.  q_heads is a multiple of kv_heads.  Returns
+    q's shape and, with return_lse, the float32 [.., q_heads] that the backward pass takes.  Rows that see no key, past
+    the length among them, give zeros and -inf; packed rows of no entry too."""
+    if stream is not None:
+        with _on(stream, q, k, v, lens, offsets, kv_mask, error):
+            return self_attention(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, return_lse, error)
+    _forward_of("self_attention", q, k, v, lens, offsets, kv_mask, error)
+    q, k, v = _heads(q), _heads(k), _heads(v)
+    d, keep = _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error)
+    out = _like(q) if d.batch and d.len else q.new_zeros(q.shape)
+    d.o_strides[:] = _st(out)
+    lse = None
+    if return_lse:
+        lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
+        if offsets is not None:
+            lse.fill_(-math.inf)
+    nbytes = recis.recis_self_attn_workspace_bytes(d, False)
+    workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
+    recis.recis_self_attn_fwd(d, q, k, v, out, lse, workspace, nbytes)
+    return (out, lse) if return_lse else out
+
+
+def self_attention_backward(grad_out, q, k, v, out, lse, lens=None, offsets=None, kv_mask=None,
+                            max_len: Optional[int] = None, window: Optional[int] = None, sinks: int = 0,
+                            scale: Optional[float] = None, error=None, stream=None):
+    """Gradients (grad_q, grad_k, grad_v) of self_attention from its out and lse; the other arguments as there.  Rows
+    that see no key and positions that do not count get zeros."""
+    if stream is not None:
+        with _on(stream, grad_out, q, k, v, out, lse, lens, offsets, kv_mask, error):
+            return self_attention_backward(grad_out, q, k, v, out, lse, lens, offsets, kv_mask, max_len, window, sinks,
+                                           scale, error)
+    _on_gpu(grad_out, q, k, v, out, lse, lens, offsets, kv_mask, error)
+    if not grad_out.shape == out.shape == q.shape or not grad_out.dtype == out.dtype == q.dtype:
+        raise ValueError("grad_out and out must have q's shape and type")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:-1] or not lse.is_contiguous():
+        raise ValueError("lse must be self_attention's, contiguous float32 over q's leading axes and heads")
+    q, k, v, out, grad_out = _heads(q), _heads(k), _heads(v), _heads(out), _heads(grad_out)
+    d, keep = _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error)
+    dq, dk, dv = _like(q), _like(k), _like(v)
+    if not d.batch or not d.len:  # without an entry nothing is written
+        dq.zero_(), dk.zero_(), dv.zero_()
+    d.o_strides[:], d.do_strides[:], d.dq_strides[:] = _st(out), _st(grad_out), _st(dq)
+    d.dk_strides[:], d.dv_strides[:] = _st(dk), _st(dv)
+    nbytes = recis.recis_self_attn_workspace_bytes(d, True)
+    workspace = q.new_empty(max(nbytes, 0), dtype=torch.uint8)
+    recis.recis_self_attn_bwd(d, grad_out, q, k, v, out, lse, dq, dk, dv, workspace, nbytes)
+    return dq, dk, dv

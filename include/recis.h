@@ -714,6 +714,56 @@ recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* desc, const void*
                                   const void* v_cache, void* out, float* lse, void* workspace,
                                   int64_t workspace_bytes, hipStream_t s);
 
+/* Self attention of histories: the row at position p of an entry sees the keys j
+ * <= p of that entry with p - j < window (window > 0) or j < sinks, and kv_mask[j]
+ * != 0.  q, k, v: [batch, len] padded, entry b having its first lens[b] positions
+ * (NULL: all), or packed by offsets.  The limits are recis_cross_attn_fwd's, with
+ * both lengths `len` and tiles of 128 queries or keys. */
+typedef struct {
+  int32_t dtype;              /* of q, k, v, out and every gradient */
+  int32_t batch;
+  int32_t len;                /* positions an entry; packed: the most any entry has */
+  int32_t q_heads;            /* a multiple of kv_heads */
+  int32_t kv_heads;
+  int32_t head_dim;           /* 1 .. 128 (else UNSUPPORTED) */
+  int32_t window;             /* 0: none */
+  int32_t sinks;              /* without a window they change nothing */
+  float scale;                /* of the scores, > 0 */
+  int64_t rows;               /* packed: rows of q, k and v */
+  int64_t q_strides[3];       /* (batch entry, position, head); packed: the first is not read */
+  int64_t k_strides[3];
+  int64_t v_strides[3];
+  int64_t o_strides[3];
+  int64_t do_strides[3];      /* backward only, as are the rest */
+  int64_t dq_strides[3];
+  int64_t dk_strides[3];
+  int64_t dv_strides[3];
+  const int32_t* lens;        /* device [batch], or NULL */
+  const int32_t* offsets;     /* device [batch + 1], or NULL; excludes lens */
+  const uint8_t* kv_mask;     /* device [batch, len], or [rows] when packed; or NULL */
+  int64_t mask_stride;        /* of a batch entry in kv_mask (padded) */
+  uint32_t* error;            /* as in recis_attn_desc */
+} recis_self_attn_desc;
+
+int64_t recis_self_attn_workspace_bytes(const recis_self_attn_desc* desc, int32_t backward);
+
+/* out and lse (float32 [batch, len, q_heads] or [rows, q_heads], may be NULL) as
+ * recis_cross_attn_fwd.  A row that sees no key, past its entry's length among
+ * them, gives 0 and -infinity; packed rows of no entry get 0 in out and nothing in
+ * lse.  What masked positions and positions past the length hold is not looked at;
+ * a value that is not finite may reach rows of its own entry that do not see it. */
+recis_status recis_self_attn_fwd(const recis_self_attn_desc* desc, const void* q, const void* k, const void* v,
+                                 void* out, float* lse, void* workspace, int64_t workspace_bytes, hipStream_t s);
+
+/* Gradients of q, k and v from the forward's out and lse; with bfloat16 rounded on
+ * the way as recis_cross_attn_bwd's, sum(grad_out * out) carrying out's rounding
+ * for rows whose tile sees more than 64 keys.  Rows that see nothing and keys that
+ * do not count get zeros (packed rows of no entry among them); the gradients of a
+ * shared key head are summed over its query heads. */
+recis_status recis_self_attn_bwd(const recis_self_attn_desc* desc, const void* grad_out, const void* q, const void* k,
+                                 const void* v, const void* out, const float* lse, void* grad_q, void* grad_k,
+                                 void* grad_v, void* workspace, int64_t workspace_bytes, hipStream_t s);
+
 #ifdef __cplusplus
 }
 #endif
