@@ -15,11 +15,32 @@
 // in that order.
 #pragma once
 
+#include <type_traits>
+
 #include "attn.h"
 
 namespace recis {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// x / d for 0 <= x < 2^31, without a division: the compiler's takes some 30 dependent
+// instructions, and a block of few tiles does a dozen before its first load.
+struct Quick {
+  int d, shift;
+  unsigned mul, one;
+  Quick() = default;
+  explicit Quick(int64_t by) : d((int)by), shift(0), mul(0), one(~0u) {
+    if (by <= 1) return;
+    int bits = 0;
+    while ((1ll << bits) < by) ++bits;
+    mul = (unsigned)((1ull << (31 + bits)) / by + 1);
+    shift = bits - 1;
+    one = 0;
+  }
+};
+__device__ __forceinline__ int divided(int x, const Quick& q) {
+  return (int)((__umulhi((unsigned)x, q.mul) + ((unsigned)x & q.one)) >> q.shift);
+}
 
 struct BandArgs {
   const void *q, *k, *v, *o, *dout;
@@ -37,10 +58,11 @@ struct BandArgs {
   int max_len;                 // most keys an entry has
   int rows;                    // most rows a pair has: q_len * group
   int causal, window, sinks;   // window: more than any length where there is none
-  int page_size, page_mul, page_shift;
+  Quick by_page, by_group, by_kv_heads;
   int row_tiles, key_tiles, splits, q_splits, kv_splits, sink_splits;
   int part_keys, far_keys;     // keys that have parts of dK and dV, and sinks in whole blocks of 32
-  int dies, unit;              // `unit` pairs share a die, `dies` units lie side by side
+  int die_bits, unit;          // `unit` pairs share a die, 2^die_bits units lie side by side
+  Quick by_across, by_per, by_splits;  // of this launch: blocks of a unit, of a pair, and of a tile
   float scale;
   float *part_o, *part_ml;     // parts of key ranges: [pair][split][rows][head_dim], [..][2]
   float* part_kv;              // parts of row ranges: [pair][split][part_keys][2][head_dim], then far ones
@@ -49,20 +71,26 @@ struct BandArgs {
 
 // Sizes a launch of one of the many-row kernels needs (band_fwd.hip, band_bwd.hip).
 constexpr int kBandWaves = 4, kBandRows = 32 * kBandWaves;
+constexpr int kDies = 8, kDieBits = 3;
 constexpr int kLeastTiles = 2;      // tiles of keys a split has where there are so many
 inline int band_dp(int head_dim) { return (head_dim + 31) / 32 * 32; }
 inline int band_keys(int dtype, int head_dim) { return dtype == RECIS_DTYPE_F32 && head_dim > 64 ? 32 : 64; }
-inline dim3 band_grid(const BandArgs& a, int64_t per) {
-  return grid_of(round_up((int64_t)a.batch * a.kv_heads, (int64_t)a.dies * a.unit) * per);
+// The grid of a launch of `tiles` tiles a pair in `splits` parts each.
+inline dim3 band_grid(BandArgs* a, int64_t tiles, int64_t splits) {
+  const int64_t per = tiles * splits;
+  a->by_per = Quick(per);
+  a->by_across = Quick(per * a->unit);
+  a->by_splits = Quick(splits);
+  return grid_of(round_up((int64_t)a->batch * a->kv_heads, (int64_t)a->unit << a->die_bits) * per);
 }
 void launch_band_fwd(int dtype, bool paged, bool aln, const BandArgs& a, hipStream_t s);
 
 namespace {
 
-// x / page_size for 0 <= x < 2^31.
-__device__ __forceinline__ int page_of(const BandArgs& a, int key) {
-  return a.page_size == 1 ? key : (int)(__umulhi((unsigned)key, (unsigned)a.page_mul) >> a.page_shift);
-}
+template <int N>
+using Const = std::integral_constant<int, N>;
+
+__device__ __forceinline__ int page_of(const BandArgs& a, int key) { return divided(key, a.by_page); }
 
 // --------------------------------------------------------------- an entry
 struct Entry {
@@ -107,8 +135,8 @@ struct Reach {
   int low, high;
 };
 __device__ __forceinline__ Reach reach_of(const BandArgs& a, Entry e, int row0, int row1) {
-  const int last = std::min(std::min(row1 / a.group, e.n - 1) * e.step + e.shift, e.len - 1);
-  return Reach{row0 / a.group * e.step + e.shift, last};
+  const int last = std::min(std::min(divided(row1, a.by_group), e.n - 1) * e.step + e.shift, e.len - 1);
+  return Reach{divided(row0, a.by_group) * e.step + e.shift, last};
 }
 
 // The tiles of K keys that rows of a reach see, in order: tiles of sinks that lie
@@ -159,25 +187,27 @@ __device__ __forceinline__ int split_size(int n, int splits, int least) {
 
 // Consecutive blocks go to the eight dies in turn; `unit` pairs, all `per` blocks of
 // each, share a die and its L2.
-constexpr int kDies = 8;
-__device__ __forceinline__ bool band_place(const BandArgs& a, int per, int* b, int* h, int* t) {
-  const int id = block_id(), slot = id / a.dies, across = per * a.unit, rest = slot % across;
-  const int pair = ((slot / across) * a.dies + id % a.dies) * a.unit + rest / per;
-  *t = rest % per;
-  *b = pair / a.kv_heads;
-  *h = pair % a.kv_heads;
-  return pair < a.batch * a.kv_heads;
+__device__ __forceinline__ bool band_place(const BandArgs& a, int* b, int* h, int* tile, int* split) {
+  const int id = block_id(), slot = id >> a.die_bits, turn = divided(slot, a.by_across);
+  const int rest = slot - turn * a.by_across.d, in_unit = divided(rest, a.by_per);
+  const int t = rest - in_unit * a.by_per.d;
+  const int pair = ((turn << a.die_bits) + (id & ((1 << a.die_bits) - 1))) * a.unit + in_unit;
+  *tile = divided(t, a.by_splits);
+  *split = t - *tile * a.by_splits.d;
+  *b = divided(pair, a.by_kv_heads);
+  *h = pair - *b * a.kv_heads;
+  return *b < a.batch;
 }
 
 // Offset of query q, head g of the group, in a tensor of queries.
 __device__ __forceinline__ long long query_at(const BandArgs& a, const long long (&st)[3], Entry e, int b,
                                               int h, int r) {
-  const int q = r / a.group, g = r - q * a.group;
+  const int q = divided(r, a.by_group), g = r - q * a.group;
   return (a.offsets ? e.row0 * st[1] : (long long)b * st[0]) + (long long)q * st[1] +
          (long long)(h * a.group + g) * st[2];
 }
 __device__ __forceinline__ long long lse_at(const BandArgs& a, Entry e, int b, int h, int r) {
-  const int q = r / a.group, g = r - q * a.group;
+  const int q = divided(r, a.by_group), g = r - q * a.group;
   return ((a.offsets ? e.row0 : (long long)b * a.q_len) + q) * a.q_heads + h * a.group + g;
 }
 
@@ -188,11 +218,11 @@ __device__ __forceinline__ long long keys_at(const BandArgs& a, const long long 
 }
 
 // Bit i: key first + i is there and not masked (not paged).
-__device__ __forceinline__ unsigned long long band_bits(const BandArgs& a, Entry e, int b, int first,
-                                                        int lane) {
-  const int key = first + lane;
-  bool in = key < e.len;
-  if (in && a.kv_mask) in = a.kv_mask[(a.offsets ? e.row0 : (long long)b * a.mask_stride) + key] != 0;
+__device__ __forceinline__ unsigned long long band_bits(const BandArgs& a, Entry e, int b, int first, int lane) {
+  const int n = e.len - first;
+  if (!a.kv_mask) return n >= 64 ? ~0ull : n <= 0 ? 0 : (1ull << n) - 1;
+  bool in = lane < n;
+  if (in) in = a.kv_mask[(a.offsets ? e.row0 : (long long)b * a.mask_stride) + first + lane] != 0;
   return __ballot(in);
 }
 
@@ -259,17 +289,32 @@ __device__ __forceinline__ Frag<T> half_of(const f32x16& x) {
   return __builtin_convertvector(y, Frag<T>);
 }
 
-// A lane's operand for chunk c (16 elements) of a row of `dim`.
-template <typename T, bool ALN>
-__device__ __forceinline__ Frag<T> load_head16(const T* row, int c, int lane, int dim, bool in) {
-  return load8<T, ALN>(row, c * 16 + (lane >> 5) * 8, dim, in);
+// A lane's operands for the KK chunks (16 elements each) of a row that is there; zeros
+// past its `dim` elements.
+template <typename T, int KK, bool ALN>
+__device__ __forceinline__ void load_row16(Frag<T> (&f)[KK], const T* row, int lane, int dim) {
+#pragma unroll
+  for (int c = 0; c < KK; ++c) {
+    const int d = c * 16 + (lane >> 5) * 8;
+    if constexpr (ALN)
+      f[c] = *reinterpret_cast<const Frag<T>*>(row + (d < dim ? d : 0));
+    else
+      f[c] = load8<T, false>(row, d, dim, true);
+  }
+  if (ALN && dim < KK * 16) {
+#pragma unroll
+    for (int c = 0; c < KK; ++c)
+      if (c * 16 + (lane >> 5) * 8 >= dim) f[c] = Frag<T>{};
+  }
 }
 
-// The same for rows row0 .. row0 + 31 of a tile in LDS.
+// A lane's operand for chunk c of rows row0 .. row0 + 31 of a tile in LDS.
 template <int DP>
 __device__ __forceinline__ bf16x8 rows32(const __bf16* tile, int row0, int c, int lane) {
-  return *reinterpret_cast<const bf16x8*>(tile + row0 * kLd<__bf16, DP> +
-                                          chunk_at<__bf16, DP>(lane & 31, c * 2 + (lane >> 5)));
+  // (the exchange leaves all but the low 3 bits of a chunk's number alone: four addresses
+  // serve all chunks)
+  return *reinterpret_cast<const bf16x8*>(tile + row0 * kLd<__bf16, DP> + (c & ~3) * 16 +
+                                          chunk_at<__bf16, DP>(lane & 31, (c & 3) * 2 + (lane >> 5)));
 }
 template <int DP>
 __device__ __forceinline__ f32x8 rows32(const float* tile, int row0, int c, int lane) {
@@ -284,8 +329,9 @@ __device__ __forceinline__ bf16x8 cols32(const __bf16* tile, int row0, int c0, i
   typedef short s16x4 __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const int row = (lane >> 5) * 4 + ((lane & 15) >> 2);
-  const __bf16* p = tile + row0 * kLd<__bf16, DP> +
-                    chunk_at<__bf16, DP>(row, c0 / 8 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) + (lane & 1) * 4;
+  const __bf16* p = tile + row0 * kLd<__bf16, DP> + (c0 & ~63) +
+                    chunk_at<__bf16, DP>(row, (c0 & 63) / 8 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) +
+                    (lane & 1) * 4;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * kLd<__bf16, DP>));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -299,6 +345,85 @@ __device__ __forceinline__ f32x8 cols32(const float* tile, int row0, int c0, int
   return x;
 }
 
+// A tile of K keys of K and V in registers on its way to LDS.  What is not there -- keys
+// past the length or masked, elements past the head -- is loaded from a place that is,
+// and replaced by zeros on the way to LDS: no load stands behind a branch, after which
+// the compiler would wait for it (that wait took a third of the forward's time).
+template <typename T, int DP, int K, bool PAGED, bool ALN>
+struct KeyStage {
+  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = K / kStep;
+  static_assert(K % kStep == 0, "every thread has the same number of chunks");
+  Frag<T> fk[kPer], fv[kPer];
+  int page[kPer];  // of the tile that comes next
+  int row, d0;
+  unsigned at_d;   // bytes into the head
+  bool bad;
+  __device__ __forceinline__ void start(const BandArgs& a) {
+    row = threadIdx.x / kAcross;
+    d0 = (threadIdx.x % kAcross) * 8;
+    at_d = d0 < a.head_dim ? d0 * (unsigned)sizeof(T) : 0;
+    bad = false;
+  }
+  __device__ __forceinline__ void ask_pages(const BandArgs& a, const int* table, int first, int len) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) page[i] = table[page_of(a, std::min(first + row + i * kStep, len - 1))];
+  }
+  static __device__ __forceinline__ Frag<T> at_bytes(const T* base, unsigned bytes) {
+    return *reinterpret_cast<const Frag<T>*>(reinterpret_cast<const char*>(base) + bytes);
+  }
+  __device__ __forceinline__ void load(const BandArgs& a, const T* kb, const T* vb, int first, int len,
+                                       unsigned long long bits) {
+    const T* tile_k = kb + (long long)first * a.ks[1];
+    const T* tile_v = vb + (long long)first * a.vs[1];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int in_tile = row + i * kStep;
+      if constexpr (PAGED) {
+        const int key = std::min(first + in_tile, len - 1), slot = key - page_of(a, key) * a.by_page.d;
+        int p = page[i];
+        if ((unsigned)p >= (unsigned long long)a.pages) p = 0, bad = true;
+        if constexpr (ALN) {  // (strides are below 2^31)
+          fk[i] = at_bytes(kb + ((unsigned long long)(unsigned)p * (unsigned)a.ks[0] +
+                                 (unsigned long long)(unsigned)slot * (unsigned)a.ks[1]), at_d);
+          fv[i] = at_bytes(vb + ((unsigned long long)(unsigned)p * (unsigned)a.vs[0] +
+                                 (unsigned long long)(unsigned)slot * (unsigned)a.vs[1]), at_d);
+        } else {
+          const bool in = first + in_tile < len;
+          fk[i] = load8<T, false>(kb + (long long)p * a.ks[0] + (long long)slot * a.ks[1], d0, a.head_dim, in);
+          fv[i] = load8<T, false>(vb + (long long)p * a.vs[0] + (long long)slot * a.vs[1], d0, a.head_dim, in);
+        }
+      } else if constexpr (ALN) {  // (a tile's bytes are below 2^31)
+        const unsigned r = std::min(in_tile, len - 1 - first);
+        fk[i] = at_bytes(tile_k, r * (unsigned)(a.ks[1] * sizeof(T)) + at_d);
+        fv[i] = at_bytes(tile_v, r * (unsigned)(a.vs[1] * sizeof(T)) + at_d);
+      } else {
+        const bool in = bits >> in_tile & 1;
+        fk[i] = load8<T, false>(tile_k + (long long)in_tile * a.ks[1], d0, a.head_dim, in);
+        fv[i] = load8<T, false>(tile_v + (long long)in_tile * a.vs[1], d0, a.head_dim, in);
+      }
+    }
+  }
+  // `bits`: the keys of the loaded tile that are there
+  __device__ __forceinline__ void store(const BandArgs& a, T* tk, T* tv, unsigned long long bits) {
+    if (ALN && ((K == 64 ? bits != ~0ull : (unsigned)bits != ~0u) || a.head_dim < kCols<DP>)) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (!(bits >> (row + i * kStep) & 1) || d0 >= a.head_dim) fk[i] = fv[i] = Frag<T>{};
+    }
+    if (kCols<DP> > DP && d0 >= DP) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
+      *reinterpret_cast<Frag<T>*>(tk + at) = fk[i];
+      *reinterpret_cast<Frag<T>*>(tv + at) = fv[i];
+    }
+  }
+  // (a page out of range is read as page 0, which is there)
+  __device__ __forceinline__ void tell(const BandArgs& a) const {
+    if (PAGED && bad && a.error) atomicOr(a.error, kErrInvalid);
+  }
+};
+
 // -------------------------------------------------------------------- joins
 // Joins the key ranges of a row, V elements a thread; rows of one range are done.
 template <typename T, int V, bool PAGED, int K, int ROWS, int LEAST>
@@ -308,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void k_band_join(BandArgs a) {
   const unsigned row = id / per_row, d = (id - row * per_row) * V;
   const unsigned pair = row / a.rows, r = row - pair * a.rows;
   if (pair >= (unsigned)(a.batch * a.kv_heads)) return;
-  const int h = (int)pair % a.kv_heads, b = (int)pair / a.kv_heads;
+  const int b = divided((int)pair, a.by_kv_heads), h = (int)pair - b * a.kv_heads;
   const Entry e = entry_at<PAGED>(a, b, false);
   if ((int)r >= e.n * a.group) return;
   const int tile_row = r / ROWS * ROWS;
@@ -348,7 +473,7 @@ __global__ __launch_bounds__(kThreads) void k_band_join_few(BandArgs a) {
   __shared__ float part[kBandWaves][kMaxHeadDim + 1];
   const int lane = threadIdx.x & 63, wave = wave_of();
   const int r = (int)(blockIdx.x % a.rows), pair = (int)(blockIdx.x / a.rows);
-  const int h = pair % a.kv_heads, b = pair / a.kv_heads;
+  const int b = divided(pair, a.by_kv_heads), h = pair - b * a.kv_heads;
   const Entry e = entry_at<PAGED>(a, b, false);
   if (r >= e.n * a.group) return;
   const int tile_row = r / ROWS * ROWS;

@@ -21,50 +21,16 @@
 namespace recis {
 namespace {
 
-// A tile of K keys of K and V in registers on its way to LDS (keys that are not paged).
-template <typename T, int DP, int K, bool ALN>
-struct PairStage {
-  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross;
-  static constexpr int kPer = (K + kStep - 1) / kStep;
-  Frag<T> fk[kPer], fv[kPer];
-  int row, d0;
-  __device__ __forceinline__ void start() {
-    row = threadIdx.x / kAcross;
-    d0 = (threadIdx.x % kAcross) * 8;
-  }
-  // rows whose bit is clear are zero, whatever memory holds there
-  __device__ __forceinline__ void load(const BandArgs& a, const T* kb, const T* vb, int first,
-                                       unsigned long long bits) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int in_tile = row + i * kStep;
-      const bool in = in_tile < K && (bits >> in_tile & 1);
-      fk[i] = load8<T, ALN>(kb + (long long)(first + in_tile) * a.ks[1], d0, a.head_dim, in);
-      fv[i] = load8<T, ALN>(vb + (long long)(first + in_tile) * a.vs[1], d0, a.head_dim, in);
-    }
-  }
-  __device__ __forceinline__ void store(T* tk, T* tv) const {
-    if (d0 >= DP) return;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (K == kPer * kStep || row + i * kStep < K) {
-        const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
-        *reinterpret_cast<Frag<T>*>(tk + at) = fk[i];
-        *reinterpret_cast<Frag<T>*>(tv + at) = fv[i];
-      }
-  }
-};
-
 // dQ, and each row's L (in log2 of the weight) and delta for dK and dV.
 template <typename T, int DP, bool ALN>
 __global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32, K = kBandKeys<T, DP>, KB = K / 32;
   constexpr int kTile = K * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
-  int b, h, t;
-  if (!band_place(a, a.row_tiles * a.q_splits, &b, &h, &t)) return;
-  zero_spare<T>(a, a.dq, a.dqs, h * a.group, a.group, b, t, a.row_tiles * a.q_splits);
-  const int split = t % a.q_splits, tile = a.row_tiles - 1 - t / a.q_splits;
+  int b, h, tile, split;
+  if (!band_place(a, &b, &h, &tile, &split)) return;
+  zero_spare<T>(a, a.dq, a.dqs, h * a.group, a.group, b, tile * a.q_splits + split, a.by_per.d);
+  tile = a.row_tiles - 1 - tile;
   const Entry e = entry_at<false>(a, b);
   const int tile_row = tile * kBandRows, rows = e.n * a.group;
   if (tile_row >= rows) return;
@@ -78,53 +44,50 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
   const T* vb = static_cast<const T*>(a.v) + keys_at(a, a.vs, e, b, h);
   const int r = tile_row + wave * 32 + (lane & 31);
   const bool exists = r < rows;
-  const int p = exists ? position(a, e, r / a.group) : -1;
+  const int p = exists ? position(a, e, divided(r, a.by_group)) : -1;
   const float c2 = a.scale * kLog2e;
-  Frag<T> q[KK], g[KK];
-  float delta = 0.f;
-  {
-    const T* pq = static_cast<const T*>(a.q) + (exists ? query_at(a, a.qs, e, b, h, r) : 0);
-    const T* pg = static_cast<const T*>(a.dout) + (exists ? query_at(a, a.dos, e, b, h, r) : 0);
-    const T* po = static_cast<const T*>(a.o) + (exists ? query_at(a, a.os, e, b, h, r) : 0);
-#pragma unroll
-    for (int c = 0; c < KK; ++c) {
-      q[c] = load_head16<T, ALN>(pq, c, lane, a.head_dim, p >= 0);
-      g[c] = load_head16<T, ALN>(pg, c, lane, a.head_dim, p >= 0);
-      const Frag<T> o = load_head16<T, ALN>(po, c, lane, a.head_dim, p >= 0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) delta += (float)g[c][i] * (float)o[i];
-    }
-    delta = halves_add(delta);
-  }
-  const float lse = p >= 0 ? a.lse[lse_at(a, e, b, h, r)] : -INFINITY;
-  const float lse2 = lse != -INFINITY ? lse * kLog2e : INFINITY;  // exp2(s - inf) = 0
   f32x16 dq[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) dq[d] = zeros16();
-  PairStage<T, DP, K, ALN> st;
-  st.start();
+  KeyStage<T, DP, K, false, ALN> st;
+  st.start(a);
   unsigned long long bits = 0;
   if (i0 < i1) {
     const int first = walk.tile(i0) * K;
     bits = band_bits(a, e, b, first, lane);
-    st.load(a, kb, vb, first, bits);
+    st.load(a, kb, vb, first, e.len, bits);
   }
+  Frag<T> q[KK], g[KK];  // (after the first keys' loads, which take longer)
+  float delta = 0.f;
+  {
+    const int in = std::min(r, rows - 1);
+    Frag<T> out[KK];
+    load_row16<T, KK, ALN>(q, static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, in), lane, a.head_dim);
+    load_row16<T, KK, ALN>(g, static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, in), lane, a.head_dim);
+    load_row16<T, KK, ALN>(out, static_cast<const T*>(a.o) + query_at(a, a.os, e, b, h, in), lane, a.head_dim);
+#pragma unroll
+    for (int c = 0; c < KK; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta += (float)g[c][i] * (float)out[c][i];
+    delta = halves_add(delta);
+  }
+  const float lse = a.lse[lse_at(a, e, b, h, std::min(r, rows - 1))];
+  const float lse2 = p >= 0 && lse != -INFINITY ? lse * kLog2e : INFINITY;  // exp2(s - inf) = 0
+  if (p < 0) delta = 0.f;
   int buffer = 0;
   for (int i = i0; i < i1; ++i, buffer ^= 1) {
     const int first = walk.tile(i) * K;
     T* tk = tiles + buffer * 2 * kTile;
     T* tv = tk + kTile;
-    st.store(tk, tv);
-    __syncthreads();
     const unsigned long long now = bits;
-    if (i + 1 < i1) {
-      const int next = walk.tile(i + 1) * K;
+    st.store(a, tk, tv, now);
+    __syncthreads();
+    {  // (after the last tile, that one again: a branch would have its loads waited for)
+      const int next = walk.tile(std::min(i + 1, i1 - 1)) * K;
       bits = band_bits(a, e, b, next, lane);
-      st.load(a, kb, vb, next, bits);
+      st.load(a, kb, vb, next, e.len, bits);
     }
     if (none_seen<K>(a, reach, first)) continue;
-    const bool whole = (K == 64 ? now == ~0ull : (unsigned)now == ~0u) && all_seen<K>(a, reach, first);
-    const unsigned long long mine = whole ? ~0ull : (seen_bits(a, p, first) & now) >> (4 * (lane >> 5));
     // delta from out carries out's rounding, which a key with nearly all the weight
     // sees whole: rows that see one tile of keys get it from P and dP
     if (sizeof(T) == 2 && walk.n == 1) {
@@ -137,14 +100,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
           s = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s);
           dp = mma32(rows32<DP>(tv, n * 32, c, lane), g[c], dp);
         }
+        const unsigned mine =
+            (unsigned)((seen_bits(a, p, first + n * 32) & (now >> (n * 32))) >> (4 * (lane >> 5)));
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if ((mine >> (n * 32 + 8 * (x / 4) + x % 4)) & 1) delta += __builtin_amdgcn_exp2f(s[x] * c2 - lse2) * dp[x];
+          if (mine >> (8 * (x / 4) + x % 4) & 1) delta += __builtin_amdgcn_exp2f(s[x] * c2 - lse2) * dp[x];
       }
       delta = halves_add(delta);
     }
 #pragma unroll
     for (int n = 0; n < KB; ++n) {
+      if (none_seen<32>(a, reach, first + n * 32)) continue;
       f32x16 s = zeros16(), dp;
 #pragma unroll
       for (int x = 0; x < 16; ++x) dp[x] = -delta;
@@ -155,10 +121,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
       }
 #pragma unroll
       for (int x = 0; x < 16; ++x) s[x] = __builtin_amdgcn_exp2f(s[x] * c2 - lse2) * dp[x];
-      if (!whole) {
+      const int at = first + n * 32;
+      const unsigned there = (unsigned)(now >> (n * 32));
+      if (there != ~0u || !all_seen<32>(a, reach, at)) {
+        const unsigned mine = (unsigned)(seen_bits(a, p, at) & there) >> (4 * (lane >> 5));
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (!((mine >> (n * 32 + 8 * (x / 4) + x % 4)) & 1)) s[x] = 0.f;
+          if (!(mine >> (8 * (x / 4) + x % 4) & 1)) s[x] = 0.f;
       }
       const Frag<T> d0 = half_of<T, 0>(s), d1 = half_of<T, 1>(s);
 #pragma unroll
@@ -201,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void k_band_join_q(BandArgs a) {
   const unsigned row = id / per_row, d = (id - row * per_row) * V;
   const unsigned pair = row / a.rows, r = row - pair * a.rows;
   if (pair >= (unsigned)(a.batch * a.kv_heads)) return;
-  const int h = (int)pair % a.kv_heads, b = (int)pair / a.kv_heads;
+  const int b = divided((int)pair, a.by_kv_heads), h = (int)pair - b * a.kv_heads;
   const Entry e = entry_at<false>(a, b, false);
   if ((int)r >= e.n * a.group) return;
   const int tile_row = r / kBandRows * kBandRows;
@@ -231,30 +200,42 @@ constexpr int kWalkRows = FAR ? 128 : DP <= 64 ? 64 : 32;
 // Walks a thread's chunks of the folded rows of Q and dO, from row `first` on.
 template <typename T, int DP, int R, bool ALN>
 struct RowStage {
-  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = (R + kStep - 1) / kStep;
+  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = R / kStep;
+  static_assert(R % kStep == 0, "every thread has the same number of chunks");
   Frag<T> fq[kPer], fg[kPer];
   const T *pq[kPer], *pg[kPer];  // of the row that comes next
-  int head[kPer];                // its head in the group
-  int row, d0;
+  const T *first_q, *first_g;    // of a row that is there
+  int head[kPer];                // the next row's head in the group
+  int row, d0, here;
   __device__ __forceinline__ void start(const BandArgs& a, Entry e, int b, int h, int first) {
     row = threadIdx.x / kAcross;
     d0 = (threadIdx.x % kAcross) * 8;
+    first_q = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, first);
+    first_g = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, first);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = first + row + i * kStep;
-      head[i] = r % a.group;
+      head[i] = r - divided(r, a.by_group) * a.group;
       pq[i] = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, r);
       pg[i] = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, r);
     }
   }
-  // `left` rows from the next one on exist; the others are zero
+  // `left` rows from the next one on exist: the others are zero, or loaded from a row
+  // that is there and zeroed by store() (no load stands behind a branch)
   __device__ __forceinline__ void load(const BandArgs& a, int left) {
-    const int dq = R / a.group, dh = R % a.group;  // R rows on
+    const int dq = divided(R, a.by_group), dh = R - dq * a.group;  // R rows on
+    const int d = d0 < a.head_dim ? d0 : 0;
+    here = left;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const bool in = row + i * kStep < std::min(left, R);
-      fq[i] = load8<T, ALN>(pq[i], d0, a.head_dim, in);
-      fg[i] = load8<T, ALN>(pg[i], d0, a.head_dim, in);
+      const bool in = row + i * kStep < left;
+      if constexpr (ALN) {
+        fq[i] = *reinterpret_cast<const Frag<T>*>((in ? pq[i] : first_q) + d);
+        fg[i] = *reinterpret_cast<const Frag<T>*>((in ? pg[i] : first_g) + d);
+      } else {
+        fq[i] = load8<T, ALN>(pq[i], d0, a.head_dim, in);
+        fg[i] = load8<T, ALN>(pg[i], d0, a.head_dim, in);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -270,15 +251,19 @@ struct RowStage {
       }
     }
   }
-  __device__ __forceinline__ void store(T* tq, T* tg) const {
-    if (d0 >= DP) return;
+  __device__ __forceinline__ void store(const BandArgs& a, T* tq, T* tg) {
+    if (ALN && (here < R || a.head_dim < kCols<DP>)) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (R == kPer * kStep || row + i * kStep < R) {
-        const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
-        *reinterpret_cast<Frag<T>*>(tq + at) = fq[i];
-        *reinterpret_cast<Frag<T>*>(tg + at) = fg[i];
-      }
+      for (int i = 0; i < kPer; ++i)
+        if (row + i * kStep >= here || d0 >= a.head_dim) fq[i] = fg[i] = Frag<T>{};
+    }
+    if (kCols<DP> > DP && d0 >= DP) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
+      *reinterpret_cast<Frag<T>*>(tq + at) = fq[i];
+      *reinterpret_cast<Frag<T>*>(tg + at) = fg[i];
+    }
   }
 };
 
@@ -306,15 +291,14 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
   T* const tiles = reinterpret_cast<T*>(tile_bytes);
   __shared__ __attribute__((aligned(16))) float stat_l[kBuffers][R], stat_d[kBuffers][R];
   __shared__ __attribute__((aligned(16))) int stat_p[kBuffers][R];
-  int b, h, t;
-  const int key_blocks = FAR ? a.far_keys / 32 : a.key_tiles, splits = FAR ? a.sink_splits : a.kv_splits;
-  if (!band_place(a, key_blocks * splits, &b, &h, &t)) return;
+  int b, h, tile, split;
+  if (!band_place(a, &b, &h, &tile, &split)) return;
+  const int splits = a.by_splits.d;
   const long long pair = (long long)b * a.kv_heads + h;
-  const int split = t % splits, tile = t / splits;
   const int lane = threadIdx.x & 63, wave = wave_of();
   if constexpr (!FAR) {
-    zero_spare<T>(a, a.dk, a.dks, h, 1, b, t, key_blocks * splits);
-    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, t, key_blocks * splits);
+    zero_spare<T>(a, a.dk, a.dks, h, 1, b, tile * splits + split, a.by_per.d);
+    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, tile * splits + split, a.by_per.d);
   }
   const Entry e = entry_at<false>(a, b);
   const int block_key = FAR ? tile * 32 : tile * kTileKeys128;
@@ -340,24 +324,25 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
   Frag<T> k[KK], v[KK];
   f32x16 dk[DB], dv[DB];
 #pragma unroll
-  for (int c = 0; c < KK; ++c) {
-    k[c] = load_head16<T, ALN>(kb + (long long)key * a.ks[1], c, lane, a.head_dim, in);
-    v[c] = load_head16<T, ALN>(vb + (long long)key * a.vs[1], c, lane, a.head_dim, in);
-  }
-#pragma unroll
   for (int d = 0; d < DB; ++d) dk[d] = dv[d] = zeros16();
   const f32x2* row_stats = a.stats + pair * a.rows;
   const f32x2 none{INFINITY, 0.f};  // rows that do not exist: weight 0
   RowStage<T, DP, R, ALN> st;
   f32x2 stat = none;
-  auto load = [&](int first) {
-    st.load(a, until - first);
-    stat = none;
-    if ((int)threadIdx.x < std::min(until - first, R)) stat = row_stats[first + threadIdx.x];
+  auto load = [&](int first) {  // (past the last step: that one's first row again)
+    const int left = until - first;
+    st.load(a, left);
+    stat = row_stats[(int)threadIdx.x < left ? first + threadIdx.x : from];
+    if ((int)threadIdx.x >= left) stat = none;
   };
   if (s0 < s1) {
     st.start(a, e, b, h, from + s0 * R);
     load(from + s0 * R);
+  }
+  if (e.len > 0) {  // (a key that does not count spoils its own column only, which is zero at the end)
+    const int there = std::min(key, e.len - 1);
+    load_row16<T, KK, ALN>(k, kb + (long long)there * a.ks[1], lane, a.head_dim);
+    load_row16<T, KK, ALN>(v, vb + (long long)there * a.vs[1], lane, a.head_dim);
   }
   int buffer = 0;
   for (int step = s0; step < s1; ++step, buffer ^= kBuffers - 1) {
@@ -365,18 +350,18 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
     T* tq = tiles + buffer * 2 * kTile;
     T* tg = tq + kTile;
     if (FAR && step > s0) __syncthreads();
-    st.store(tq, tg);
+    st.store(a, tq, tg);
     if (threadIdx.x < R) {
       stat_l[buffer][threadIdx.x] = stat[0];
       stat_d[buffer][threadIdx.x] = -stat[1];
-      stat_p[buffer][threadIdx.x] = (first + (int)threadIdx.x) / a.group;
+      stat_p[buffer][threadIdx.x] = divided(first + (int)threadIdx.x, a.by_group);
     }
     __syncthreads();
-    if (step + 1 < s1) load(first + R);
+    load(first + R);
 #pragma unroll
     for (int n0 = 0; n0 < (FAR ? 32 : R); n0 += 32) {
       const int n = FAR ? wave * 32 : n0;
-      const int p_lo = (first + n) / a.group, p_hi = (first + n + 31) / a.group;
+      const int p_lo = divided(first + n, a.by_group), p_hi = divided(first + n + 31, a.by_group);
       // (of the far walk's rows every one sees every sink)
       const bool far_sinks = key_lo < a.sinks;
       if (!FAR && (p_hi < key_lo || (p_lo - (key_lo + 31) >= a.window && !far_sinks))) continue;
@@ -525,12 +510,12 @@ __global__ __launch_bounds__(kThreads) void k_band_join_kv(BandArgs a) {
 
 // ----------------------------------------------------------- sizes, launches
 template <typename T, int DP, bool ALN>
-void launch_bwd(const BandArgs& a, hipStream_t s) {
+void launch_bwd(BandArgs a, hipStream_t s) {
   constexpr int K = kBandKeys<T, DP>;
   const int64_t pairs = (int64_t)a.batch * a.kv_heads;
   const int v = a.head_dim % 4 ? 1 : 4;
-  hipLaunchKernelGGL((k_band_bwd_q<T, DP, ALN>), band_grid(a, (int64_t)a.row_tiles * a.q_splits), dim3(kThreads), 0, s,
-                     a);
+  dim3 grid = band_grid(&a, a.row_tiles, a.q_splits);
+  hipLaunchKernelGGL((k_band_bwd_q<T, DP, ALN>), grid, dim3(kThreads), 0, s, a);
   if (a.q_splits > 1) {
     const dim3 blocks((unsigned)((pairs * a.rows * (a.head_dim / v) + kThreads - 1) / kThreads));
     if (v == 4)
@@ -538,11 +523,12 @@ void launch_bwd(const BandArgs& a, hipStream_t s) {
     else
       hipLaunchKernelGGL((k_band_join_q<T, 1, K>), blocks, dim3(kThreads), 0, s, a);
   }
-  hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, false>), band_grid(a, (int64_t)a.key_tiles * a.kv_splits),
-                     dim3(kThreads), 0, s, a);
-  if (a.sink_splits)
-    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, true>), band_grid(a, (int64_t)(a.far_keys / 32) * a.sink_splits),
-                       dim3(kThreads), 0, s, a);
+  grid = band_grid(&a, a.key_tiles, a.kv_splits);
+  hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, false>), grid, dim3(kThreads), 0, s, a);
+  if (a.sink_splits) {
+    grid = band_grid(&a, a.far_keys / 32, a.sink_splits);
+    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, true>), grid, dim3(kThreads), 0, s, a);
+  }
   if (a.sink_splits || a.kv_splits > 1) {
     const dim3 blocks = grid_of((pairs * a.part_keys * 2 * (a.head_dim / v) + kThreads - 1) / kThreads);
     if (v == 4)
@@ -661,7 +647,9 @@ void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
   a->causal = 1;
   a->window = p.window;
   a->sinks = p.sinks;
-  a->page_size = 1;
+  a->by_page = Quick(1);
+  a->by_group = Quick(a->group);
+  a->by_kv_heads = Quick(d->kv_heads);
   a->row_tiles = p.row_tiles;
   a->key_tiles = p.key_tiles;
   a->splits = p.splits;
@@ -671,7 +659,7 @@ void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
   a->part_keys = (int)p.part_keys;
   a->far_keys = (int)p.far_keys;
   a->unit = 1;
-  a->dies = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDies : 1;
+  a->die_bits = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDieBits : 0;
   a->scale = d->scale;
 }
 
@@ -685,6 +673,9 @@ bool self_aligned(const recis_self_attn_desc* d, std::initializer_list<const voi
   for (const int64_t* s : strides)
     for (int i = 0; i < 3; ++i)
       if (s[i] % per) return false;
+  // a tile's rows stay within 32 bits of byte offset
+  for (const int64_t* s : {d->k_strides, d->v_strides})
+    if (s[1] < 0 || s[1] >= (1 << 23)) return false;
   return true;
 }
 

@@ -21,73 +21,19 @@
 namespace recis {
 namespace {
 
-// A tile of K keys of K and V in registers on its way to LDS.
-template <typename T, int DP, int K, bool PAGED, bool ALN>
-struct KeyStage {
-  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross;
-  static constexpr int kPer = (K + kStep - 1) / kStep;
-  Frag<T> fk[kPer], fv[kPer];
-  int page[kPer];  // of the tile that comes next
-  int row, d0;
-  __device__ __forceinline__ void start() {
-    row = threadIdx.x / kAcross;
-    d0 = (threadIdx.x % kAcross) * 8;
-  }
-  __device__ __forceinline__ void ask_pages(const BandArgs& a, const int* table, int first, int len) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int key = first + row + i * kStep;
-      page[i] = key < len ? table[page_of(a, key)] : 0;
-    }
-  }
-  // rows whose bit is clear, and those past the length, are zero, whatever memory holds there
-  __device__ __forceinline__ void load(const BandArgs& a, const T* kb, const T* vb, int first, int len,
-                                       unsigned long long bits) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int in_tile = row + i * kStep, key = first + in_tile;
-      bool in = in_tile < K;
-      const T *pk, *pv;
-      if constexpr (PAGED) {
-        in = in && key < len;
-        if (in && (unsigned)page[i] >= (unsigned long long)a.pages) {
-          in = false;
-          if (a.error) atomicOr(a.error, kErrInvalid);
-        }
-        const int slot = key - page_of(a, key) * a.page_size;
-        pk = kb + (long long)page[i] * a.ks[0] + (long long)slot * a.ks[1];
-        pv = vb + (long long)page[i] * a.vs[0] + (long long)slot * a.vs[1];
-      } else {
-        in = in && (bits >> in_tile & 1);
-        pk = kb + (long long)key * a.ks[1];
-        pv = vb + (long long)key * a.vs[1];
-      }
-      fk[i] = load8<T, ALN>(pk, d0, a.head_dim, in);
-      fv[i] = load8<T, ALN>(pv, d0, a.head_dim, in);
-    }
-  }
-  __device__ __forceinline__ void store(T* tk, T* tv) const {
-    if (d0 >= DP) return;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (K == kPer * kStep || row + i * kStep < K) {
-        const int at = chunk_at<T, DP>(row + i * kStep, d0 / 8);
-        *reinterpret_cast<Frag<T>*>(tk + at) = fk[i];
-        *reinterpret_cast<Frag<T>*>(tv + at) = fv[i];
-      }
-  }
-};
+// Waves a SIMD, as many as leave no more than a few spilled registers.
+template <typename T, int DP>
+constexpr int kForwardWaves = DP > 64 ? 2 : sizeof(T) == 2 ? 4 : DP > 32 ? 2 : 3;
 
 template <typename T, int DP, bool PAGED, bool ALN>
-__global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
+__global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32, K = kBandKeys<T, DP>, KB = K / 32;
   constexpr int kTile = K * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
-  int b, h, t;
-  if (!band_place(a, a.row_tiles * a.splits, &b, &h, &t)) return;
-  if constexpr (!PAGED) zero_spare<T>(a, a.out, a.os, h * a.group, a.group, b, t, a.row_tiles * a.splits);
-  // the last rows see the most keys: they start first
-  const int split = t % a.splits, tile = a.row_tiles - 1 - t / a.splits;
+  int b, h, tile, split;
+  if (!band_place(a, &b, &h, &tile, &split)) return;
+  if constexpr (!PAGED) zero_spare<T>(a, a.out, a.os, h * a.group, a.group, b, tile * a.splits + split, a.by_per.d);
+  tile = a.row_tiles - 1 - tile;  // the last rows see the most keys: they start first
   const Entry e = entry_at<PAGED>(a, b);
   const int tile_row = tile * kBandRows, rows = e.n * a.group;
   if (tile_row >= rows) return;
@@ -109,13 +55,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
   }
   const int r = tile_row + wave * 32 + (lane & 31);
   const bool exists = r < rows;
-  const int p = exists ? position(a, e, r / a.group) : -1;
-  Frag<T> q[KK];
-  {
-    const T* from = static_cast<const T*>(a.q) + (exists ? query_at(a, a.qs, e, b, h, r) : 0);
-#pragma unroll
-    for (int c = 0; c < KK; ++c) q[c] = load_head16<T, ALN>(from, c, lane, a.head_dim, exists);
-  }
+  const int p = exists ? position(a, e, divided(r, a.by_group)) : -1;
   f32x16 o[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = zeros16();
@@ -124,57 +64,56 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
   float m = -INFINITY, ref = 0.f, most = -INFINITY, l = 0.f;
   const float c2 = a.scale * kLog2e;
   KeyStage<T, DP, K, PAGED, ALN> st;
-  st.start();
-  unsigned long long bits = ~0ull;
+  st.start(a);
+  unsigned long long bits = 0;
   if (i0 < i1) {
     const int first = walk.tile(i0) * K;
-    if constexpr (PAGED)
-      st.ask_pages(a, table, first, e.len);
-    else
-      bits = band_bits(a, e, b, first, lane);
+    if constexpr (PAGED) st.ask_pages(a, table, first, e.len);
+    bits = band_bits(a, e, b, first, lane);
     st.load(a, kb, vb, first, e.len, bits);
-    if constexpr (PAGED)
-      if (i0 + 1 < i1) st.ask_pages(a, table, walk.tile(i0 + 1) * K, e.len);
+    if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i0 + 1, i1 - 1)) * K, e.len);
   }
+  Frag<T> q[KK];  // (after the first keys' loads, which take longer)
+  load_row16<T, KK, ALN>(q, static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, std::min(r, rows - 1)), lane,
+                         a.head_dim);
   int buffer = 0;
   for (int i = i0; i < i1; ++i, buffer ^= 1) {
     const int first = walk.tile(i) * K;
     T* tk = tiles + buffer * 2 * kTile;
     T* tv = tk + kTile;
-    st.store(tk, tv);
-    __syncthreads();
     const unsigned long long now = bits;
-    if (i + 1 < i1) {
-      const int next = walk.tile(i + 1) * K;
-      if constexpr (!PAGED) bits = band_bits(a, e, b, next, lane);
+    st.store(a, tk, tv, now);
+    __syncthreads();
+    {  // (after the last tile, that one again: a branch would have its loads waited for)
+      const int next = walk.tile(std::min(i + 1, i1 - 1)) * K;
+      bits = band_bits(a, e, b, next, lane);
       st.load(a, kb, vb, next, e.len, bits);
-      if constexpr (PAGED)
-        if (i + 2 < i1) st.ask_pages(a, table, walk.tile(i + 2) * K, e.len);
+      if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i + 2, i1 - 1)) * K, e.len);
     }
     if (none_seen<K>(a, reach, first)) continue;
     f32x16 s[KB];
-#pragma unroll
-    for (int n = 0; n < KB; ++n) {
+    auto scores = [&](int n) {
       s[n] = zeros16();
 #pragma unroll
       for (int c = 0; c < KK; ++c) s[n] = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s[n]);
-    }
-    const bool whole = K == 64 ? now == ~0ull : (unsigned)now == ~0u;
-    if (!whole || !all_seen<K>(a, reach, first)) {
-      const unsigned long long mine = (seen_bits(a, p, first) & now) >> (4 * (lane >> 5));
+    };
+    auto mask = [&](int n) {
+      const int at = first + n * 32;
+      const unsigned there = (unsigned)(now >> (n * 32));
+      if (there == ~0u && all_seen<32>(a, reach, at)) return;
+      const unsigned mine = (unsigned)(seen_bits(a, p, at) & there) >> (4 * (lane >> 5));
 #pragma unroll
-      for (int n = 0; n < KB; ++n)
+      for (int x = 0; x < 16; ++x)
+        if (!(mine >> (8 * (x / 4) + x % 4) & 1)) s[n][x] = -INFINITY;
+    };
+    auto highest = [&](int n) {
+      float top = s[n][0];
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          if (!((mine >> (n * 32 + 8 * (x / 4) + x % 4)) & 1)) s[n][x] = -INFINITY;
-    }
-    float top = s[0][0];
-#pragma unroll
-    for (int n = 0; n < KB; ++n)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) top = fmaxf(top, s[n][x]);
-    top = halves_max(top);
-    if (__any(top * c2 > most)) {
+      for (int x = 1; x < 16; ++x) top = fmaxf(top, s[n][x]);
+      return halves_max(top);
+    };
+    auto raise = [&](float top) {
+      if (!__any(top * c2 > most)) return;
       const float to = fmaxf(m, top);
       ref = to == -INFINITY ? 0.f : to * c2;
       const float alpha = __builtin_amdgcn_exp2f(m * c2 - ref);
@@ -183,24 +122,45 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
       l *= alpha;
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] *= alpha;
-    }
-#pragma unroll
-    for (int n = 0; n < KB; ++n)
+    };
+    auto weights = [&](int n) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         s[n][x] = __builtin_amdgcn_exp2f(s[n][x] * c2 - ref);
         l += s[n][x];
       }
-#pragma unroll
-    for (int n = 0; n < KB; ++n) {
+    };
+    auto products = [&](int n) {
       const Frag<T> p0 = half_of<T, 0>(s[n]), p1 = half_of<T, 1>(s[n]);
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         o[d] = mma32(cols32<DP>(tv, n * 32, d * 32, lane), p0, o[d]);
         o[d] = mma32(cols32<DP>(tv, n * 32 + 16, d * 32, lane), p1, o[d]);
       }
+    };
+    auto finish = [&](int n) {
+      mask(n);
+      raise(highest(n));
+      weights(n);
+      products(n);
+    };
+    if constexpr (DP > 64 && KB == 2) {
+      // both blocks' scores first: at two waves a SIMD the products of one run behind the
+      // exponentials of the other
+      scores(0);
+      scores(1);
+      finish(0);
+      finish(1);
+    } else {
+#pragma unroll
+      for (int n = 0; n < KB; ++n) {
+        if (none_seen<32>(a, reach, first + n * 32)) continue;
+        scores(n);
+        finish(n);
+      }
     }
   }
+  st.tell(a);
   l = halves_add(l);
   if (!exists) return;
   if (p < 0) {  // a row that sees nothing, whatever its block walked
@@ -236,8 +196,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_fwd(BandArgs a) {
 }
 
 template <typename T, int DP, bool PAGED>
-void launch_fwd(bool aln, const BandArgs& a, hipStream_t s) {
-  const dim3 grid = band_grid(a, (int64_t)a.row_tiles * a.splits);
+void launch_fwd(bool aln, BandArgs a, hipStream_t s) {
+  const dim3 grid = band_grid(&a, a.row_tiles, a.splits);
   if (aln)
     hipLaunchKernelGGL((k_band_fwd<T, DP, PAGED, true>), grid, dim3(kThreads), 0, s, a);
   else

@@ -37,8 +37,8 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
   __shared__ __attribute__((aligned(128))) T tiles[kBandWaves * kTile];
   __shared__ float refs[kBandWaves][kFewRows], sums[kBandWaves][kFewRows];
   static_assert(kTile * (int)sizeof(T) >= kFewRows * DP * 4, "a wave's output fits its tile");
-  int b, h, split;
-  if (!band_place(a, a.splits, &b, &h, &split)) return;
+  int b, h, tile, split;
+  if (!band_place(a, &b, &h, &tile, &split)) return;
   const int lane = threadIdx.x & 63, wave = wave_of();
   const Entry e = entry_at<true>(a, b);
   const int rows = e.n * a.group;
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
   const float c2 = a.scale * kLog2e;
   const f32x4 zero = zeros();
   const int kr = lane & 15;  // the lane's row of the queries, and its key of 16
-  const int p = kr < rows ? position(a, e, kr / a.group) : -1;
+  const int p = kr < rows ? position(a, e, divided(kr, a.by_group)) : -1;
   Frag<T> q[KK];
   {
     const bool in = kr < rows;
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
   constexpr int kHalf = sizeof(T) == 2 ? 8 : 4;              // the operand's first elements (load_head)
   const unsigned k_at = (unsigned)((kr * a.ks[1] + (lane >> 4) * kHalf) * (long long)sizeof(T));  // ALN: fits
   const unsigned v_at = (unsigned)((vr * a.vs[1] + vd) * (long long)sizeof(T));
-  const bool by16 = ALN && a.page_size % 16 == 0 && a.head_dim == kCols<DP>;
+  const bool by16 = ALN && a.by_page.d % 16 == 0 && a.head_dim == kCols<DP>;
   auto ask_page = [&](int first) {
     const int key = first + (lane & 31);
     return key < e.len ? table[page_of(a, key)] : 0;
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
       if (a.error) atomicOr(a.error, kErrInvalid);
     }
     const unsigned bits = (unsigned)__ballot(in);
-    const int slot = key - page_of(a, key) * a.page_size;
+    const int slot = key - page_of(a, key) * a.by_page.d;
     const long long ko = in ? (long long)page * a.ks[0] + (long long)slot * a.ks[1] : 0;
     const long long vo = in ? (long long)page * a.vs[0] + (long long)slot * a.vs[1] : 0;
     if (by16 && bits == ~0u) {
@@ -248,8 +248,8 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
 }
 
 template <typename T, int DP>
-void launch_few(bool aln, const BandArgs& a, hipStream_t s) {
-  const dim3 grid = band_grid(a, a.splits);
+void launch_few(bool aln, BandArgs a, hipStream_t s) {
+  const dim3 grid = band_grid(&a, 1, a.splits);
   if (aln)
     hipLaunchKernelGGL((k_paged_few<T, DP, true>), grid, dim3(kThreads), 0, s, a);
   else
@@ -332,9 +332,9 @@ bool paged_aligned(const recis_paged_attn_desc* d, std::initializer_list<const v
   for (const int64_t* s : {d->q_strides, d->o_strides, d->k_strides, d->v_strides})
     for (int i = 0; i < 3; ++i)
       if (s[i] % per) return false;
-  // 16 slots stay within 32 bits of byte offset
+  // a wave's slots stay within 32 bits of byte offset
   for (const int64_t* s : {d->k_strides, d->v_strides})
-    if (s[1] < 0 || s[1] >= (1 << 23)) return false;
+    if (s[1] < 0 || s[1] >= (1 << 23) || s[0] < 0 || s[0] >= (1ll << 31)) return false;
   return true;
 }
 
@@ -390,20 +390,18 @@ recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* d, const void* q,
   a.kv_heads = d->kv_heads;
   a.group = d->q_heads / d->kv_heads;
   a.head_dim = d->head_dim;
-  a.max_len = d->table_width * d->page_size;
+  a.max_len = d->pages > 0 ? d->table_width * d->page_size : 0;
   a.rows = d->q_len * a.group;
   a.causal = d->causal != 0;
   a.window = window_of(d->window);
   a.sinks = std::min(d->sinks, 1 << 30);
-  a.page_size = d->page_size;
-  int bits = 0;
-  while ((1ll << bits) < d->page_size) ++bits;
-  a.page_mul = (int)(unsigned)((1ull << (31 + bits)) / d->page_size + 1);
-  a.page_shift = bits - 1;
+  a.by_page = Quick(d->page_size);
+  a.by_group = Quick(a.group);
+  a.by_kv_heads = Quick(d->kv_heads);
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
   a.unit = p.row_tiles <= 1 && d->batch >= kEntriesForDies ? d->kv_heads : 1;
-  a.dies = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDies : 1;
+  a.die_bits = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDieBits : 0;
   a.scale = d->scale;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
