@@ -62,7 +62,10 @@ struct BandArgs {
   int row_tiles, key_tiles, splits, q_splits, kv_splits, sink_splits;
   int part_keys, far_keys;     // keys that have parts of dK and dV, and sinks in whole blocks of 32
   int die_bits, unit;          // `unit` pairs share a die, 2^die_bits units lie side by side
-  Quick by_across, by_per, by_splits;  // of this launch: blocks of a unit, of a pair, and of a tile
+  int ranked;                  // entries take their turns by length, the longest first
+  int pairs_inner;             // in a unit: a tile's pairs next to each other, else a pair's tiles
+  int per;                     // blocks of a pair, in this launch
+  Quick by_inner, by_across, by_splits;  // blocks of the inner order, of a unit and of a tile, in this launch
   float scale;
   float *part_o, *part_ml;     // parts of key ranges: [pair][split][rows][head_dim], [..][2]
   float* part_kv;              // parts of row ranges: [pair][split][part_keys][2][head_dim], then far ones
@@ -77,11 +80,25 @@ inline int band_dp(int head_dim) { return (head_dim + 31) / 32 * 32; }
 inline int band_keys(int dtype, int head_dim) { return dtype == RECIS_DTYPE_F32 && head_dim > 64 ? 32 : 64; }
 // The grid of a launch of `tiles` tiles a pair in `splits` parts each.
 inline dim3 band_grid(BandArgs* a, int64_t tiles, int64_t splits) {
-  const int64_t per = tiles * splits;
-  a->by_per = Quick(per);
-  a->by_across = Quick(per * a->unit);
+  const int64_t per = tiles * splits, unit = a->unit;
+  a->per = (int)per;
+  a->by_inner = Quick(a->pairs_inner ? unit : per);
+  a->by_across = Quick(per * unit);
   a->by_splits = Quick(splits);
-  return grid_of(round_up((int64_t)a->batch * a->kv_heads, (int64_t)a->unit << a->die_bits) * per);
+  return grid_of(round_up((int64_t)a->batch * a->kv_heads, unit << a->die_bits) * per);
+}
+// How the blocks of a call are laid over the dies.
+//  - All pairs of an entry on one die where its keys are read about once (one tile of
+//    rows), a pair's blocks side by side, which reads a pair's keys in one stretch.
+//  - The same where the heads are shorter than a 128-byte line, which would be fetched by
+//    several dies, but the pairs of a tile side by side, as they meet in the lines.
+//  - With few pairs a pair's blocks go to every die.
+constexpr int kEntriesForDies = 64, kPairsForDies = 128;
+inline void place_pairs(BandArgs* a, int dtype) {
+  const bool once = a->row_tiles <= 1, together = once || a->head_dim * dtype_size(dtype) < 128;
+  a->unit = together && a->batch >= kEntriesForDies ? a->kv_heads : 1;
+  a->pairs_inner = !once;
+  a->die_bits = (int64_t)a->batch * a->kv_heads >= kPairsForDies ? kDieBits : 0;
 }
 void launch_band_fwd(int dtype, bool paged, bool aln, const BandArgs& a, hipStream_t s);
 
@@ -129,14 +146,14 @@ __device__ __forceinline__ int position(const BandArgs& a, Entry e, int query) {
   return p < e.len ? p : -1;
 }
 
-// Positions of the rows row0 .. row1 of a pair, rows of the entry at most: the
-// lowest and the highest that see a key (high < low: none does).
+// Positions of the rows row0 .. row1 of a pair that the entry has: the lowest and the
+// highest that see a key (high < low: none does).
 struct Reach {
   int low, high;
 };
 __device__ __forceinline__ Reach reach_of(const BandArgs& a, Entry e, int row0, int row1) {
   const int last = std::min(std::min(divided(row1, a.by_group), e.n - 1) * e.step + e.shift, e.len - 1);
-  return Reach{divided(row0, a.by_group) * e.step + e.shift, last};
+  return Reach{divided(row0, a.by_group) * e.step + e.shift, row0 < e.n * a.group ? last : -1};
 }
 
 // The tiles of K keys that rows of a reach see, in order: tiles of sinks that lie
@@ -185,18 +202,37 @@ __device__ __forceinline__ int split_size(int n, int splits, int least) {
   return per > least ? per : least;
 }
 
-// Consecutive blocks go to the eight dies in turn; `unit` pairs, all `per` blocks of
-// each, share a die and its L2.
+// Consecutive blocks go to the eight dies in turn; a unit is the pairs of an entry, or one
+// pair, and shares a die and its L2.
 __device__ __forceinline__ bool band_place(const BandArgs& a, int* b, int* h, int* tile, int* split) {
   const int id = block_id(), slot = id >> a.die_bits, turn = divided(slot, a.by_across);
-  const int rest = slot - turn * a.by_across.d, in_unit = divided(rest, a.by_per);
-  const int t = rest - in_unit * a.by_per.d;
+  const int rest = slot - turn * a.by_across.d, outer = divided(rest, a.by_inner);
+  const int inner = rest - outer * a.by_inner.d;
+  const int t = a.pairs_inner ? outer : inner, in_unit = a.pairs_inner ? inner : outer;
   const int pair = ((turn << a.die_bits) + (id & ((1 << a.die_bits) - 1))) * a.unit + in_unit;
   *tile = divided(t, a.by_splits);
   *split = t - *tile * a.by_splits.d;
   *b = divided(pair, a.by_kv_heads);
   *h = pair - *b * a.kv_heads;
   return *b < a.batch;
+}
+
+// The entry that is `rank`th by length, of 64 at most, those without rows last: blocks of a
+// long walk that start late run alone at the end.  Found by every wave for itself, in less
+// than a microsecond.
+__device__ __forceinline__ int entry_of_rank(const BandArgs& a, int rank) {
+  const int lane = threadIdx.x & 63;
+  int mine = -1;
+  if (lane < a.batch) {
+    const Entry e = entry_at<true>(a, lane, false);
+    mine = e.n > 0 ? e.len : -1;
+  }
+  int before = 0;
+  for (int i = 0; i < a.batch; ++i) {
+    const int other = __builtin_amdgcn_readlane(mine, i);
+    before += other > mine || (other == mine && i < lane);
+  }
+  return __ffsll((unsigned long long)__ballot(lane < a.batch && before == rank)) - 1;
 }
 
 // Offset of query q, head g of the group, in a tensor of queries.
@@ -263,6 +299,12 @@ __device__ __forceinline__ f32x16 mma32(f32x8 a, f32x8 b, f32x16 c) {
   for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
   return c;
 }
+// Whether chunk c of a head is worth its products: float32's take eight instructions, of
+// twice bfloat16's length, so those past the head are left out.
+template <typename T>
+__device__ __forceinline__ bool chunk_counts(int c, int dim) {
+  return sizeof(T) == 2 || c * 16 < dim;
+}
 __device__ __forceinline__ f32x16 zeros16() {
   f32x16 z;
 #pragma unroll
@@ -287,6 +329,30 @@ __device__ __forceinline__ Frag<T> half_of(const f32x16& x) {
   const f32x8 y = G == 0 ? __builtin_shufflevector(x, x, 0, 1, 2, 3, 4, 5, 6, 7)
                          : __builtin_shufflevector(x, x, 8, 9, 10, 11, 12, 13, 14, 15);
   return __builtin_convertvector(y, Frag<T>);
+}
+
+// Elements 32 * block .. of a lane's row of a result (columns are rows of the tensor), times
+// `by`.  A lane and the one 32 away hold alternate 4 elements; bfloat16 pairs are exchanged
+// so that each stores 8 in a row.
+template <typename T, bool ALN>
+__device__ __forceinline__ void store_result(T* row, int block, int lane, int dim, const f32x16& x, float by) {
+  if constexpr (ALN && sizeof(T) == 2) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    auto two = [&](int i) { return __builtin_bit_cast(unsigned, bf16x2{(__bf16)(x[i] * by), (__bf16)(x[i + 1] * by)}); };
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      const auto lo = __builtin_amdgcn_permlane32_swap(two(i), two(i + 4), false, false);
+      const auto hi = __builtin_amdgcn_permlane32_swap(two(i + 2), two(i + 6), false, false);
+      const int d0 = block * 32 + 2 * i + 8 * (lane >> 5);
+      if (d0 < dim) *reinterpret_cast<u32x4*>(row + d0) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      store4<T, ALN>(row, block * 32 + result_row(lane, i), dim,
+                     f32x4{x[i] * by, x[i + 1] * by, x[i + 2] * by, x[i + 3] * by});
+  }
 }
 
 // A lane's operands for the KK chunks (16 elements each) of a row that is there; zeros

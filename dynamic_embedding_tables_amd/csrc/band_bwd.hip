@@ -21,15 +21,20 @@
 namespace recis {
 namespace {
 
+// Waves a SIMD of dQ's kernel: its time goes by them (32 entries of up to 4096 positions, 8
+// heads of 64, window 512, bfloat16: 2 265 us, 3 233).
+template <typename T, int DP>
+constexpr int kBackwardWaves = DP > 64 || (sizeof(T) == 4 && DP > 32) ? 2 : sizeof(T) == 2 && DP <= 32 ? 4 : 3;
+
 // dQ, and each row's L (in log2 of the weight) and delta for dK and dV.
 template <typename T, int DP, bool ALN>
-__global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
+__global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_q(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32, K = kBandKeys<T, DP>, KB = K / 32;
   constexpr int kTile = K * kLd<T, DP>;
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, tile, split;
   if (!band_place(a, &b, &h, &tile, &split)) return;
-  zero_spare<T>(a, a.dq, a.dqs, h * a.group, a.group, b, tile * a.q_splits + split, a.by_per.d);
+  zero_spare<T>(a, a.dq, a.dqs, h * a.group, a.group, b, tile * a.q_splits + split, a.per);
   tile = a.row_tiles - 1 - tile;
   const Entry e = entry_at<false>(a, b);
   const int tile_row = tile * kBandRows, rows = e.n * a.group;
@@ -116,6 +121,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
       for (int x = 0; x < 16; ++x) dp[x] = -delta;
 #pragma unroll
       for (int c = 0; c < KK; ++c) {
+        if (!chunk_counts<T>(c, a.head_dim)) continue;
         s = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s);
         dp = mma32(rows32<DP>(tv, n * 32, c, lane), g[c], dp);
       }
@@ -146,20 +152,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_band_bwd_q(BandArgs a) {
   if (walk.n > per) {
     float* to = a.part_o + ((((long long)b * a.kv_heads + h) * a.q_splits + split) * a.rows + r) * a.head_dim;
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int x = 0; x < 16; x += 4)
-        store4<float, false>(to, d * 32 + result_row(lane, x), a.head_dim,
-                             f32x4{dq[d][x], dq[d][x + 1], dq[d][x + 2], dq[d][x + 3]});
+    for (int d = 0; d < DB; ++d) store_result<float, false>(to, d, lane, a.head_dim, dq[d], 1.f);
     return;
   }
   T* to = static_cast<T*>(a.dq) + query_at(a, a.dqs, e, b, h, r);
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int x = 0; x < 16; x += 4)
-      store4<T, ALN>(to, d * 32 + result_row(lane, x), a.head_dim,
-                     f32x4{dq[d][x] * a.scale, dq[d][x + 1] * a.scale, dq[d][x + 2] * a.scale, dq[d][x + 3] * a.scale});
+  for (int d = 0; d < DB; ++d) store_result<T, ALN>(to, d, lane, a.head_dim, dq[d], a.scale);
 }
 
 // Adds the key ranges' parts of dQ, in order: V elements of a row a thread.
@@ -197,57 +195,34 @@ __global__ __launch_bounds__(kThreads) void k_band_join_q(BandArgs a) {
 template <int DP, bool FAR>
 constexpr int kWalkRows = FAR ? 128 : DP <= 64 ? 64 : 32;
 
-// Walks a thread's chunks of the folded rows of Q and dO, from row `first` on.
-template <typename T, int DP, int R, bool ALN>
+// A thread's chunks of R folded rows of Q and dO on their way to LDS.  Rows from `until` on
+// are loaded from the one before it and zeroed by store(): no load stands behind a branch.
+// OWN: each wave stages 32 rows of its own.
+template <typename T, int DP, int R, bool OWN, bool ALN>
 struct RowStage {
-  static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = R / kStep;
-  static_assert(R % kStep == 0, "every thread has the same number of chunks");
+  static constexpr int kAcross = kCols<DP> / 8, kStep = (OWN ? 64 : kThreads) / kAcross, kPer = (OWN ? 32 : R) / kStep;
+  static_assert((OWN ? 32 : R) % kStep == 0, "every thread has the same number of chunks");
   Frag<T> fq[kPer], fg[kPer];
-  const T *pq[kPer], *pg[kPer];  // of the row that comes next
-  const T *first_q, *first_g;    // of a row that is there
-  int head[kPer];                // the next row's head in the group
   int row, d0, here;
-  __device__ __forceinline__ void start(const BandArgs& a, Entry e, int b, int h, int first) {
-    row = threadIdx.x / kAcross;
+  __device__ __forceinline__ void start() {
+    row = OWN ? wave_of() * 32 + (threadIdx.x & 63) / kAcross : threadIdx.x / kAcross;
     d0 = (threadIdx.x % kAcross) * 8;
-    first_q = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, first);
-    first_g = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, first);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = first + row + i * kStep;
-      head[i] = r - divided(r, a.by_group) * a.group;
-      pq[i] = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, r);
-      pg[i] = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, r);
-    }
   }
-  // `left` rows from the next one on exist: the others are zero, or loaded from a row
-  // that is there and zeroed by store() (no load stands behind a branch)
-  __device__ __forceinline__ void load(const BandArgs& a, int left) {
-    const int dq = divided(R, a.by_group), dh = R - dq * a.group;  // R rows on
+  __device__ __forceinline__ void load(const BandArgs& a, Entry e, int b, int h, int first, int until) {
     const int d = d0 < a.head_dim ? d0 : 0;
-    here = left;
+    here = until - first;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const bool in = row + i * kStep < left;
+      const int r = std::min(first + row + i * kStep, until - 1);
+      const T* pq = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, r);
+      const T* pg = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, r);
       if constexpr (ALN) {
-        fq[i] = *reinterpret_cast<const Frag<T>*>((in ? pq[i] : first_q) + d);
-        fg[i] = *reinterpret_cast<const Frag<T>*>((in ? pg[i] : first_g) + d);
+        fq[i] = *reinterpret_cast<const Frag<T>*>(pq + d);
+        fg[i] = *reinterpret_cast<const Frag<T>*>(pg + d);
       } else {
-        fq[i] = load8<T, ALN>(pq[i], d0, a.head_dim, in);
-        fg[i] = load8<T, ALN>(pg[i], d0, a.head_dim, in);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      pq[i] += dq * a.qs[1] + dh * a.qs[2];
-      pg[i] += dq * a.dos[1] + dh * a.dos[2];
-      if (dh) {
-        head[i] += dh;
-        if (head[i] >= a.group) {
-          head[i] -= a.group;
-          pq[i] += a.qs[1] - a.group * a.qs[2];
-          pg[i] += a.dos[1] - a.group * a.dos[2];
-        }
+        const bool in = row + i * kStep < here;
+        fq[i] = load8<T, false>(pq, d0, a.head_dim, in);
+        fg[i] = load8<T, false>(pg, d0, a.head_dim, in);
       }
     }
   }
@@ -283,7 +258,7 @@ template <typename T, int DP, bool ALN, bool FAR>
 __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32;
   constexpr int R = kWalkRows<DP, FAR>, kTile = R * kLd<T, DP>;
-  // (the far walk's 128 rows fit once; they are staged between two barriers)
+  // (the far walk's waves have rows of their own, so one buffer and no barrier)
   constexpr int kBuffers = FAR ? 1 : 2;
   constexpr int kTileBytes = kBuffers * 2 * kTile * (int)sizeof(T);
   constexpr int kJoinBytes = FAR ? 32 * DP * 4 : 0;
@@ -297,8 +272,8 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
   const long long pair = (long long)b * a.kv_heads + h;
   const int lane = threadIdx.x & 63, wave = wave_of();
   if constexpr (!FAR) {
-    zero_spare<T>(a, a.dk, a.dks, h, 1, b, tile * splits + split, a.by_per.d);
-    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, tile * splits + split, a.by_per.d);
+    zero_spare<T>(a, a.dk, a.dks, h, 1, b, tile * splits + split, a.per);
+    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, tile * splits + split, a.per);
   }
   const Entry e = entry_at<false>(a, b);
   const int block_key = FAR ? tile * 32 : tile * kTileKeys128;
@@ -327,16 +302,17 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
   for (int d = 0; d < DB; ++d) dk[d] = dv[d] = zeros16();
   const f32x2* row_stats = a.stats + pair * a.rows;
   const f32x2 none{INFINITY, 0.f};  // rows that do not exist: weight 0
-  RowStage<T, DP, R, ALN> st;
+  RowStage<T, DP, R, FAR, ALN> st;
   f32x2 stat = none;
-  auto load = [&](int first) {  // (past the last step: that one's first row again)
-    const int left = until - first;
-    st.load(a, left);
-    stat = row_stats[(int)threadIdx.x < left ? first + threadIdx.x : from];
-    if ((int)threadIdx.x >= left) stat = none;
+  // the row whose L and delta the thread takes (twice over in a wave of its own rows)
+  const int stat_row = FAR ? wave * 32 + (lane & 31) : (int)threadIdx.x;
+  auto load = [&](int first) {  // (past the last row: that one again)
+    st.load(a, e, b, h, first, until);
+    stat = row_stats[std::min(first + stat_row, until - 1)];
+    if (first + stat_row >= until) stat = none;
   };
   if (s0 < s1) {
-    st.start(a, e, b, h, from + s0 * R);
+    st.start();
     load(from + s0 * R);
   }
   if (e.len > 0) {  // (a key that does not count spoils its own column only, which is zero at the end)
@@ -349,14 +325,16 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
     const int first = from + step * R;
     T* tq = tiles + buffer * 2 * kTile;
     T* tg = tq + kTile;
-    if (FAR && step > s0) __syncthreads();
     st.store(a, tq, tg);
-    if (threadIdx.x < R) {
-      stat_l[buffer][threadIdx.x] = stat[0];
-      stat_d[buffer][threadIdx.x] = -stat[1];
-      stat_p[buffer][threadIdx.x] = divided(first + (int)threadIdx.x, a.by_group);
+    if (stat_row < R) {
+      stat_l[buffer][stat_row] = stat[0];
+      stat_d[buffer][stat_row] = -stat[1];
+      stat_p[buffer][stat_row] = divided(first + stat_row, a.by_group);
     }
-    __syncthreads();
+    if constexpr (FAR)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are executed in order
+    else
+      __syncthreads();
     load(first + R);
 #pragma unroll
     for (int n0 = 0; n0 < (FAR ? 32 : R); n0 += 32) {
@@ -376,6 +354,7 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
       }
 #pragma unroll
       for (int c = 0; c < KK; ++c) {
+        if (!chunk_counts<T>(c, a.head_dim)) continue;
         s = mma32(rows32<DP>(tq, n, c, lane), k[c], s);
         dp = mma32(rows32<DP>(tg, n, c, lane), v[c], dp);
       }
@@ -406,6 +385,7 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
         dk[d] = mma32(cols32<DP>(tq, n + 16, d * 32, lane), d1, dk[d]);
       }
     }
+    if constexpr (FAR) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   if constexpr (FAR) {
     // the waves' sums, one wave after the other, dK and then dV
@@ -424,7 +404,8 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
           }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < 32 * a.head_dim; i += kThreads) {
+      const int keys = std::min(32, a.sinks - block_key);
+      for (int i = threadIdx.x; i < keys * a.head_dim; i += kThreads) {
         const int at_key = i / a.head_dim, d = i - at_key * a.head_dim;
         part_far(a, pair, split, block_key + at_key)[half * a.head_dim + d] = sums[d * 32 + at_key];
       }
@@ -436,27 +417,20 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
     if (a.kv_splits > 1 || sink) {
       float* to = part_near(a, pair, split, key);
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int x = 0; x < 16; x += 4) {
-          const int d0 = d * 32 + result_row(lane, x);
-          store4<float, false>(to, d0, a.head_dim, f32x4{dk[d][x], dk[d][x + 1], dk[d][x + 2], dk[d][x + 3]});
-          store4<float, false>(to + a.head_dim, d0, a.head_dim, f32x4{dv[d][x], dv[d][x + 1], dv[d][x + 2], dv[d][x + 3]});
-        }
+      for (int d = 0; d < DB; ++d) {
+        store_result<float, false>(to, d, lane, a.head_dim, dk[d], 1.f);
+        store_result<float, false>(to + a.head_dim, d, lane, a.head_dim, dv[d], 1.f);
+      }
       return;
     }
     T* tk = static_cast<T*>(a.dk) + keys_at(a, a.dks, e, b, h) + (long long)key * a.dks[1];
     T* tv = static_cast<T*>(a.dv) + keys_at(a, a.dvs, e, b, h) + (long long)key * a.dvs[1];
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int x = 0; x < 16; x += 4) {
-        const int d0 = d * 32 + result_row(lane, x);
-        f32x4 xk{dk[d][x], dk[d][x + 1], dk[d][x + 2], dk[d][x + 3]};
-        f32x4 xv{dv[d][x], dv[d][x + 1], dv[d][x + 2], dv[d][x + 3]};
-        store4<T, ALN>(tk, d0, a.head_dim, in ? xk * a.scale : f32x4{0.f, 0.f, 0.f, 0.f});
-        store4<T, ALN>(tv, d0, a.head_dim, in ? xv : f32x4{0.f, 0.f, 0.f, 0.f});
-      }
+    for (int d = 0; d < DB; ++d) {
+      if (!in) dk[d] = dv[d] = zeros16();
+      store_result<T, ALN>(tk, d, lane, a.head_dim, dk[d], a.scale);
+      store_result<T, ALN>(tv, d, lane, a.head_dim, dv[d], 1.f);
+    }
   }
 }
 
@@ -548,7 +522,7 @@ void launch_bwd_dp(bool aln, const BandArgs& a, hipStream_t s) {
   }
 }
 
-constexpr int kMaxSplits = 256, kPairsForDies = 128;
+constexpr int kMaxSplits = 256;
 
 recis_status check_self(const recis_self_attn_desc* d) {
   if (!d || !dtype_known(d->dtype) || d->batch < 0 || d->len < 0 || d->q_heads < 1 || d->kv_heads < 1 ||
@@ -583,7 +557,7 @@ SelfPlan self_plan(const recis_self_attn_desc* d) {
   p.row_tiles = std::max<int64_t>(1, (rows + kBandRows - 1) / kBandRows);
   p.key_tiles = std::max(1, (d->len + kTileKeys128 - 1) / kTileKeys128);
   const int64_t near = band ? (int64_t)d->window + kBandRows / group + 1 + p.sinks : d->len;
-  const int64_t walk = std::min<int64_t>(d->len, near) / keys + 2;
+  const int64_t walk = d->len ? std::min<int64_t>(d->len, near) / keys + 2 : 0;  // (no keys: packed rows of no entry)
   // keys (rows) are split until there are `want` blocks
   auto split = [&](int64_t blocks, int64_t want, int64_t most) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, want / std::max<int64_t>(1, blocks), most}));
@@ -596,7 +570,7 @@ SelfPlan self_plan(const recis_self_attn_desc* d) {
   if (p.sinks > 0 && p.sinks <= kMostFarSinks) {
     p.far_keys = round_up(p.sinks, 32);
     p.part_keys = p.far_keys;
-    // 8 steps of 128 rows a part, more where that leaves the chip empty
+    // parts of 8 steps of 128 rows, less where that leaves the chip empty
     const int64_t steps = std::max<int64_t>(1, rows / 128);
     p.sink_splits = (int)std::max<int64_t>(
         1, std::min<int64_t>({64, steps, std::max<int64_t>(steps / 8, 512 / std::max<int64_t>(1, pairs))}));
@@ -611,7 +585,7 @@ SelfPlan self_plan(const recis_self_attn_desc* d) {
   if (p.part_keys)
     p.bwd_bytes += round_up(std::max<int64_t>(pairs, 1) * (p.kv_splits * p.part_keys + p.sink_splits * p.far_keys) * 2 *
                                 d->head_dim * 4, 256);
-  auto fits = [&](int64_t per) { return round_up(pairs, kDies) * per <= kMaxBlocks; };
+  auto fits = [&](int64_t per) { return round_up(pairs, (int64_t)kDies * d->kv_heads) * per <= kMaxBlocks; };
   p.launchable[0] = fits((int64_t)p.row_tiles * p.splits);
   p.launchable[1] = p.launchable[0] && fits((int64_t)p.key_tiles * p.kv_splits) &&
                     fits(std::max<int64_t>(1, p.far_keys / 32) * std::max(1, p.sink_splits)) &&
@@ -658,8 +632,7 @@ void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
   a->sink_splits = p.sink_splits;
   a->part_keys = (int)p.part_keys;
   a->far_keys = (int)p.far_keys;
-  a->unit = 1;
-  a->die_bits = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDieBits : 0;
+  place_pairs(a, d->dtype);
   a->scale = d->scale;
 }
 

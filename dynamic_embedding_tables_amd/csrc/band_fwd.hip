@@ -32,7 +32,8 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   __shared__ __attribute__((aligned(128))) T tiles[4 * kTile];
   int b, h, tile, split;
   if (!band_place(a, &b, &h, &tile, &split)) return;
-  if constexpr (!PAGED) zero_spare<T>(a, a.out, a.os, h * a.group, a.group, b, tile * a.splits + split, a.by_per.d);
+  if (PAGED && a.ranked) b = entry_of_rank(a, b);
+  if constexpr (!PAGED) zero_spare<T>(a, a.out, a.os, h * a.group, a.group, b, tile * a.splits + split, a.per);
   tile = a.row_tiles - 1 - tile;  // the last rows see the most keys: they start first
   const Entry e = entry_at<PAGED>(a, b);
   const int tile_row = tile * kBandRows, rows = e.n * a.group;
@@ -95,7 +96,8 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     auto scores = [&](int n) {
       s[n] = zeros16();
 #pragma unroll
-      for (int c = 0; c < KK; ++c) s[n] = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s[n]);
+      for (int c = 0; c < KK; ++c)
+        if (chunk_counts<T>(c, a.head_dim)) s[n] = mma32(rows32<DP>(tk, n * 32, c, lane), q[c], s[n]);
     };
     auto mask = [&](int n) {
       const int at = first + n * 32;
@@ -173,11 +175,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     const long long at = (((long long)b * a.kv_heads + h) * a.splits + split) * a.rows + r;
     float* po = a.part_o + at * a.head_dim;
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int x = 0; x < 16; x += 4)
-        store4<float, false>(po, d * 32 + result_row(lane, x), a.head_dim,
-                             f32x4{o[d][x], o[d][x + 1], o[d][x + 2], o[d][x + 3]});
+    for (int d = 0; d < DB; ++d) store_result<float, false>(po, d, lane, a.head_dim, o[d], 1.f);
     if (lane < 32) {
       a.part_ml[2 * at] = m * c2;
       a.part_ml[2 * at + 1] = l;
@@ -187,11 +185,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* out = static_cast<T*>(a.out) + query_at(a, a.os, e, b, h, r);
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int x = 0; x < 16; x += 4)
-      store4<T, ALN>(out, d * 32 + result_row(lane, x), a.head_dim,
-                     f32x4{o[d][x] * inv, o[d][x + 1] * inv, o[d][x + 2] * inv, o[d][x + 3] * inv});
+  for (int d = 0; d < DB; ++d) store_result<T, ALN>(out, d, lane, a.head_dim, o[d], inv);
   if (a.lse && lane < 32) a.lse[lse_at(a, e, b, h, r)] = l == 0.f ? -INFINITY : m * a.scale + __logf(l);
 }
 

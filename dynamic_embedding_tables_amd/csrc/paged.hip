@@ -273,7 +273,7 @@ void launch_few_dp(bool aln, const BandArgs& a, hipStream_t s) {
 }
 
 // ----------------------------------------------------------- sizes, launches
-constexpr int kMaxSplits = 256, kEntriesForDies = 64, kPairsForDies = 128;
+constexpr int kMaxSplits = 256;
 
 struct PagedPlan {
   bool few;
@@ -400,8 +400,8 @@ recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* d, const void* q,
   a.by_kv_heads = Quick(d->kv_heads);
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
-  a.unit = p.row_tiles <= 1 && d->batch >= kEntriesForDies ? d->kv_heads : 1;
-  a.die_bits = (int64_t)d->batch * d->kv_heads >= kPairsForDies ? kDieBits : 0;
+  a.ranked = !p.few && !d->window && d->batch > 1 && d->batch <= 64;
+  place_pairs(&a, d->dtype);
   a.scale = d->scale;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
