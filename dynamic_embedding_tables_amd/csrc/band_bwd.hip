@@ -601,15 +601,17 @@ void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
   a->error = d->error;
   a->mask_stride = d->mask_stride;
   a->total_rows = d->rows;
+  const int64_t lead[2] = {d->offsets ? 1 : d->batch, d->offsets ? d->rows : d->len};
+  const int64_t q_axes[3] = {lead[0], lead[1], d->q_heads}, kv_axes[3] = {lead[0], lead[1], d->kv_heads};
   for (int i = 0; i < 3; ++i) {
-    a->qs[i] = d->q_strides[i];
-    a->ks[i] = d->k_strides[i];
-    a->vs[i] = d->v_strides[i];
-    a->os[i] = d->o_strides[i];
-    a->dos[i] = d->do_strides[i];
-    a->dqs[i] = d->dq_strides[i];
-    a->dks[i] = d->dk_strides[i];
-    a->dvs[i] = d->dv_strides[i];
+    a->qs[i] = stride_of(d->q_strides[i], q_axes[i]);
+    a->ks[i] = stride_of(d->k_strides[i], kv_axes[i]);
+    a->vs[i] = stride_of(d->v_strides[i], kv_axes[i]);
+    a->os[i] = stride_of(d->o_strides[i], q_axes[i]);
+    a->dos[i] = stride_of(d->do_strides[i], q_axes[i]);
+    a->dqs[i] = stride_of(d->dq_strides[i], q_axes[i]);
+    a->dks[i] = stride_of(d->dk_strides[i], kv_axes[i]);
+    a->dvs[i] = stride_of(d->dv_strides[i], kv_axes[i]);
   }
   a->batch = d->batch;
   a->q_len = a->max_len = d->len;
@@ -637,17 +639,17 @@ void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
 }
 
 // Rows can be moved 16 bytes at a time.
-bool self_aligned(const recis_self_attn_desc* d, std::initializer_list<const void*> ptrs,
-                  std::initializer_list<const int64_t*> strides) {
-  const int per = 16 / dtype_size(d->dtype);
-  if (d->head_dim % 8) return false;
+bool self_aligned(int dtype, const BandArgs& a, std::initializer_list<const void*> ptrs,
+                  std::initializer_list<const long long*> strides) {
+  const int per = 16 / dtype_size(dtype);
+  if (a.head_dim % 8) return false;
   for (const void* p : ptrs)
     if (!aligned_to(p, 16)) return false;
-  for (const int64_t* s : strides)
+  for (const long long* s : strides)
     for (int i = 0; i < 3; ++i)
       if (s[i] % per) return false;
   // a tile's rows stay within 32 bits of byte offset
-  for (const int64_t* s : {d->k_strides, d->v_strides})
+  for (const long long* s : {a.ks, a.vs})
     if (s[1] < 0 || s[1] >= (1 << 23)) return false;
   return true;
 }
@@ -691,8 +693,7 @@ recis_status recis_self_attn_fwd(const recis_self_attn_desc* desc, const void* q
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
-  const bool aln = self_aligned(desc, {q, k, v, out},
-                                {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides});
+  const bool aln = self_aligned(desc->dtype, a, {q, k, v, out}, {a.qs, a.ks, a.vs, a.os});
   launch_band_fwd(desc->dtype, false, aln, a, s);
   return launch_status();
 }
@@ -722,9 +723,8 @@ recis_status recis_self_attn_bwd(const recis_self_attn_desc* desc, const void* g
   a.stats = static_cast<f32x2*>(workspace);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.dq_at);
   a.part_kv = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.kv_at);
-  const bool aln = self_aligned(desc, {q, k, v, out, grad_out, grad_q, grad_k, grad_v},
-                                {desc->q_strides, desc->k_strides, desc->v_strides, desc->o_strides,
-                                 desc->do_strides, desc->dq_strides, desc->dk_strides, desc->dv_strides});
+  const bool aln = self_aligned(desc->dtype, a, {q, k, v, out, grad_out, grad_q, grad_k, grad_v},
+                                {a.qs, a.ks, a.vs, a.os, a.dos, a.dqs, a.dks, a.dvs});
   if (desc->dtype == RECIS_DTYPE_BF16)
     launch_bwd_dp<__bf16>(aln, a, s);
   else

@@ -324,16 +324,16 @@ bool paged_grid_fits(const recis_paged_attn_desc* d, const PagedPlan& p) {
 }
 
 // Rows can be moved 16 bytes at a time.
-bool paged_aligned(const recis_paged_attn_desc* d, std::initializer_list<const void*> ptrs) {
-  const int per = 16 / dtype_size(d->dtype);
-  if (d->head_dim % 8) return false;
+bool paged_aligned(int dtype, const BandArgs& a, std::initializer_list<const void*> ptrs) {
+  const int per = 16 / dtype_size(dtype);
+  if (a.head_dim % 8) return false;
   for (const void* p : ptrs)
     if (!aligned_to(p, 16)) return false;
-  for (const int64_t* s : {d->q_strides, d->o_strides, d->k_strides, d->v_strides})
+  for (const long long* s : {a.qs, a.os, a.ks, a.vs})
     for (int i = 0; i < 3; ++i)
       if (s[i] % per) return false;
   // a wave's slots stay within 32 bits of byte offset
-  for (const int64_t* s : {d->k_strides, d->v_strides})
+  for (const long long* s : {a.ks, a.vs})
     if (s[1] < 0 || s[1] >= (1 << 23) || s[0] < 0 || s[0] >= (1ll << 31)) return false;
   return true;
 }
@@ -378,11 +378,13 @@ recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* d, const void* q,
   a.total_rows = d->q_rows;
   a.table_stride = d->table_stride;
   a.pages = d->pages;
+  const int64_t q_axes[3] = {d->q_offsets ? 1 : d->batch, d->q_offsets ? d->q_rows : d->q_len, d->q_heads};
+  const int64_t cache_axes[3] = {d->pages, d->page_size, d->kv_heads};
   for (int i = 0; i < 3; ++i) {
-    a.qs[i] = d->q_strides[i];
-    a.os[i] = d->o_strides[i];
-    a.ks[i] = d->k_strides[i];
-    a.vs[i] = d->v_strides[i];
+    a.qs[i] = stride_of(d->q_strides[i], q_axes[i]);
+    a.os[i] = stride_of(d->o_strides[i], q_axes[i]);
+    a.ks[i] = stride_of(d->k_strides[i], cache_axes[i]);
+    a.vs[i] = stride_of(d->v_strides[i], cache_axes[i]);
   }
   a.batch = d->batch;
   a.q_len = d->q_len;
@@ -405,7 +407,7 @@ recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* d, const void* q,
   a.scale = d->scale;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
-  const bool aln = paged_aligned(d, {q, out, k_cache, v_cache});
+  const bool aln = paged_aligned(d->dtype, a, {q, out, k_cache, v_cache});
   if (!p.few)
     launch_band_fwd(d->dtype, true, aln, a, s);
   else if (d->dtype == RECIS_DTYPE_BF16)

@@ -350,9 +350,10 @@ recis_status recis_rotary(const recis_rotary_desc* d, int32_t backward, const vo
   a.tokens = d->batch * d->seq;
   a.seq = d->seq;
   bool same = x == out;
+  const int64_t axes[3] = {d->batch, d->seq, d->heads};
   for (int i = 0; i < 3; ++i) {
-    a.xs[i] = d->x_strides[i];
-    a.os[i] = d->out_strides[i];
+    a.xs[i] = stride_of(d->x_strides[i], axes[i]);
+    a.os[i] = stride_of(d->out_strides[i], axes[i]);
     same = same && a.xs[i] == a.os[i];
   }
   a.ps[0] = d->pos_strides[0];
@@ -410,13 +411,16 @@ recis_status recis_cache_append(const recis_append_desc* d, const void* q, const
   a.rows = rows;
   a.table_stride = d->table_stride;
   a.pages = d->pages;
+  const int64_t lead[2] = {d->q_offsets ? 1 : d->batch, d->q_offsets ? rows : d->new_len};
+  const int64_t q_axes[3] = {lead[0], lead[1], d->q_heads}, kv_axes[3] = {lead[0], lead[1], d->kv_heads};
+  const int64_t cache_axes[3] = {d->pages, d->page_size, d->kv_heads};
   for (int i = 0; i < 3; ++i) {
-    a.qs[i] = d->q_strides[i];
-    a.qos[i] = d->q_out_strides[i];
-    a.ks[i] = d->k_strides[i];
-    a.vs[i] = d->v_strides[i];
-    a.kcs[i] = d->k_cache_strides[i];
-    a.vcs[i] = d->v_cache_strides[i];
+    a.qs[i] = stride_of(d->q_strides[i], q_axes[i]);
+    a.qos[i] = stride_of(d->q_out_strides[i], q_axes[i]);
+    a.ks[i] = stride_of(d->k_strides[i], kv_axes[i]);
+    a.vs[i] = stride_of(d->v_strides[i], kv_axes[i]);
+    a.kcs[i] = stride_of(d->k_cache_strides[i], cache_axes[i]);
+    a.vcs[i] = stride_of(d->v_cache_strides[i], cache_axes[i]);
   }
   a.batch = d->batch;
   a.new_len = d->new_len;

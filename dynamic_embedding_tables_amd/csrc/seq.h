@@ -106,6 +106,9 @@ inline int access_width(int size, int64_t dim, std::initializer_list<const void*
   return v;
 }
 
+// A stride, or 0 for an axis of one element, whose stride may be any.
+inline int64_t stride_of(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
+
 inline int dtype_size(int dtype) { return dtype == RECIS_DTYPE_BF16 ? 2 : 4; }
 inline bool dtype_known(int dtype) { return dtype == RECIS_DTYPE_F32 || dtype == RECIS_DTYPE_BF16; }
 

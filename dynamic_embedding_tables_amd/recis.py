@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Iterable, List, Optional, Sequence
 
 import numpy as np
@@ -149,6 +150,20 @@ class recis_self_attn_desc(C.Structure):
                 ("error", C.c_void_p)]
 
 
+def _packer(cls):
+    """cls's values, in the order of its fields, to its bytes: a call's description in one step, where setting a
+    structure's twenty fields takes longer than the call's work on the GPU.  (Pointers: 0 for none.)"""
+    code = {C.c_int32: "i", C.c_float: "f", C.c_int64: "q", C.c_void_p: "P", C.c_int64 * 2: "2q", C.c_int64 * 3: "3q"}
+    form = "@" + "".join(code[f[1]] for f in cls._fields_)
+    return struct.Struct(form + "x" * (C.sizeof(cls) - struct.calcsize(form))).pack
+
+
+pack_rotary_desc = _packer(recis_rotary_desc)
+pack_append_desc = _packer(recis_append_desc)
+pack_paged_attn_desc = _packer(recis_paged_attn_desc)
+pack_self_attn_desc = _packer(recis_self_attn_desc)
+
+
 class RecisError(RuntimeError):
     def __init__(self, status: int, where: str = ""):
         self.status = int(status)
@@ -253,7 +268,8 @@ def _stream(stream=None):
     global _raw_stream, _current_device
     if _raw_stream is None:
         import torch
-        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        torch.cuda.current_device()   # (initialises what the two below take for granted)
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     return _raw_stream(_current_device())
 
 
@@ -493,42 +509,52 @@ def recis_cross_attn_bwd(desc: recis_attn_desc, grad_out, q, k, v, out, lse, gra
         _stream(stream)), "recis_cross_attn_bwd")
 
 
-def recis_rotary(desc: recis_rotary_desc, backward: bool, x, out, stream=None):
-    _check(load_library().recis_rotary(C.byref(desc), 1 if backward else 0, x.data_ptr(), out.data_ptr(),
-                                       _stream(stream)), "recis_rotary")
+# (a description is its structure or, as the pack_* functions make them, its bytes)
+def _ref(desc):
+    return desc if type(desc) is bytes else C.byref(desc)
 
 
-def recis_cache_append(desc: recis_append_desc, q, k, v, q_out, k_cache, v_cache, stream=None):
-    _check(load_library().recis_cache_append(
-        C.byref(desc), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-        _stream(stream)), "recis_cache_append")
+def recis_rotary(desc, backward: bool, x, out, stream=None):
+    st = (_lib or load_library()).recis_rotary(_ref(desc), 1 if backward else 0, x.data_ptr(), out.data_ptr(),
+                                               _stream(stream))
+    if st:
+        _check(st, "recis_rotary")
 
 
-def recis_paged_attn_workspace_bytes(desc: recis_paged_attn_desc) -> int:
-    return int(load_library().recis_paged_attn_workspace_bytes(C.byref(desc)))
+def recis_cache_append(desc, q, k, v, q_out, k_cache, v_cache, stream=None):
+    st = (_lib or load_library()).recis_cache_append(
+        _ref(desc), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+        _stream(stream))
+    if st:
+        _check(st, "recis_cache_append")
 
 
-def recis_paged_attn_fwd(desc: recis_paged_attn_desc, q, k_cache, v_cache, out, lse, workspace, workspace_bytes: int,
-                         stream=None):
-    _check(load_library().recis_paged_attn_fwd(
-        C.byref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse),
-        _ptr(workspace), workspace_bytes, _stream(stream)), "recis_paged_attn_fwd")
+def recis_paged_attn_workspace_bytes(desc) -> int:
+    return (_lib or load_library()).recis_paged_attn_workspace_bytes(_ref(desc))
 
 
-def recis_self_attn_workspace_bytes(desc: recis_self_attn_desc, backward: bool) -> int:
-    return int(load_library().recis_self_attn_workspace_bytes(C.byref(desc), 1 if backward else 0))
+def recis_paged_attn_fwd(desc, q, k_cache, v_cache, out, lse, workspace, workspace_bytes: int, stream=None):
+    st = (_lib or load_library()).recis_paged_attn_fwd(
+        _ref(desc), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse),
+        _ptr(workspace), workspace_bytes, _stream(stream))
+    if st:
+        _check(st, "recis_paged_attn_fwd")
 
 
-def recis_self_attn_fwd(desc: recis_self_attn_desc, q, k, v, out, lse, workspace, workspace_bytes: int, stream=None):
+def recis_self_attn_workspace_bytes(desc, backward: bool) -> int:
+    return load_library().recis_self_attn_workspace_bytes(_ref(desc), 1 if backward else 0)
+
+
+def recis_self_attn_fwd(desc, q, k, v, out, lse, workspace, workspace_bytes: int, stream=None):
     _check(load_library().recis_self_attn_fwd(
-        C.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(workspace),
+        _ref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(workspace),
         workspace_bytes, _stream(stream)), "recis_self_attn_fwd")
 
 
-def recis_self_attn_bwd(desc: recis_self_attn_desc, grad_out, q, k, v, out, lse, grad_q, grad_k, grad_v, workspace,
-                        workspace_bytes: int, stream=None):
+def recis_self_attn_bwd(desc, grad_out, q, k, v, out, lse, grad_q, grad_k, grad_v, workspace, workspace_bytes: int,
+                        stream=None):
     _check(load_library().recis_self_attn_bwd(
-        C.byref(desc), grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        _ref(desc), grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
         grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), workspace.data_ptr(), workspace_bytes,
         _stream(stream)), "recis_self_attn_bwd")
 

@@ -349,16 +349,18 @@ def cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens=None, kv_offse
 
 # --------------------------------------------------------- rotary positions
 def _st(t):
-    """Strides of (batch entry, position, head) or (page, slot, head); axes of one element have none."""
-    s = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
+    """Strides of (batch entry, position, head) or (page, slot, head)."""
+    s = t.stride()
     return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
 def _serves(name: str, *tensors):
     """Checks of a call that serves only: it has no backward pass."""
     _on_gpu(*tensors)
+    if not torch.is_grad_enabled():
+        return
     for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
+        if t is not None and t.requires_grad:
             warnings.warn(f"sequence.{name} is for serving and has no backward pass: pass detached tensors or work "
                           "under torch.no_grad()", stacklevel=3)
             return
@@ -366,11 +368,11 @@ def _serves(name: str, *tensors):
 
 def _head_tensor(name: str, t, shape, dtype):
     """An output or a cache given by the caller: head vectors contiguous, no element twice."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if (t.shape[-1] > 1 and t.stride(-1) != 1) or any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+    if not t.is_contiguous() and ((t.shape[-1] > 1 and t.stride(-1) != 1) or any(
+            st == 0 and n > 1 for st, n in zip(t.stride(), t.shape))):
         raise ValueError(f"{name} is written in place: its head vectors must be contiguous and no axis expanded")
-    return t
 
 
 def _freqs(freqs, head_dim: int) -> int:
@@ -416,28 +418,27 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
 def _rotary(x, freqs, positions, interleaved, amplitude, out, backward):
     if x.dim() not in (3, 4):
         raise ValueError("x must be [seq, heads, head_dim] or [batch, seq, heads, head_dim]")
-    d = recis.recis_rotary_desc()
-    d.dtype = _dtype("x", x)
+    dtype = _dtype("x", x)
     heads, head_dim = x.shape[-2:]
-    d.rot_dim = _freqs(freqs, head_dim)
+    rot_dim = _freqs(freqs, head_dim)
     x = _heads(x)
     if out is None:
         out = _like(x)
     else:
         _head_tensor("out", out, x.shape, x.dtype)
-    d.heads, d.head_dim = recis.int32(heads), recis.int32(head_dim)
-    d.batch, d.seq = (x.shape[0] if x.dim() == 4 else 1), x.shape[-3]
-    d.interleaved, d.amplitude = 1 if interleaved else 0, amplitude
-    if d.rot_dim:
-        d.freqs = freqs.data_ptr()
+    batch, seq = (x.shape[0] if x.dim() == 4 else 1), x.shape[-3]
+    at, at_strides = 0, (0, 0)
     if positions is not None:
-        if positions.dtype != torch.int64 or tuple(positions.shape) not in (tuple(x.shape[:-2]), (d.seq,)):
-            raise ValueError(f"positions must be int64 {list(x.shape[:-2])} or [{d.seq}]")
-        d.positions = positions.data_ptr()
-        d.pos_strides[:] = positions.stride() if positions.dim() == 2 else (0, *positions.stride())
-    d.x_strides[:], d.out_strides[:] = _st(x), _st(out)
+        if positions.dtype != torch.int64 or positions.shape not in (x.shape[:-2], x.shape[-3:-2]):
+            raise ValueError(f"positions must be int64 {list(x.shape[:-2])} or [{seq}]")
+        at, at_strides = positions.data_ptr(), positions.stride()
+        if len(at_strides) == 1:
+            at_strides = (0, *at_strides)
     if x.numel():
-        recis.recis_rotary(d, backward, x, out)
+        desc = recis.pack_rotary_desc(dtype, recis.int32(heads), recis.int32(head_dim), rot_dim,
+                                      1 if interleaved else 0, amplitude, batch, seq,
+                                      freqs.data_ptr() if rot_dim else 0, at, *at_strides, *_st(x), *_st(out))
+        recis.recis_rotary(desc, backward, x, out)
     return out
 
 
@@ -464,25 +465,22 @@ def rotary_backward(grad_out, freqs, positions=None, interleaved: bool = False, 
 
 
 # -------------------------------------------------------------- paged cache
-def _paged(d, k_cache, v_cache, page_table, kv_lens, q_offsets, batch, rows, error):
-    """What both calls on a cache check and describe alike; returns what has to stay."""
+def _paged(k_cache, v_cache, page_table, kv_lens, q_offsets, batch, error):
+    """What both calls on a cache check alike: contiguous (page_table, kv_lens, q_offsets)."""
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must both be [pages, page_size, kv_heads, head_dim] of one type")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch:
         raise ValueError(f"page_table must be int32 [{batch}, pages an entry may have]")
-    keep = [page_table if page_table.shape[1] <= 1 or page_table.stride(1) == 1 else page_table.contiguous(),
-            _index("kv_lens", kv_lens, torch.int32, (batch,))]
-    d.batch = recis.int32(batch)
-    d.page_size, d.pages = recis.int32(k_cache.shape[1]), k_cache.shape[0]
-    d.table_width = recis.int32(page_table.shape[1])
-    d.table_stride = keep[0].stride(0) if batch > 1 else page_table.shape[1]
-    d.page_table, d.kv_lens = keep[0].data_ptr(), keep[1].data_ptr()
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        page_table = page_table.contiguous()
+    if kv_lens.dtype != torch.int32 or kv_lens.shape != (batch,):
+        raise ValueError(f"kv_lens must be torch.int32 [{batch}], not {kv_lens.dtype} {list(kv_lens.shape)}")
     if q_offsets is not None:
-        keep.append(_index("q_offsets", q_offsets, torch.int32, (batch + 1,)))
-        d.q_offsets = keep[-1].data_ptr()
-    if error is not None:
-        d.error = _error_word(error).data_ptr()
-    return keep
+        if q_offsets.dtype != torch.int32 or q_offsets.dim() != 1:
+            raise ValueError("q_offsets must be int32 [batch + 1]")
+        q_offsets = q_offsets.contiguous()
+    _error_word(error)
+    return page_table, kv_lens.contiguous(), q_offsets
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, q_offsets=None, freqs=None,
@@ -509,29 +507,31 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, q_offsets=
         raise ValueError("q must have k's rows and head_dim")
     if q is not None and freqs is None:
         raise ValueError("q is turned by its positions: it takes freqs")
-    _head_tensor("k_cache", k_cache, (*k_cache.shape[:2], *k.shape[-2:]), k.dtype)
-    _head_tensor("v_cache", v_cache, k_cache.shape, k.dtype)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    if v.dtype != k.dtype or k_cache.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         raise ValueError("q, k, v and the caches must be of one type")
-    d = recis.recis_append_desc()
-    d.dtype = _dtype("k", k)
-    k, v, q = _heads(k), _heads(v), None if q is None else _heads(q)
+    dtype = _dtype("k", k)
     batch = k.shape[0] if q_offsets is None else q_offsets.numel() - 1
-    keep = _paged(d, k_cache, v_cache, page_table, kv_lens, q_offsets, batch, k.shape[0], error)
-    d.new_len, d.rows = (recis.int32(k.shape[1]), 0) if q_offsets is None else (0, k.shape[0])
-    d.kv_heads, d.head_dim = recis.int32(k.shape[-2]), recis.int32(k.shape[-1])
-    d.interleaved, d.amplitude = 1 if interleaved else 0, amplitude
-    if freqs is not None:
-        d.rot_dim = _freqs(freqs, k.shape[-1])
-        d.freqs = freqs.data_ptr() if d.rot_dim else None
-    out = None
+    table, lens, offsets = _paged(k_cache, v_cache, page_table, kv_lens, q_offsets, batch, error)
+    pages, page_size = k_cache.shape[:2]
+    kv_heads, head_dim = k.shape[-2:]
+    _head_tensor("k_cache", k_cache, (pages, page_size, kv_heads, head_dim), k.dtype)
+    _head_tensor("v_cache", v_cache, k_cache.shape, k.dtype)
+    k, v = _heads(k), _heads(v)
+    out, q_heads, q_st, out_st = None, 0, (0, 0, 0), (0, 0, 0)
     if q is not None:
+        q = _heads(q)
         out = _like(q) if batch else torch.zeros_like(q)
-        d.q_heads = recis.int32(q.shape[-2])
-        d.q_strides[:], d.q_out_strides[:] = _st(q), _st(out)
-    d.k_strides[:], d.v_strides[:] = _st(k), _st(v)
-    d.k_cache_strides[:], d.v_cache_strides[:] = _st(k_cache), _st(v_cache)
-    recis.recis_cache_append(d, q, k, v, out, k_cache, v_cache)
+        q_heads, q_st, out_st = q.shape[-2], _st(q), _st(out)
+    rot_dim = 0 if freqs is None else _freqs(freqs, head_dim)
+    int32 = recis.int32
+    new_len, rows = (int32(k.shape[1]), 0) if q_offsets is None else (0, k.shape[0])
+    desc = recis.pack_append_desc(
+        dtype, int32(batch), new_len, int32(q_heads), int32(kv_heads), int32(head_dim), rot_dim,
+        1 if interleaved else 0, amplitude, int32(page_size), int32(table.shape[1]), pages,
+        table.stride(0) if batch > 1 else table.shape[1], rows, *q_st, *out_st, *_st(k), *_st(v), *_st(k_cache),
+        *_st(v_cache), freqs.data_ptr() if rot_dim else 0, 0 if offsets is None else offsets.data_ptr(),
+        lens.data_ptr(), table.data_ptr(), 0 if error is None else error.data_ptr())
+    recis.recis_cache_append(desc, q, k, v, out, k_cache, v_cache)
     return out
 
 
@@ -567,28 +567,29 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
                          "max_q_len")
     if k_cache.dim() != 4 or not q.dtype == k_cache.dtype or q.shape[-1] != k_cache.shape[-1]:
         raise ValueError("q and the caches must be of one type and head_dim")
-    q, k_cache, v_cache = _heads(q), _heads(k_cache), _heads(v_cache)
-    d = recis.recis_paged_attn_desc()
-    d.dtype = _dtype("q", q)
-    batch = q_offsets.numel() - 1 if packed else q.shape[0]
-    keep = _paged(d, k_cache, v_cache, page_table, kv_lens, q_offsets, batch, q.shape[0], error)
-    d.q_len, d.q_rows = (recis.int32(max_q_len), q.shape[0]) if packed else (recis.int32(q.shape[1]), 0)
-    d.q_heads, d.kv_heads, d.head_dim = map(recis.int32, (q.shape[-2], k_cache.shape[-2], q.shape[-1]))
     if not causal and (window is not None or sinks):
         raise ValueError("a window takes causal rows")
-    d.causal = 1 if causal else 0
-    d.window, d.sinks = _band(window, sinks)
-    d.scale = max(q.shape[-1], 1) ** -0.5 if scale is None else scale
+    dtype = _dtype("q", q)
+    batch = q_offsets.numel() - 1 if packed else q.shape[0]
+    table, lens, offsets = _paged(k_cache, v_cache, page_table, kv_lens, q_offsets, batch, error)
+    q, k_cache, v_cache = _heads(q), _heads(k_cache), _heads(v_cache)
     if out is None:
         out = q.new_zeros(q.shape) if packed else _like(q)
     else:
         _head_tensor("out", out, q.shape, q.dtype)
     lse = q.new_full(q.shape[:-1], -math.inf, dtype=torch.float32) if return_lse else None
-    d.q_strides[:], d.o_strides[:] = _st(q), _st(out)
-    d.k_strides[:], d.v_strides[:] = _st(k_cache), _st(v_cache)
-    nbytes = recis.recis_paged_attn_workspace_bytes(d)
+    int32 = recis.int32
+    head_dim = q.shape[-1]
+    desc = recis.pack_paged_attn_desc(
+        dtype, int32(batch), int32(max_q_len if packed else q.shape[1]), int32(q.shape[-2]), int32(k_cache.shape[2]),
+        int32(head_dim), 1 if causal else 0, *_band(window, sinks), int32(k_cache.shape[1]), int32(table.shape[1]),
+        max(head_dim, 1) ** -0.5 if scale is None else scale, k_cache.shape[0],
+        table.stride(0) if batch > 1 else table.shape[1], q.shape[0] if packed else 0, *_st(q), *_st(out),
+        *_st(k_cache), *_st(v_cache), 0 if offsets is None else offsets.data_ptr(), lens.data_ptr(),
+        table.data_ptr(), 0 if error is None else error.data_ptr())
+    nbytes = recis.recis_paged_attn_workspace_bytes(desc)
     workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
-    recis.recis_paged_attn_fwd(d, q, k_cache, v_cache, out, lse, workspace, nbytes)
+    recis.recis_paged_attn_fwd(desc, q, k_cache, v_cache, out, lse, workspace, nbytes)
     return (out, lse) if return_lse else out
 
 
@@ -603,29 +604,26 @@ def _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, e
         raise ValueError("q, k and v must be of one type")
     if packed != (max_len is not None) or (packed and lens is not None):
         raise ValueError("packed histories (offsets) take max_len, and no lens; padded ones no max_len")
-    d = recis.recis_self_attn_desc()
-    d.dtype = _dtype("q", q)
+    dtype = _dtype("q", q)
     batch, length = (offsets.numel() - 1, max_len) if packed else q.shape[:2]
-    d.batch, d.len, d.rows = recis.int32(batch), recis.int32(length), q.shape[0] if packed else 0
-    d.q_heads, d.kv_heads, d.head_dim = map(recis.int32, (q.shape[-2], k.shape[-2], q.shape[-1]))
-    d.window, d.sinks = _band(window, sinks)
-    d.scale = max(q.shape[-1], 1) ** -0.5 if scale is None else scale
-    keep = []
+    keep, mask, mask_stride = None, 0, 0
     if packed:
-        keep.append(_index("offsets", offsets, torch.int32, (batch + 1,)))
-        d.offsets = keep[-1].data_ptr()
+        keep = _index("offsets", offsets, torch.int32, (batch + 1,))
     elif lens is not None:
-        keep.append(_index("lens", lens, torch.int32, (batch,)))
-        d.lens = keep[-1].data_ptr()
+        keep = _index("lens", lens, torch.int32, (batch,))
     if kv_mask is not None:
         if kv_mask.dtype not in (torch.bool, torch.uint8) or kv_mask.shape != k.shape[:-2]:
             raise ValueError(f"kv_mask must be bool or uint8 {list(k.shape[:-2])}")
-        keep.append(kv_mask if kv_mask.stride(-1) == 1 else kv_mask.contiguous())
-        d.kv_mask, d.mask_stride = keep[-1].data_ptr(), 0 if packed else keep[-1].stride(0)
-    if error is not None:
-        d.error = _error_word(error).data_ptr()
-    d.q_strides[:], d.k_strides[:], d.v_strides[:] = _st(q), _st(k), _st(v)
-    return d, keep
+        kv_mask = kv_mask if kv_mask.stride(-1) == 1 else kv_mask.contiguous()
+        mask, mask_stride = kv_mask.data_ptr(), 0 if packed else kv_mask.stride(0)
+    int32, head_dim = recis.int32, q.shape[-1]
+    head = (dtype, int32(batch), int32(length), int32(q.shape[-2]), int32(k.shape[-2]), int32(head_dim),
+            *_band(window, sinks), max(head_dim, 1) ** -0.5 if scale is None else scale, q.shape[0] if packed else 0,
+            *_st(q), *_st(k), *_st(v))
+    at = keep.data_ptr() if keep is not None else 0
+    tail = (0 if packed else at, at if packed else 0, mask, mask_stride,
+            0 if error is None else _error_word(error).data_ptr())
+    return head, tail, batch > 0 and length > 0, (keep, kv_mask)
 
 
 def self_attention(q, k, v, lens=None, offsets=None, kv_mask=None, max_len: Optional[int] = None,
@@ -645,17 +643,17 @@ def self_attention(q, k, v, lens=None, offsets=None, kv_mask=None, max_len: Opti
             return self_attention(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, return_lse, error)
     _forward_of("self_attention", q, k, v, lens, offsets, kv_mask, error)
     q, k, v = _heads(q), _heads(k), _heads(v)
-    d, keep = _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error)
-    out = _like(q) if d.batch and d.len else q.new_zeros(q.shape)
-    d.o_strides[:] = _st(out)
+    head, tail, some, keep = _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error)
+    out = _like(q) if some else q.new_zeros(q.shape)
     lse = None
     if return_lse:
         lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
         if offsets is not None:
             lse.fill_(-math.inf)
-    nbytes = recis.recis_self_attn_workspace_bytes(d, False)
+    desc = recis.pack_self_attn_desc(*head, *_st(out), *[0] * 12, *tail)
+    nbytes = recis.recis_self_attn_workspace_bytes(desc, False)
     workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
-    recis.recis_self_attn_fwd(d, q, k, v, out, lse, workspace, nbytes)
+    recis.recis_self_attn_fwd(desc, q, k, v, out, lse, workspace, nbytes)
     return (out, lse) if return_lse else out
 
 
@@ -674,13 +672,12 @@ def self_attention_backward(grad_out, q, k, v, out, lse, lens=None, offsets=None
     if lse.dtype != torch.float32 or lse.shape != q.shape[:-1] or not lse.is_contiguous():
         raise ValueError("lse must be self_attention's, contiguous float32 over q's leading axes and heads")
     q, k, v, out, grad_out = _heads(q), _heads(k), _heads(v), _heads(out), _heads(grad_out)
-    d, keep = _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error)
+    head, tail, some, keep = _self_desc(q, k, v, lens, offsets, kv_mask, max_len, window, sinks, scale, error)
     dq, dk, dv = _like(q), _like(k), _like(v)
-    if not d.batch or not d.len:  # without an entry nothing is written
+    if not some:  # without an entry nothing is written
         dq.zero_(), dk.zero_(), dv.zero_()
-    d.o_strides[:], d.do_strides[:], d.dq_strides[:] = _st(out), _st(grad_out), _st(dq)
-    d.dk_strides[:], d.dv_strides[:] = _st(dk), _st(dv)
-    nbytes = recis.recis_self_attn_workspace_bytes(d, True)
+    desc = recis.pack_self_attn_desc(*head, *_st(out), *_st(grad_out), *_st(dq), *_st(dk), *_st(dv), *tail)
+    nbytes = recis.recis_self_attn_workspace_bytes(desc, True)
     workspace = q.new_empty(max(nbytes, 0), dtype=torch.uint8)
-    recis.recis_self_attn_bwd(d, grad_out, q, k, v, out, lse, dq, dk, dv, workspace, nbytes)
+    recis.recis_self_attn_bwd(desc, grad_out, q, k, v, out, lse, dq, dk, dv, workspace, nbytes)
     return dq, dk, dv

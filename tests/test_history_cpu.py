@@ -37,6 +37,21 @@ def test_desc_layouts(lib, tmp_path, name):
         assert getattr(cls, field).offset == int(at), field
 
 
+@pytest.mark.parametrize("name", ["rotary", "append", "paged_attn", "self_attn"])
+def test_packed_descriptions_are_the_structures(lib, name):
+    cls = getattr(lib, f"recis_{name}_desc")
+    d, values = cls(), []
+    for i, (field, kind) in enumerate(cls._fields_):
+        if hasattr(kind, "_length_"):
+            value = [1000 * i + j for j in range(kind._length_)]
+            getattr(d, field)[:] = value
+            values += value
+        else:
+            setattr(d, field, i + 1)
+            values.append(i + 1)
+    assert getattr(lib, f"pack_{name}_desc")(*values) == bytes(d)
+
+
 def described(cls, values, **change):
     d = cls()
     for name, value in {**values, **change}.items():
@@ -225,9 +240,10 @@ def test_frequencies():
 def test_sizes_past_32_bits_are_refused(lib, size):
     from dynamic_embedding_tables_amd import sequence
     q, off = torch.zeros(10, 2, 8), torch.tensor([0, 4, 10], dtype=torch.int32)
-    d, _ = sequence._self_desc(q, q, q, None, off, None, size, None, 0, None, None)
+    head, tail, *_ = sequence._self_desc(q, q, q, None, off, None, size, None, 0, None, None)
+    d = lib.pack_self_attn_desc(*head, *[0] * 15, *tail)
     assert lib.recis_self_attn_workspace_bytes(d, True) == -1
-    assert lib.load_library().recis_self_attn_fwd(C.byref(d), *[P] * 6, 1 << 60, None) == UNSUPPORTED
+    assert lib.load_library().recis_self_attn_fwd(d, *[P] * 6, 1 << 60, None) == UNSUPPORTED
     window, sinks = sequence._band(size, size)
     assert window == (1 << 31) - 1 and sinks == (1 << 31) - 1   # more than any length
 
