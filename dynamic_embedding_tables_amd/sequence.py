@@ -348,10 +348,21 @@ def cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens=None, kv_offse
 
 
 # --------------------------------------------------------- rotary positions
+# (These calls are made for a few microseconds of work, and a tensor's shape, taken from it, costs a quarter of one:
+# each is taken once.)
 def _st(t):
     """Strides of (batch entry, position, head) or (page, slot, head)."""
     s = t.stride()
     return s[:3] if len(s) == 4 else (0, s[0], s[1])
+
+
+def _heads_st(t, head_dim):
+    """t with its head vectors contiguous, and those strides."""
+    s = t.stride()
+    if s[-1] != 1 and head_dim != 1:
+        t = t.contiguous()
+        s = t.stride()
+    return t, (s[:3] if len(s) == 4 else (0, s[0], s[1]))
 
 
 def _serves(name: str, *tensors):
@@ -368,7 +379,7 @@ def _serves(name: str, *tensors):
 
 def _head_tensor(name: str, t, shape, dtype):
     """An output or a cache given by the caller: head vectors contiguous, no element twice."""
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
     if not t.is_contiguous() and ((t.shape[-1] > 1 and t.stride(-1) != 1) or any(
             st == 0 and n > 1 for st, n in zip(t.stride(), t.shape))):
@@ -379,9 +390,10 @@ def _freqs(freqs, head_dim: int) -> int:
     """Elements of a head that turn."""
     if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be contiguous float64 [rotated elements / 2]")
-    if 2 * freqs.numel() > head_dim:
-        raise ValueError(f"{freqs.numel()} pairs are more than a head of {head_dim} has")
-    return 2 * freqs.numel()
+    rot_dim = 2 * freqs.numel()
+    if rot_dim > head_dim:
+        raise ValueError(f"{rot_dim // 2} pairs are more than a head of {head_dim} has")
+    return rot_dim
 
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -416,28 +428,27 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
 
 
 def _rotary(x, freqs, positions, interleaved, amplitude, out, backward):
-    if x.dim() not in (3, 4):
+    shape, dtype = tuple(x.shape), _dtype("x", x)
+    if len(shape) not in (3, 4):
         raise ValueError("x must be [seq, heads, head_dim] or [batch, seq, heads, head_dim]")
-    dtype = _dtype("x", x)
-    heads, head_dim = x.shape[-2:]
+    batch, seq, heads, head_dim = shape if len(shape) == 4 else (1, *shape)
     rot_dim = _freqs(freqs, head_dim)
-    x = _heads(x)
+    x, x_st = _heads_st(x, head_dim)
     if out is None:
         out = _like(x)
     else:
-        _head_tensor("out", out, x.shape, x.dtype)
-    batch, seq = (x.shape[0] if x.dim() == 4 else 1), x.shape[-3]
+        _head_tensor("out", out, shape, x.dtype)
     at, at_strides = 0, (0, 0)
     if positions is not None:
-        if positions.dtype != torch.int64 or positions.shape not in (x.shape[:-2], x.shape[-3:-2]):
-            raise ValueError(f"positions must be int64 {list(x.shape[:-2])} or [{seq}]")
+        if positions.dtype != torch.int64 or tuple(positions.shape) not in (shape[:-2], (seq,)):
+            raise ValueError(f"positions must be int64 {list(shape[:-2])} or [{seq}]")
         at, at_strides = positions.data_ptr(), positions.stride()
         if len(at_strides) == 1:
             at_strides = (0, *at_strides)
-    if x.numel():
-        desc = recis.pack_rotary_desc(dtype, recis.int32(heads), recis.int32(head_dim), rot_dim,
-                                      1 if interleaved else 0, amplitude, batch, seq,
-                                      freqs.data_ptr() if rot_dim else 0, at, *at_strides, *_st(x), *_st(out))
+    if batch and seq and heads:
+        int32 = recis.int32
+        desc = recis.pack_rotary_desc(dtype, int32(heads), int32(head_dim), rot_dim, 1 if interleaved else 0, amplitude,
+                                      batch, seq, freqs.data_ptr() if rot_dim else 0, at, *at_strides, *x_st, *_st(out))
         recis.recis_rotary(desc, backward, x, out)
     return out
 
@@ -465,22 +476,27 @@ def rotary_backward(grad_out, freqs, positions=None, interleaved: bool = False, 
 
 
 # -------------------------------------------------------------- paged cache
-def _paged(k_cache, v_cache, page_table, kv_lens, q_offsets, batch, error):
-    """What both calls on a cache check alike: contiguous (page_table, kv_lens, q_offsets)."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must both be [pages, page_size, kv_heads, head_dim] of one type")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch:
+def _paged(page_table, kv_lens, q_offsets, batch, error):
+    """What both calls on a cache check alike: (page_table, its width and stride, pointers of it, kv_lens, q_offsets and
+    error), and what of it has to stay."""
+    width = tuple(page_table.shape)
+    if page_table.dtype != torch.int32 or len(width) != 2 or width[0] != batch:
         raise ValueError(f"page_table must be int32 [{batch}, pages an entry may have]")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+    stride = page_table.stride()
+    if width[1] > 1 and stride[1] != 1:
         page_table = page_table.contiguous()
-    if kv_lens.dtype != torch.int32 or kv_lens.shape != (batch,):
+        stride = page_table.stride()
+    if kv_lens.dtype != torch.int32 or tuple(kv_lens.shape) != (batch,):
         raise ValueError(f"kv_lens must be torch.int32 [{batch}], not {kv_lens.dtype} {list(kv_lens.shape)}")
+    kv_lens, at = kv_lens.contiguous(), 0
     if q_offsets is not None:
         if q_offsets.dtype != torch.int32 or q_offsets.dim() != 1:
             raise ValueError("q_offsets must be int32 [batch + 1]")
         q_offsets = q_offsets.contiguous()
-    _error_word(error)
-    return page_table, kv_lens.contiguous(), q_offsets
+        at = q_offsets.data_ptr()
+    return (recis.int32(width[1]), stride[0] if batch > 1 else width[1],
+            (at, kv_lens.data_ptr(), page_table.data_ptr(), 0 if error is None else _error_word(error).data_ptr()),
+            (page_table, kv_lens, q_offsets))
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, q_offsets=None, freqs=None,
@@ -500,37 +516,39 @@ def cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q=None, q_offsets=
             return cache_append(k, v, k_cache, v_cache, page_table, kv_lens, q, q_offsets, freqs, interleaved,
                                 amplitude, error)
     _serves("cache_append", k, v, k_cache, v_cache, page_table, kv_lens, q, q_offsets, freqs, error)
-    if k.dim() != (4 if q_offsets is None else 3) or v.shape != k.shape:
+    shape, packed = tuple(k.shape), q_offsets is not None
+    if len(shape) != (3 if packed else 4) or tuple(v.shape) != shape:
         raise ValueError("k and v must both be [batch, new, kv_heads, head_dim], or [rows, kv_heads, head_dim] with "
                          "q_offsets")
-    if q is not None and (q.shape[:-2] != k.shape[:-2] or q.dim() != k.dim() or q.shape[-1] != k.shape[-1]):
-        raise ValueError("q must have k's rows and head_dim")
-    if q is not None and freqs is None:
-        raise ValueError("q is turned by its positions: it takes freqs")
-    if v.dtype != k.dtype or k_cache.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    kv_heads, head_dim = shape[-2:]
+    kind, dtype = k.dtype, _dtype("k", k)
+    if v.dtype != kind or k_cache.dtype != kind or (q is not None and q.dtype != kind):
         raise ValueError("q, k, v and the caches must be of one type")
-    dtype = _dtype("k", k)
-    batch = k.shape[0] if q_offsets is None else q_offsets.numel() - 1
-    table, lens, offsets = _paged(k_cache, v_cache, page_table, kv_lens, q_offsets, batch, error)
-    pages, page_size = k_cache.shape[:2]
-    kv_heads, head_dim = k.shape[-2:]
-    _head_tensor("k_cache", k_cache, (pages, page_size, kv_heads, head_dim), k.dtype)
-    _head_tensor("v_cache", v_cache, k_cache.shape, k.dtype)
-    k, v = _heads(k), _heads(v)
+    batch = q_offsets.numel() - 1 if packed else shape[0]
+    cache = tuple(k_cache.shape)
+    if len(cache) != 4:
+        raise ValueError("k_cache and v_cache must both be [pages, page_size, kv_heads, head_dim] of one type")
+    _head_tensor("k_cache", k_cache, (cache[0], cache[1], kv_heads, head_dim), kind)
+    _head_tensor("v_cache", v_cache, cache, kind)
+    width, table_st, at, keep = _paged(page_table, kv_lens, q_offsets, batch, error)
+    k, k_st = _heads_st(k, head_dim)
+    v, v_st = _heads_st(v, head_dim)
     out, q_heads, q_st, out_st = None, 0, (0, 0, 0), (0, 0, 0)
     if q is not None:
-        q = _heads(q)
+        if freqs is None:
+            raise ValueError("q is turned by its positions: it takes freqs")
+        q_shape = tuple(q.shape)
+        if len(q_shape) != len(shape) or q_shape[:-2] != shape[:-2] or q_shape[-1] != head_dim:
+            raise ValueError("q must have k's rows and head_dim")
+        q, q_st = _heads_st(q, head_dim)
         out = _like(q) if batch else torch.zeros_like(q)
-        q_heads, q_st, out_st = q.shape[-2], _st(q), _st(out)
+        q_heads, out_st = q_shape[-2], _st(out)
     rot_dim = 0 if freqs is None else _freqs(freqs, head_dim)
     int32 = recis.int32
-    new_len, rows = (int32(k.shape[1]), 0) if q_offsets is None else (0, k.shape[0])
     desc = recis.pack_append_desc(
-        dtype, int32(batch), new_len, int32(q_heads), int32(kv_heads), int32(head_dim), rot_dim,
-        1 if interleaved else 0, amplitude, int32(page_size), int32(table.shape[1]), pages,
-        table.stride(0) if batch > 1 else table.shape[1], rows, *q_st, *out_st, *_st(k), *_st(v), *_st(k_cache),
-        *_st(v_cache), freqs.data_ptr() if rot_dim else 0, 0 if offsets is None else offsets.data_ptr(),
-        lens.data_ptr(), table.data_ptr(), 0 if error is None else error.data_ptr())
+        dtype, int32(batch), 0 if packed else int32(shape[1]), int32(q_heads), int32(kv_heads), int32(head_dim), rot_dim,
+        1 if interleaved else 0, amplitude, int32(cache[1]), width, cache[0], table_st, shape[0] if packed else 0, *q_st,
+        *out_st, *k_st, *v_st, *_st(k_cache), *_st(v_cache), freqs.data_ptr() if rot_dim else 0, *at)
     recis.recis_cache_append(desc, q, k, v, out, k_cache, v_cache)
     return out
 
@@ -561,32 +579,34 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
             return paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal, window,
                                    sinks, scale, return_lse, out, error)
     _serves("paged_attention", q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, error)
-    packed = q_offsets is not None
-    if q.dim() != (3 if packed else 4) or packed != (max_q_len is not None):
+    shape, packed = tuple(q.shape), q_offsets is not None
+    if len(shape) != (3 if packed else 4) or packed != (max_q_len is not None):
         raise ValueError("q must be [batch, new, q_heads, head_dim], or [rows, q_heads, head_dim] with q_offsets and "
                          "max_q_len")
-    if k_cache.dim() != 4 or not q.dtype == k_cache.dtype or q.shape[-1] != k_cache.shape[-1]:
-        raise ValueError("q and the caches must be of one type and head_dim")
+    cache, kind, head_dim = tuple(k_cache.shape), q.dtype, shape[-1]
+    if len(cache) != 4 or tuple(v_cache.shape) != cache or cache[3] != head_dim or k_cache.dtype != kind \
+            or v_cache.dtype != kind:
+        raise ValueError("k_cache and v_cache must both be [pages, page_size, kv_heads, head_dim], of q's type and "
+                         "head_dim")
     if not causal and (window is not None or sinks):
         raise ValueError("a window takes causal rows")
     dtype = _dtype("q", q)
-    batch = q_offsets.numel() - 1 if packed else q.shape[0]
-    table, lens, offsets = _paged(k_cache, v_cache, page_table, kv_lens, q_offsets, batch, error)
-    q, k_cache, v_cache = _heads(q), _heads(k_cache), _heads(v_cache)
+    batch = q_offsets.numel() - 1 if packed else shape[0]
+    width, table_st, at, keep = _paged(page_table, kv_lens, q_offsets, batch, error)
+    q, q_st = _heads_st(q, head_dim)
+    k_cache, k_st = _heads_st(k_cache, head_dim)
+    v_cache, v_st = _heads_st(v_cache, head_dim)
     if out is None:
-        out = q.new_zeros(q.shape) if packed else _like(q)
+        out = q.new_zeros(shape) if packed else _like(q)
     else:
-        _head_tensor("out", out, q.shape, q.dtype)
-    lse = q.new_full(q.shape[:-1], -math.inf, dtype=torch.float32) if return_lse else None
+        _head_tensor("out", out, shape, kind)
+    lse = q.new_full(shape[:-1], -math.inf, dtype=torch.float32) if return_lse else None
     int32 = recis.int32
-    head_dim = q.shape[-1]
     desc = recis.pack_paged_attn_desc(
-        dtype, int32(batch), int32(max_q_len if packed else q.shape[1]), int32(q.shape[-2]), int32(k_cache.shape[2]),
-        int32(head_dim), 1 if causal else 0, *_band(window, sinks), int32(k_cache.shape[1]), int32(table.shape[1]),
-        max(head_dim, 1) ** -0.5 if scale is None else scale, k_cache.shape[0],
-        table.stride(0) if batch > 1 else table.shape[1], q.shape[0] if packed else 0, *_st(q), *_st(out),
-        *_st(k_cache), *_st(v_cache), 0 if offsets is None else offsets.data_ptr(), lens.data_ptr(),
-        table.data_ptr(), 0 if error is None else error.data_ptr())
+        dtype, int32(batch), int32(max_q_len if packed else shape[1]), int32(shape[-2]), int32(cache[2]),
+        int32(head_dim), 1 if causal else 0, *_band(window, sinks), int32(cache[1]), width,
+        max(head_dim, 1) ** -0.5 if scale is None else scale, cache[0], table_st, shape[0] if packed else 0, *q_st,
+        *_st(out), *k_st, *v_st, *at)
     nbytes = recis.recis_paged_attn_workspace_bytes(desc)
     workspace = q.new_empty(nbytes, dtype=torch.uint8) if nbytes > 0 else None
     recis.recis_paged_attn_fwd(desc, q, k_cache, v_cache, out, lse, workspace, nbytes)
