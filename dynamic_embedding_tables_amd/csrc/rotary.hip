@@ -11,7 +11,13 @@
 //
 // Bound by memory.  A block takes whole tokens: their cosines and sines once, into
 // LDS, for all heads; then its threads walk the tokens' elements in order, V pairs
-// at a time.
+// at a time, 16 bytes of either element.  The table is small, 8 KB, so that eight
+// blocks stay on a CU: at 32 KB four do, and appending 2048 packed histories of up to
+// 1000 events (1.57 GB; 4 heads of 32, bf16) took 457 us, at 8 KB 355.  Values are
+// copied by a loop of their own, since a wave that holds both kinds rotates with half
+// its lanes: 338 -> 307 us, 5.1 TB/s, where a large copy reaches 4.9.  Rotating 2048 x
+// 1000 events alone, 4 heads: 184 us a pass, 5.7 TB/s of requests, some of which the
+// last-level cache answers.  One event each for 64 users: 3 to 4 us, the launch.
 #include <algorithm>
 
 #include "seq.h"
@@ -21,7 +27,7 @@ namespace {
 
 constexpr int kMaxTurnDim = 1024;           // elements a head
 constexpr int kMaxTokenElems = 1 << 18;     // elements a token
-constexpr int kTurnTable = 4096;            // pairs of LDS a block: 32 KB
+constexpr int kTurnTable = 1024;            // pairs of LDS a block: 8 KB
 constexpr int kMaxTokens = 64;              // tokens a block
 
 // x / d for x * d < 2^32.
@@ -139,7 +145,7 @@ struct AppendArgs {
   int batch, new_len, width, page_size;
   int q_heads, kv_heads, head_dim;
   int per_block, turned, items, copied;  // items of a head of q and k, and of one of v
-  Div by_half, by_token, by_head, by_copied;
+  Div by_half, by_token, by_head, by_v_token, by_copied;  // by_token: of q and k
 };
 
 // The entry of a packed row: the largest b in [lo, hi] with offsets[b] <= row.
@@ -233,19 +239,10 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a) {
   __syncthreads();
   fill_turns(a.turns, pos, tokens, a.by_half, table);
   __syncthreads();
-  const unsigned all = tokens * a.by_token.d, both = (unsigned)(a.q_heads + a.kv_heads) * a.items;
-  for (unsigned x = threadIdx.x; x < all; x += kThreads) {
+  const unsigned turned = tokens * a.by_token.d;
+  for (unsigned x = threadIdx.x; x < turned; x += kThreads) {
     const unsigned t = a.per_block == 1 ? 0 : divided(x, a.by_token);
-    unsigned in = x - t * a.by_token.d;
-    if (in >= both) {
-      in -= both;
-      const unsigned h = divided(in, a.by_copied), j = in - h * a.by_copied.d;
-      if (at_vc[t] < 0) continue;
-      *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.vc) + at_vc[t] + h * a.vcs[2] + j * V) =
-          *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.v) + at_v[t] + h * a.vs[2] + j * V);
-      continue;
-    }
-    const unsigned head = divided(in, a.by_head), j = in - head * a.by_head.d;
+    const unsigned in = x - t * a.by_token.d, head = divided(in, a.by_head), j = in - head * a.by_head.d;
     const T* from;
     T* to;
     if (head < (unsigned)a.q_heads) {
@@ -269,14 +266,24 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a) {
     }
     turn_item<T, V, NEIGHBOURS>(from, to, table + t * a.turns.half, j, a.turned, a.turns.half);
   }
+  const unsigned copied = tokens * a.by_v_token.d;
+  for (unsigned x = threadIdx.x; x < copied; x += kThreads) {
+    const unsigned t = a.per_block == 1 ? 0 : divided(x, a.by_v_token);
+    const unsigned in = x - t * a.by_v_token.d, h = divided(in, a.by_copied), j = in - h * a.by_copied.d;
+    if (at_vc[t] < 0) continue;
+    *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.vc) + at_vc[t] + h * a.vcs[2] + j * V) =
+        *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.v) + at_v[t] + h * a.vs[2] + j * V);
+  }
 }
 
-// Tokens a block: about 1024 items, but 512 blocks before any takes a second
-// token, and their turns fit the table.
+// Tokens a block: about 2048 items, but 4096 blocks -- two turns of all that the
+// chip holds -- before any takes a second token, and their turns fit the table.
+// (Items 1024 / 2048: appending those histories 310 / 307 us; blocks 512 / 4096
+// with 47 397 tokens of 42 items: 25.6 / 23.1 us a pass.)
 int tokens_a_block(int64_t tokens, int64_t items, int half) {
-  int64_t n = std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, 1024 / std::max<int64_t>(1, items)));
+  int64_t n = std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, 2048 / std::max<int64_t>(1, items)));
   if (half) n = std::min<int64_t>(n, kTurnTable / half);
-  return (int)std::max<int64_t>(1, std::min(n, (tokens + 511) / 512));
+  return (int)std::max<int64_t>(1, std::min(n, (tokens + 4095) / 4096));
 }
 
 // The widest access of a head's halves (or neighbours) and its rest.
@@ -441,8 +448,9 @@ recis_status recis_cache_append(const recis_append_desc* d, const void* q, const
   const int64_t per_token = (int64_t)(d->q_heads + d->kv_heads) * a.items + (int64_t)d->kv_heads * a.copied;
   a.per_block = tokens_a_block(rows, per_token, a.turns.half);
   a.by_half = div_by(std::max(1, a.turns.half));
-  a.by_token = div_by(per_token);
+  a.by_token = div_by((int64_t)(d->q_heads + d->kv_heads) * a.items);
   a.by_head = div_by(a.items);
+  a.by_v_token = div_by((int64_t)d->kv_heads * a.copied);
   a.by_copied = div_by(a.copied);
   const int64_t blocks = (rows + a.per_block - 1) / a.per_block;
   if (blocks > kMaxBlocks) return RECIS_ERR_UNSUPPORTED;
