@@ -156,6 +156,12 @@ __device__ __forceinline__ Reach reach_of(const BandArgs& a, Entry e, int row0, 
   return Reach{divided(row0, a.by_group) * e.step + e.shift, row0 < e.n * a.group ? last : -1};
 }
 
+// A key, or where no row of a reach sees it -- behind the sinks, before the window, where
+// a cache's pages may be gone -- the first of the window.
+__device__ __forceinline__ int in_reach(const BandArgs& a, int key, int window_lo) {
+  return key < a.sinks ? key : std::max(key, window_lo);
+}
+
 // The tiles of K keys that rows of a reach see, in order: tiles of sinks that lie
 // before the window, then the window's.
 struct Walk {
@@ -421,10 +427,11 @@ struct KeyStage {
   static_assert(K % kStep == 0, "every thread has the same number of chunks");
   Frag<T> fk[kPer], fv[kPer];
   int page[kPer];  // of the tile that comes next
-  int row, d0;
+  int row, d0, window_lo;
   unsigned at_d;   // bytes into the head
   bool bad;
-  __device__ __forceinline__ void start(const BandArgs& a) {
+  __device__ __forceinline__ void start(const BandArgs& a, int from = 0) {
+    window_lo = from;  // paged: the first key of the block's window
     row = threadIdx.x / kAcross;
     d0 = (threadIdx.x % kAcross) * 8;
     at_d = d0 < a.head_dim ? d0 * (unsigned)sizeof(T) : 0;
@@ -432,7 +439,8 @@ struct KeyStage {
   }
   __device__ __forceinline__ void ask_pages(const BandArgs& a, const int* table, int first, int len) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) page[i] = table[page_of(a, std::min(first + row + i * kStep, len - 1))];
+    for (int i = 0; i < kPer; ++i)
+      page[i] = table[page_of(a, in_reach(a, std::min(first + row + i * kStep, len - 1), window_lo))];
   }
   static __device__ __forceinline__ Frag<T> at_bytes(const T* base, unsigned bytes) {
     return *reinterpret_cast<const Frag<T>*>(reinterpret_cast<const char*>(base) + bytes);
@@ -445,7 +453,8 @@ struct KeyStage {
     for (int i = 0; i < kPer; ++i) {
       const int in_tile = row + i * kStep;
       if constexpr (PAGED) {
-        const int key = std::min(first + in_tile, len - 1), slot = key - page_of(a, key) * a.by_page.d;
+        const int key = in_reach(a, std::min(first + in_tile, len - 1), window_lo);
+        const int slot = key - page_of(a, key) * a.by_page.d;
         int p = page[i];
         if ((unsigned)p >= (unsigned long long)a.pages) p = 0, bad = true;
         if constexpr (ALN) {  // (strides are below 2^31)

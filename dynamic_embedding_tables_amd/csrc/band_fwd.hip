@@ -39,7 +39,8 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   const int tile_row = tile * kBandRows, rows = e.n * a.group;
   if (tile_row >= rows) return;
   const int lane = threadIdx.x & 63, wave = wave_of();
-  const Walk walk = walk_of<K>(a, reach_of(a, e, tile_row, tile_row + kBandRows - 1));
+  const Reach block_reach = reach_of(a, e, tile_row, tile_row + kBandRows - 1);
+  const Walk walk = walk_of<K>(a, block_reach);
   const Reach reach = reach_of(a, e, tile_row + wave * 32, tile_row + wave * 32 + 31);
   const int per = split_size(walk.n, a.splits, kLeastTiles);
   const int i0 = split * per, i1 = std::min(walk.n, i0 + per);
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   float m = -INFINITY, ref = 0.f, most = -INFINITY, l = 0.f;
   const float c2 = a.scale * kLog2e;
   KeyStage<T, DP, K, PAGED, ALN> st;
-  st.start(a);
+  st.start(a, block_reach.low - a.window + 1);  // (below 0: all of them)
   unsigned long long bits = 0;
   if (i0 < i1) {
     const int first = walk.tile(i0) * K;

@@ -67,9 +67,11 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
   const unsigned k_at = (unsigned)((kr * a.ks[1] + (lane >> 4) * kHalf) * (long long)sizeof(T));  // ALN: fits
   const unsigned v_at = (unsigned)((vr * a.vs[1] + vd) * (long long)sizeof(T));
   const bool by16 = ALN && a.by_page.d % 16 == 0 && a.head_dim == kCols<DP>;
+  const int window_lo = reach.low - a.window + 1;  // before it no row sees a key but the sinks
+  auto wanted = [&](int key) { return key < e.len && (key >= window_lo || key < a.sinks); };
   auto ask_page = [&](int first) {
     const int key = first + (lane & 31);
-    return key < e.len ? table[page_of(a, key)] : 0;
+    return wanted(key) ? table[page_of(a, key)] : 0;
   };
   auto at_bytes = [](const T* base, unsigned bytes) {
     return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
@@ -77,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void k_paged_few(BandArgs a) {
   // 32 keys from `first`, whose page the lane was told; returns the keys that are there
   auto fetch = [&](int first, int page) {
     const int key = first + (lane & 31);
-    bool in = key < e.len;
+    bool in = wanted(key);
     if (in && (unsigned)page >= (unsigned long long)a.pages) {
       in = false;
       if (a.error) atomicOr(a.error, kErrInvalid);

@@ -681,8 +681,10 @@ recis_status recis_cache_append(const recis_append_desc* desc, const void* q, co
  * 0) or j < sinks; else every row sees all kv_lens[b] keys.  out and lse as
  * recis_cross_attn_fwd, lse [rows of q, q_heads]; a row that sees no key gives 0
  * and -infinity, rows of no entry are left as they were.  What the cache holds
- * past an entry's length is not looked at.  A value that is not finite may reach
- * rows of its own entry that do not see it. */
+ * past an entry's length is not looked at, nor are keys before the window that no
+ * new row sees, or the numbers of their pages, which may be given away.  Of other
+ * keys a value that is not finite may reach rows of its own entry that do not see
+ * it. */
 typedef struct {
   int32_t dtype;
   int32_t batch;

@@ -413,6 +413,32 @@ def test_paged_attention_pages_that_entries_share(seq):
         within(got, *plain.paged_attention(q, kc, vc, table, lens, 32**-0.5)["o"])
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 0), (9, 4), (100, 33), (64, 64)])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new,page_size,heads", [(1, 16, (4, 4, 32)), (2, 5, (6, 2, 40)), (50, 16, (4, 2, 64)),
+                                                 (140, 7, (2, 2, 77)), (300, 64, (2, 1, 128)), (33, 1, (3, 3, 16))])
+def test_paged_attention_pages_behind_the_window_may_be_gone(seq, new, page_size, heads, dtype, window, sinks):
+    """Pages that no new row sees a key of are not read: neither their numbers nor what lies there now."""
+    (hq, hkv, dim), lens = heads, [700, 300, 411]
+    gen = generator(new, page_size, window, 47)
+    kc, vc, table = cache_case(gen, len(lens), lens, page_size, hkv, dim, dtype)
+    q = normal(gen, len(lens), new, hq, dim, dtype=dtype).cuda()
+    how = {"window": window, "sinks": sinks}
+    before = seq.paged_attention(q, kc.cuda(), vc.cuda(), table.cuda(), ints(*lens).cuda(), return_lse=True, **how)
+    spare = kc.shape[0] - 1 if not bool(kc[-1].isfinite().any()) else int((~kc.isfinite().flatten(1).any(1)).nonzero()[0])
+    for gone in (-1, 1 << 30, spare):   # spare: a page of NaN
+        now = table.clone()
+        for b, n in enumerate(lens):
+            page = torch.arange(table.shape[1])
+            first, last = page * page_size, (page + 1) * page_size - 1
+            now[b, (first >= sinks) & (last < n - new - window + 1)] = gone
+        assert bool((now != table).any())
+        error = torch.zeros(1, dtype=I32).cuda()
+        after = seq.paged_attention(q, kc.cuda(), vc.cuda(), now.cuda(), ints(*lens).cuda(), return_lse=True, error=error, **how)
+        seq.check(error)
+        assert torch.equal(after[0], before[0]) and torch.equal(after[1], before[1])
+
+
 @pytest.mark.parametrize("factor,scale", [(30.0, None), (1e-3, 1e3), (1.0, 1e-6)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_paged_attention_large_and_small_scores(seq, dtype, factor, scale):
