@@ -444,13 +444,14 @@ __device__ __forceinline__ void walk_rows(const BandArgs& a, int b, int h, int t
 }
 
 // A pair's far blocks run beside its near ones -- both wait for memory more than for each
-// other -- in one launch, WHAT = kNear + kFar, where that leaves the near walk its waves,
-// else in one each.  (Forward and backward of 9 entries of 777 positions, 6 heads of 40,
-// window 100, 3 sinks, float32: 157 us with two launches, 148 with one; of 32 entries
-// of up to 4096, 8 heads of 64, window 512, 4 sinks, bfloat16: 662, 657.)
+// other -- in one launch, WHAT = kNear + kFar, where that leaves the near walk its registers,
+// else in one each.  (Forward and backward of 32 entries of up to 4096 positions, 8 heads of
+// 64, window 512, 4 sinks, bfloat16: 662 us with two launches, 657 with one; the backward of 8
+// entries of 2048, 8 heads of 64 that share 2, window 256, float32, whose near walk spills
+// then: 404, 505.)
 constexpr int kNear = 1, kFar = 2;
 template <typename T, int DP>
-constexpr bool kFarBeside = DP <= 64;
+constexpr bool kFarBeside = sizeof(T) == 2 && DP <= 64;
 
 template <typename T, int DP, bool ALN, int WHAT>
 __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(BandArgs a) {
