@@ -65,8 +65,7 @@ struct BandArgs {
   int ranked;                  // entries take their turns by length, the longest first
   int pairs_inner;             // in a unit: a tile's pairs next to each other, else a pair's tiles
   int per;                     // blocks of a pair, in this launch
-  int far_per;                 // those of them that walk the sinks' far rows: the first
-  Quick by_inner, by_across, by_splits, by_far;  // blocks of the inner order, of a unit, of a tile and of a far tile
+  Quick by_inner, by_across, by_splits;  // blocks of the inner order, of a unit and of a tile, in this launch
   float scale;
   float *part_o, *part_ml;     // parts of key ranges: [pair][split][rows][head_dim], [..][2]
   float* part_kv;              // parts of row ranges: [pair][split][part_keys][2][head_dim], then far ones
@@ -82,15 +81,13 @@ inline int band_dp(int head_dim) { return (head_dim + 31) / 32 * 32; }
 // bfloat16's time and a few tiles must go round: 33 entries of up to 999 keys, 50 rows, 6 heads
 // of 40: 49 us with 64, 39 with 32.)
 inline int band_keys(int dtype, int head_dim) { return dtype == RECIS_DTYPE_F32 && head_dim > 32 ? 32 : 64; }
-// The grid of a launch of `tiles` tiles a pair in `splits` parts each, and of far ones.
-inline dim3 band_grid(BandArgs* a, int64_t tiles, int64_t splits, int64_t far_tiles = 0, int64_t far_splits = 1) {
-  const int64_t per = tiles * splits + far_tiles * far_splits, unit = a->unit;
+// The grid of a launch of `tiles` tiles a pair in `splits` parts each.
+inline dim3 band_grid(BandArgs* a, int64_t tiles, int64_t splits) {
+  const int64_t per = tiles * splits, unit = a->unit;
   a->per = (int)per;
-  a->far_per = (int)(far_tiles * far_splits);
   a->by_inner = Quick(a->pairs_inner ? unit : per);
   a->by_across = Quick(per * unit);
   a->by_splits = Quick(splits);
-  a->by_far = Quick(far_splits);
   return grid_of(round_up((int64_t)a->batch * a->kv_heads, unit << a->die_bits) * per);
 }
 // How the blocks of a call are laid over the dies.
@@ -216,24 +213,17 @@ __device__ __forceinline__ int split_size(int n, int splits, int least) {
 
 // Consecutive blocks go to the eight dies in turn; a unit is the pairs of an entry, or one
 // pair, and shares a die and its L2.
-__device__ __forceinline__ bool band_place(const BandArgs& a, int* b, int* h, int* t) {
+__device__ __forceinline__ bool band_place(const BandArgs& a, int* b, int* h, int* tile, int* split) {
   const int id = block_id(), slot = id >> a.die_bits, turn = divided(slot, a.by_across);
   const int rest = slot - turn * a.by_across.d, outer = divided(rest, a.by_inner);
   const int inner = rest - outer * a.by_inner.d;
-  *t = a.pairs_inner ? outer : inner;
-  const int in_unit = a.pairs_inner ? inner : outer;
+  const int t = a.pairs_inner ? outer : inner, in_unit = a.pairs_inner ? inner : outer;
   const int pair = ((turn << a.die_bits) + (id & ((1 << a.die_bits) - 1))) * a.unit + in_unit;
+  *tile = divided(t, a.by_splits);
+  *split = t - *tile * a.by_splits.d;
   *b = divided(pair, a.by_kv_heads);
   *h = pair - *b * a.kv_heads;
   return *b < a.batch;
-}
-// Tile and split of a pair's block t.
-__device__ __forceinline__ bool band_place(const BandArgs& a, int* b, int* h, int* tile, int* split) {
-  int t;
-  if (!band_place(a, b, h, &t)) return false;
-  *tile = divided(t, a.by_splits);
-  *split = t - *tile * a.by_splits.d;
-  return true;
 }
 
 // The entry that is `rank`th by length, of 64 at most, those without rows last: blocks of a

@@ -254,35 +254,26 @@ __device__ __forceinline__ float* part_far(const BandArgs& a, long long pair, in
   return a.part_kv + (near + (pair * a.sink_splits + split) * a.far_keys + key) * 2 * a.head_dim;
 }
 
-template <typename T, int DP, bool FAR>
-struct KvTiles {
-  static constexpr int R = kWalkRows<DP, FAR>, kTile = R * kLd<T, DP>;
-  // (the far walk's waves have rows of their own, so one buffer and no barrier)
-  static constexpr int kBuffers = FAR ? 1 : 2;
-  union {
-    T tiles[kBuffers * 2 * kTile];
-    float sums[FAR ? 32 * DP : 1];  // of the far walk's waves
-  } __attribute__((aligned(128)));
-  float stat_l[kBuffers][R] __attribute__((aligned(16)));
-  float stat_d[kBuffers][R] __attribute__((aligned(16)));
-  int stat_p[kBuffers][R] __attribute__((aligned(16)));
-};
-
 template <typename T, int DP, bool ALN, bool FAR>
-__device__ __forceinline__ void walk_rows(const BandArgs& a, int b, int h, int t, KvTiles<T, DP, FAR>& lds) {
+__global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32;
-  constexpr int R = KvTiles<T, DP, FAR>::R, kTile = KvTiles<T, DP, FAR>::kTile, kBuffers = KvTiles<T, DP, FAR>::kBuffers;
-  T* const tiles = lds.tiles;
-  auto& stat_l = lds.stat_l;
-  auto& stat_d = lds.stat_d;
-  auto& stat_p = lds.stat_p;
-  const Quick& by_splits = FAR ? a.by_far : a.by_splits;
-  const int splits = by_splits.d, tile = divided(t, by_splits), split = t - tile * splits;
+  constexpr int R = kWalkRows<DP, FAR>, kTile = R * kLd<T, DP>;
+  // (the far walk's waves have rows of their own, so one buffer and no barrier)
+  constexpr int kBuffers = FAR ? 1 : 2;
+  constexpr int kTileBytes = kBuffers * 2 * kTile * (int)sizeof(T);
+  constexpr int kJoinBytes = FAR ? 32 * DP * 4 : 0;
+  __shared__ __attribute__((aligned(128))) char tile_bytes[kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes];
+  T* const tiles = reinterpret_cast<T*>(tile_bytes);
+  __shared__ __attribute__((aligned(16))) float stat_l[kBuffers][R], stat_d[kBuffers][R];
+  __shared__ __attribute__((aligned(16))) int stat_p[kBuffers][R];
+  int b, h, tile, split;
+  if (!band_place(a, &b, &h, &tile, &split)) return;
+  const int splits = a.by_splits.d;
   const long long pair = (long long)b * a.kv_heads + h;
   const int lane = threadIdx.x & 63, wave = wave_of();
   if constexpr (!FAR) {
-    zero_spare<T>(a, a.dk, a.dks, h, 1, b, t, a.per - a.far_per);
-    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, t, a.per - a.far_per);
+    zero_spare<T>(a, a.dk, a.dks, h, 1, b, tile * splits + split, a.per);
+    zero_spare<T>(a, a.dv, a.dvs, h, 1, b, tile * splits + split, a.per);
   }
   const Entry e = entry_at<false>(a, b);
   const int block_key = FAR ? tile * 32 : tile * kTileKeys128;
@@ -398,7 +389,7 @@ __device__ __forceinline__ void walk_rows(const BandArgs& a, int b, int h, int t
   }
   if constexpr (FAR) {
     // the waves' sums, one wave after the other, dK and then dV
-    float* sums = lds.sums;
+    float* sums = reinterpret_cast<float*>(tile_bytes);
     for (int half = 0; half < 2; ++half) {
       for (int w = 0; w < kBandWaves; ++w) {
         __syncthreads();
@@ -441,32 +432,6 @@ __device__ __forceinline__ void walk_rows(const BandArgs& a, int b, int h, int t
       store_result<T, ALN>(tv, d, lane, a.head_dim, dv[d], 1.f);
     }
   }
-}
-
-// A pair's far blocks run beside its near ones -- both wait for memory more than for each
-// other -- in one launch, WHAT = kNear + kFar, where that leaves the near walk its registers,
-// else in one each.  (Forward and backward of 32 entries of up to 4096 positions, 8 heads of
-// 64, window 512, 4 sinks, bfloat16: 662 us with two launches, 657 with one; the backward of 8
-// entries of 2048, 8 heads of 64 that share 2, window 256, float32, whose near walk spills
-// then: 404, 505.)
-constexpr int kNear = 1, kFar = 2;
-template <typename T, int DP>
-constexpr bool kFarBeside = sizeof(T) == 2 && DP <= 64;
-
-template <typename T, int DP, bool ALN, int WHAT>
-__global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(BandArgs a) {
-  __shared__ union {
-    KvTiles<T, DP, WHAT == kFar> first;
-    KvTiles<T, DP, WHAT != kNear> second;
-  } lds;
-  int b, h, t;
-  if (!band_place(a, &b, &h, &t)) return;
-  if constexpr (WHAT == kNear)
-    walk_rows<T, DP, ALN, false>(a, b, h, t, lds.first);
-  else if (WHAT == kFar || t < a.far_per)
-    walk_rows<T, DP, ALN, true>(a, b, h, t, lds.second);
-  else
-    walk_rows<T, DP, ALN, WHAT == kFar>(a, b, h, t - a.far_per, lds.first);
 }
 
 // Adds a key's parts of dK and dV, near ones and then far ones, in order: V elements a
@@ -532,20 +497,11 @@ void launch_bwd(BandArgs a, hipStream_t s) {
     else
       hipLaunchKernelGGL((k_band_join_q<T, 1, K>), blocks, dim3(kThreads), 0, s, a);
   }
-  const int64_t far = a.sink_splits ? a.far_keys / 32 : 0;
-  const bool beside = far && kFarBeside<T, DP>;
-  grid = band_grid(&a, a.key_tiles, a.kv_splits, beside ? far : 0, a.sink_splits);
-  if (beside) {
-    if constexpr (kFarBeside<T, DP>)
-      hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, kNear + kFar>), grid, dim3(kThreads), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, kNear>), grid, dim3(kThreads), 0, s, a);
-  }
-  if constexpr (!kFarBeside<T, DP>) {
-    if (far) {
-      grid = band_grid(&a, 0, 1, far, a.sink_splits);
-      hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, kFar>), grid, dim3(kThreads), 0, s, a);
-    }
+  grid = band_grid(&a, a.key_tiles, a.kv_splits);
+  hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, false>), grid, dim3(kThreads), 0, s, a);
+  if (a.sink_splits) {
+    grid = band_grid(&a, a.far_keys / 32, a.sink_splits);
+    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, true>), grid, dim3(kThreads), 0, s, a);
   }
   if (a.sink_splits || a.kv_splits > 1) {
     const dim3 blocks = grid_of((pairs * a.part_keys * 2 * (a.head_dim / v) + kThreads - 1) / kThreads);
@@ -631,7 +587,8 @@ SelfPlan self_plan(const recis_self_attn_desc* d) {
                                 d->head_dim * 4, 256);
   auto fits = [&](int64_t per) { return round_up(pairs, (int64_t)kDies * d->kv_heads) * per <= kMaxBlocks; };
   p.launchable[0] = fits((int64_t)p.row_tiles * p.splits);
-  p.launchable[1] = p.launchable[0] && fits((int64_t)p.key_tiles * p.kv_splits + p.far_keys / 32 * p.sink_splits) &&
+  p.launchable[1] = p.launchable[0] && fits((int64_t)p.key_tiles * p.kv_splits) &&
+                    fits(std::max<int64_t>(1, p.far_keys / 32) * std::max(1, p.sink_splits)) &&
                     pairs * p.part_keys * 2 * d->head_dim / kThreads < kMaxBlocks;
   return p;
 }
