@@ -13,6 +13,22 @@
 // sinks, then those from the window of the first row to the position of the last.
 // The running maximum that the weights are taken relative to is raised only once a
 // score exceeds it by 2^kSlack in weight.
+//
+// Bound, at long walks, by the matrix unit's and the vector unit's turns at two to four
+// waves a SIMD (causal, 32 entries of 4096 positions, 8 heads, bfloat16: heads of 64 796 us,
+// 690 TFLOP/s, of 128 1365 us, 806 TFLOP/s; there the matrix unit is busy 35% of the
+// cycles, the vector unit 46%, LDS 44%, two fifths of that for conflicts; without the
+// exponentials it would take 1503 us, without loads and barriers 1110, with the products
+// and their LDS reads alone 960).  Short windows are bound by the tiles at a window's
+// ends, computed whole or by halves of 32 keys, and by each block's start: window 512 of
+// up to 4096, 8 heads of 64 160 us, of up to 1000 packed, window 128, 4 heads of 32 97 us.
+// Over a cache, 32 entries of up to 512 rows and 8192 keys, 16 heads of 128 that share 4:
+// 425 to 460 us, 580 to 630 TFLOP/s.  Float32: 58 to 85 TFLOP/s of the 154 that a large
+// product reaches, padded head sizes and half-seen tiles counted as lost.
+//
+// Tried, for the same time: raised wave priority around the products, a fixed order of
+// products, exponentials and LDS reads, the LDS reads ahead of the products, two blocks'
+// scores interleaved; slower: masks by comparison in place of bits.
 #include <algorithm>
 #include <cmath>
 

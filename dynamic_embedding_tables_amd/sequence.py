@@ -573,7 +573,8 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
     itself among them, and the first `sinks` ones.  Not causal (candidates reading a history), every row sees all
     kv_lens[b] keys.  Returns q's shape (in out, if given) and with return_lse the float32 log of the sums of
     exponentials [.., q_heads].  Rows that see no key, at negative positions or of an entry without keys, give zeros
-    and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf."""
+    and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf.
+    Keys before the window that no new row sees are not read, nor their pages' numbers: such pages may be given away."""
     if stream is not None:
         with _on(stream, q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, error):
             return paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal, window,

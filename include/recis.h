@@ -644,7 +644,8 @@ recis_status recis_rotary(const recis_rotary_desc* desc, int32_t backward, const
  * rot_dim > 0: recis_rotary) and values, and, where q_heads > 0, writes the turned
  * queries of the same rows to q_out (which may be q).  Padding rows, rows of no
  * entry and rows whose page is out of range are not stored; rows of no entry get
- * zeros in q_out.  Entries must not share the slots that they append to. */
+ * zeros in q_out (with batch 0 nothing is written, here and below).  Entries must
+ * not share the slots that they append to. */
 typedef struct {
   int32_t dtype;              /* of q, k, v and the caches */
   int32_t batch;
