@@ -103,7 +103,20 @@ inline void place_pairs(BandArgs* a, int dtype) {
   a->pairs_inner = !once;
   a->die_bits = (int64_t)a->batch * a->kv_heads >= kPairsForDies ? kDieBits : 0;
 }
-void launch_band_fwd(int dtype, bool paged, bool aln, const BandArgs& a, hipStream_t s);
+// Elements an access takes: 8 where rows are aligned to 16 bytes, 2 where all are to pairs, else 1.
+inline int band_access(int dtype, int head_dim, std::initializer_list<const void*> ptrs,
+                       std::initializer_list<const long long*> strides) {
+  for (int w : {8, 2}) {
+    const int bytes = w == 8 ? 16 : 2 * dtype_size(dtype), per = bytes / dtype_size(dtype);
+    bool all = head_dim % w == 0;
+    for (const void* p : ptrs) all = all && aligned_to(p, bytes);
+    for (const long long* s : strides)
+      for (int i = 0; i < 3; ++i) all = all && s[i] % per == 0;
+    if (all) return w;
+  }
+  return 1;
+}
+void launch_band_fwd(int dtype, bool paged, int access, const BandArgs& a, hipStream_t s);
 
 namespace {
 
@@ -343,9 +356,9 @@ __device__ __forceinline__ Frag<T> half_of(const f32x16& x) {
 // Elements 32 * block .. of a lane's row of a result (columns are rows of the tensor), times
 // `by`.  A lane and the one 32 away hold alternate 4 elements; bfloat16 pairs are exchanged
 // so that each stores 8 in a row.
-template <typename T, bool ALN>
+template <typename T, int W>
 __device__ __forceinline__ void store_result(T* row, int block, int lane, int dim, const f32x16& x, float by) {
-  if constexpr (ALN && sizeof(T) == 2) {
+  if constexpr (W == 8 && sizeof(T) == 2) {
     typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     auto two = [&](int i) { return __builtin_bit_cast(unsigned, bf16x2{(__bf16)(x[i] * by), (__bf16)(x[i + 1] * by)}); };
@@ -359,27 +372,54 @@ __device__ __forceinline__ void store_result(T* row, int block, int lane, int di
   } else {
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
-      store4<T, ALN>(row, block * 32 + result_row(lane, i), dim,
+      store4<T, W == 8>(row, block * 32 + result_row(lane, i), dim,
                      f32x4{x[i] * by, x[i + 1] * by, x[i + 2] * by, x[i + 3] * by});
+  }
+}
+
+// 8 elements from d0 of a row that is there, W at a time; past its `dim` elements anything,
+// which zero_past() makes zeros.  By 2, those past the end are the last pair again, since a
+// load behind a branch would be waited for there (16 entries of 1024, 8 heads of 74, bfloat16:
+// 142 us against 214 by 1 and with branches); by 1 eight such addresses cost more than the
+// branches (heads of 77: 227 us against 206).
+template <typename T, int W>
+__device__ __forceinline__ Frag<T> load_any(const T* row, int d0, int dim) {
+  Frag<T> f;
+  if constexpr (W == 8) {
+    f = *reinterpret_cast<const Frag<T>*>(row + (d0 < dim ? d0 : 0));
+  } else if constexpr (W == 2) {
+    typedef T Part __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const Part x = *reinterpret_cast<const Part*>(row + std::min(d0 + i, dim - 2));
+      f[i] = x[0], f[i + 1] = x[1];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = d0 + i < dim ? row[d0 + i] : (T)0.f;
+  }
+  return f;
+}
+template <typename T, int W>
+__device__ __forceinline__ void zero_past(Frag<T>& f, int d0, int dim) {
+  if constexpr (W == 8) {
+    if (d0 >= dim) f = Frag<T>{};
+  } else if (W == 2 && d0 + 8 > dim) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (d0 + i >= dim) f[i] = (T)0.f;
   }
 }
 
 // A lane's operands for the KK chunks (16 elements each) of a row that is there; zeros
 // past its `dim` elements.
-template <typename T, int KK, bool ALN>
+template <typename T, int KK, int W>
 __device__ __forceinline__ void load_row16(Frag<T> (&f)[KK], const T* row, int lane, int dim) {
 #pragma unroll
-  for (int c = 0; c < KK; ++c) {
-    const int d = c * 16 + (lane >> 5) * 8;
-    if constexpr (ALN)
-      f[c] = *reinterpret_cast<const Frag<T>*>(row + (d < dim ? d : 0));
-    else
-      f[c] = load8<T, false>(row, d, dim, true);
-  }
-  if (ALN && dim < KK * 16) {
+  for (int c = 0; c < KK; ++c) f[c] = load_any<T, W>(row, c * 16 + (lane >> 5) * 8, dim);
+  if (dim < KK * 16) {
 #pragma unroll
-    for (int c = 0; c < KK; ++c)
-      if (c * 16 + (lane >> 5) * 8 >= dim) f[c] = Frag<T>{};
+    for (int c = 0; c < KK; ++c) zero_past<T, W>(f[c], c * 16 + (lane >> 5) * 8, dim);
   }
 }
 
@@ -424,7 +464,7 @@ __device__ __forceinline__ f32x8 cols32(const float* tile, int row0, int c0, int
 // past the length or masked, elements past the head -- is loaded from a place that is,
 // and replaced by zeros on the way to LDS: no load stands behind a branch, after which
 // the compiler would wait for it (that wait took a third of the forward's time).
-template <typename T, int DP, int K, bool PAGED, bool ALN>
+template <typename T, int DP, int K, bool PAGED, int W>
 struct KeyStage {
   static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = K / kStep;
   static_assert(K % kStep == 0, "every thread has the same number of chunks");
@@ -460,33 +500,34 @@ struct KeyStage {
         const int slot = key - page_of(a, key) * a.by_page.d;
         int p = page[i];
         if ((unsigned)p >= (unsigned long long)a.pages) p = 0, bad = true;
-        if constexpr (ALN) {  // (strides are below 2^31)
+        if constexpr (W == 8) {  // (strides are below 2^31)
           fk[i] = at_bytes(kb + ((unsigned long long)(unsigned)p * (unsigned)a.ks[0] +
                                  (unsigned long long)(unsigned)slot * (unsigned)a.ks[1]), at_d);
           fv[i] = at_bytes(vb + ((unsigned long long)(unsigned)p * (unsigned)a.vs[0] +
                                  (unsigned long long)(unsigned)slot * (unsigned)a.vs[1]), at_d);
         } else {
-          const bool in = first + in_tile < len;
-          fk[i] = load8<T, false>(kb + (long long)p * a.ks[0] + (long long)slot * a.ks[1], d0, a.head_dim, in);
-          fv[i] = load8<T, false>(vb + (long long)p * a.vs[0] + (long long)slot * a.vs[1], d0, a.head_dim, in);
+          fk[i] = load_any<T, W>(kb + (long long)p * a.ks[0] + (long long)slot * a.ks[1], d0, a.head_dim);
+          fv[i] = load_any<T, W>(vb + (long long)p * a.vs[0] + (long long)slot * a.vs[1], d0, a.head_dim);
         }
-      } else if constexpr (ALN) {  // (a tile's bytes are below 2^31)
+      } else if constexpr (W == 8) {  // (a tile's bytes are below 2^31)
         const unsigned r = std::min(in_tile, len - 1 - first);
         fk[i] = at_bytes(tile_k, r * (unsigned)(a.ks[1] * sizeof(T)) + at_d);
         fv[i] = at_bytes(tile_v, r * (unsigned)(a.vs[1] * sizeof(T)) + at_d);
       } else {
-        const bool in = bits >> in_tile & 1;
-        fk[i] = load8<T, false>(tile_k + (long long)in_tile * a.ks[1], d0, a.head_dim, in);
-        fv[i] = load8<T, false>(tile_v + (long long)in_tile * a.vs[1], d0, a.head_dim, in);
+        const int r = std::min(in_tile, len - 1 - first);
+        fk[i] = load_any<T, W>(tile_k + (long long)r * a.ks[1], d0, a.head_dim);
+        fv[i] = load_any<T, W>(tile_v + (long long)r * a.vs[1], d0, a.head_dim);
       }
     }
   }
   // `bits`: the keys of the loaded tile that are there
   __device__ __forceinline__ void store(const BandArgs& a, T* tk, T* tv, unsigned long long bits) {
-    if (ALN && ((K == 64 ? bits != ~0ull : (unsigned)bits != ~0u) || a.head_dim < kCols<DP>)) {
+    if ((K == 64 ? bits != ~0ull : (unsigned)bits != ~0u) || a.head_dim < kCols<DP>) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (W == 2) zero_past<T, W>(fk[i], d0, a.head_dim), zero_past<T, W>(fv[i], d0, a.head_dim);
         if (!(bits >> (row + i * kStep) & 1) || d0 >= a.head_dim) fk[i] = fv[i] = Frag<T>{};
+      }
     }
     if (kCols<DP> > DP && d0 >= DP) return;
 #pragma unroll

@@ -36,7 +36,7 @@ template <typename T, int DP>
 constexpr int kBackwardWaves = DP > 64 || (sizeof(T) == 4 && DP > 32) ? 2 : sizeof(T) == 2 && DP <= 32 ? 4 : 3;
 
 // dQ, and each row's L (in log2 of the weight) and delta for dK and dV.
-template <typename T, int DP, bool ALN>
+template <typename T, int DP, int W>
 __global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_q(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32, K = kBandKeys<T, DP>, KB = K / 32;
   constexpr int kTile = K * kLd<T, DP>;
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_
   f32x16 dq[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) dq[d] = zeros16();
-  KeyStage<T, DP, K, false, ALN> st;
+  KeyStage<T, DP, K, false, W> st;
   st.start(a);
   unsigned long long bits = 0;
   if (i0 < i1) {
@@ -76,9 +76,9 @@ __global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_
   {
     const int in = std::min(r, rows - 1);
     Frag<T> out[KK];
-    load_row16<T, KK, ALN>(q, static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, in), lane, a.head_dim);
-    load_row16<T, KK, ALN>(g, static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, in), lane, a.head_dim);
-    load_row16<T, KK, ALN>(out, static_cast<const T*>(a.o) + query_at(a, a.os, e, b, h, in), lane, a.head_dim);
+    load_row16<T, KK, W>(q, static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, in), lane, a.head_dim);
+    load_row16<T, KK, W>(g, static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, in), lane, a.head_dim);
+    load_row16<T, KK, W>(out, static_cast<const T*>(a.o) + query_at(a, a.os, e, b, h, in), lane, a.head_dim);
 #pragma unroll
     for (int c = 0; c < KK; ++c)
 #pragma unroll
@@ -161,12 +161,12 @@ __global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_
   if (walk.n > per) {
     float* to = a.part_o + ((((long long)b * a.kv_heads + h) * a.q_splits + split) * a.rows + r) * a.head_dim;
 #pragma unroll
-    for (int d = 0; d < DB; ++d) store_result<float, false>(to, d, lane, a.head_dim, dq[d], 1.f);
+    for (int d = 0; d < DB; ++d) store_result<float, 1>(to, d, lane, a.head_dim, dq[d], 1.f);
     return;
   }
   T* to = static_cast<T*>(a.dq) + query_at(a, a.dqs, e, b, h, r);
 #pragma unroll
-  for (int d = 0; d < DB; ++d) store_result<T, ALN>(to, d, lane, a.head_dim, dq[d], a.scale);
+  for (int d = 0; d < DB; ++d) store_result<T, W>(to, d, lane, a.head_dim, dq[d], a.scale);
 }
 
 // Adds the key ranges' parts of dQ, in order: V elements of a row a thread.
@@ -207,7 +207,7 @@ constexpr int kWalkRows = FAR ? 128 : DP <= 64 ? 64 : 32;
 // A thread's chunks of R folded rows of Q and dO on their way to LDS.  Rows from `until` on
 // are loaded from the one before it and zeroed by store(): no load stands behind a branch.
 // OWN: each wave stages 32 rows of its own.
-template <typename T, int DP, int R, bool OWN, bool ALN>
+template <typename T, int DP, int R, bool OWN, int W>
 struct RowStage {
   static constexpr int kAcross = kCols<DP> / 8, kStep = (OWN ? 64 : kThreads) / kAcross, kPer = (OWN ? 32 : R) / kStep;
   static_assert((OWN ? 32 : R) % kStep == 0, "every thread has the same number of chunks");
@@ -218,28 +218,23 @@ struct RowStage {
     d0 = (threadIdx.x % kAcross) * 8;
   }
   __device__ __forceinline__ void load(const BandArgs& a, Entry e, int b, int h, int first, int until) {
-    const int d = d0 < a.head_dim ? d0 : 0;
     here = until - first;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = std::min(first + row + i * kStep, until - 1);
       const T* pq = static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, r);
       const T* pg = static_cast<const T*>(a.dout) + query_at(a, a.dos, e, b, h, r);
-      if constexpr (ALN) {
-        fq[i] = *reinterpret_cast<const Frag<T>*>(pq + d);
-        fg[i] = *reinterpret_cast<const Frag<T>*>(pg + d);
-      } else {
-        const bool in = row + i * kStep < here;
-        fq[i] = load8<T, false>(pq, d0, a.head_dim, in);
-        fg[i] = load8<T, false>(pg, d0, a.head_dim, in);
-      }
+      fq[i] = load_any<T, W>(pq, d0, a.head_dim);
+      fg[i] = load_any<T, W>(pg, d0, a.head_dim);
     }
   }
   __device__ __forceinline__ void store(const BandArgs& a, T* tq, T* tg) {
-    if (ALN && (here < R || a.head_dim < kCols<DP>)) {
+    if (here < R || a.head_dim < kCols<DP>) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (W == 2) zero_past<T, W>(fq[i], d0, a.head_dim), zero_past<T, W>(fg[i], d0, a.head_dim);
         if (row + i * kStep >= here || d0 >= a.head_dim) fq[i] = fg[i] = Frag<T>{};
+      }
     }
     if (kCols<DP> > DP && d0 >= DP) return;
 #pragma unroll
@@ -263,7 +258,7 @@ __device__ __forceinline__ float* part_far(const BandArgs& a, long long pair, in
   return a.part_kv + (near + (pair * a.sink_splits + split) * a.far_keys + key) * 2 * a.head_dim;
 }
 
-template <typename T, int DP, bool ALN, bool FAR>
+template <typename T, int DP, int W, bool FAR>
 __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32;
   constexpr int R = kWalkRows<DP, FAR>, kTile = R * kLd<T, DP>;
@@ -311,7 +306,7 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
   for (int d = 0; d < DB; ++d) dk[d] = dv[d] = zeros16();
   const f32x2* row_stats = a.stats + pair * a.rows;
   const f32x2 none{INFINITY, 0.f};  // rows that do not exist: weight 0
-  RowStage<T, DP, R, FAR, ALN> st;
+  RowStage<T, DP, R, FAR, W> st;
   f32x2 stat = none;
   // the row whose L and delta the thread takes (twice over in a wave of its own rows)
   const int stat_row = FAR ? wave * 32 + (lane & 31) : (int)threadIdx.x;
@@ -326,8 +321,8 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
   }
   if (e.len > 0) {  // (a key that does not count spoils its own column only, which is zero at the end)
     const int there = std::min(key, e.len - 1);
-    load_row16<T, KK, ALN>(k, kb + (long long)there * a.ks[1], lane, a.head_dim);
-    load_row16<T, KK, ALN>(v, vb + (long long)there * a.vs[1], lane, a.head_dim);
+    load_row16<T, KK, W>(k, kb + (long long)there * a.ks[1], lane, a.head_dim);
+    load_row16<T, KK, W>(v, vb + (long long)there * a.vs[1], lane, a.head_dim);
   }
   int buffer = 0;
   for (int step = s0; step < s1; ++step, buffer ^= kBuffers - 1) {
@@ -427,8 +422,8 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
       float* to = part_near(a, pair, split, key);
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        store_result<float, false>(to, d, lane, a.head_dim, dk[d], 1.f);
-        store_result<float, false>(to + a.head_dim, d, lane, a.head_dim, dv[d], 1.f);
+        store_result<float, 1>(to, d, lane, a.head_dim, dk[d], 1.f);
+        store_result<float, 1>(to + a.head_dim, d, lane, a.head_dim, dv[d], 1.f);
       }
       return;
     }
@@ -437,8 +432,8 @@ __global__ __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) void k_band_bwd_kv(Band
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
       if (!in) dk[d] = dv[d] = zeros16();
-      store_result<T, ALN>(tk, d, lane, a.head_dim, dk[d], a.scale);
-      store_result<T, ALN>(tv, d, lane, a.head_dim, dv[d], 1.f);
+      store_result<T, W>(tk, d, lane, a.head_dim, dk[d], a.scale);
+      store_result<T, W>(tv, d, lane, a.head_dim, dv[d], 1.f);
     }
   }
 }
@@ -492,13 +487,13 @@ __global__ __launch_bounds__(kThreads) void k_band_join_kv(BandArgs a) {
 }
 
 // ----------------------------------------------------------- sizes, launches
-template <typename T, int DP, bool ALN>
+template <typename T, int DP, int W>
 void launch_bwd(BandArgs a, hipStream_t s) {
   constexpr int K = kBandKeys<T, DP>;
   const int64_t pairs = (int64_t)a.batch * a.kv_heads;
   const int v = a.head_dim % 4 ? 1 : 4;
   dim3 grid = band_grid(&a, a.row_tiles, a.q_splits);
-  hipLaunchKernelGGL((k_band_bwd_q<T, DP, ALN>), grid, dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_band_bwd_q<T, DP, W>), grid, dim3(kThreads), 0, s, a);
   if (a.q_splits > 1) {
     const dim3 blocks((unsigned)((pairs * a.rows * (a.head_dim / v) + kThreads - 1) / kThreads));
     if (v == 4)
@@ -507,10 +502,10 @@ void launch_bwd(BandArgs a, hipStream_t s) {
       hipLaunchKernelGGL((k_band_join_q<T, 1, K>), blocks, dim3(kThreads), 0, s, a);
   }
   grid = band_grid(&a, a.key_tiles, a.kv_splits);
-  hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, false>), grid, dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_band_bwd_kv<T, DP, W, false>), grid, dim3(kThreads), 0, s, a);
   if (a.sink_splits) {
     grid = band_grid(&a, a.far_keys / 32, a.sink_splits);
-    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, ALN, true>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_band_bwd_kv<T, DP, W, true>), grid, dim3(kThreads), 0, s, a);
   }
   if (a.sink_splits || a.kv_splits > 1) {
     const dim3 blocks = grid_of((pairs * a.part_keys * 2 * (a.head_dim / v) + kThreads - 1) / kThreads);
@@ -521,13 +516,23 @@ void launch_bwd(BandArgs a, hipStream_t s) {
   }
 }
 
+template <typename T, int DP>
+void launch_bwd_by(int access, const BandArgs& a, hipStream_t s) {
+  if (access == 8)
+    launch_bwd<T, DP, 8>(a, s);
+  else if (access == 2)
+    launch_bwd<T, DP, 2>(a, s);
+  else
+    launch_bwd<T, DP, 1>(a, s);
+}
+
 template <typename T>
-void launch_bwd_dp(bool aln, const BandArgs& a, hipStream_t s) {
+void launch_bwd_dp(int access, const BandArgs& a, hipStream_t s) {
   switch (band_dp(a.head_dim)) {
-    case 32: return aln ? launch_bwd<T, 32, true>(a, s) : launch_bwd<T, 32, false>(a, s);
-    case 64: return aln ? launch_bwd<T, 64, true>(a, s) : launch_bwd<T, 64, false>(a, s);
-    case 96: return aln ? launch_bwd<T, 96, true>(a, s) : launch_bwd<T, 96, false>(a, s);
-    default: return aln ? launch_bwd<T, 128, true>(a, s) : launch_bwd<T, 128, false>(a, s);
+    case 32: return launch_bwd_by<T, 32>(access, a, s);
+    case 64: return launch_bwd_by<T, 64>(access, a, s);
+    case 96: return launch_bwd_by<T, 96>(access, a, s);
+    default: return launch_bwd_by<T, 128>(access, a, s);
   }
 }
 
@@ -648,19 +653,13 @@ void fill_self(const recis_self_attn_desc* d, const SelfPlan& p, BandArgs* a) {
 }
 
 // Rows can be moved 16 bytes at a time.
-bool self_aligned(int dtype, const BandArgs& a, std::initializer_list<const void*> ptrs,
-                  std::initializer_list<const long long*> strides) {
-  const int per = 16 / dtype_size(dtype);
-  if (a.head_dim % 8) return false;
-  for (const void* p : ptrs)
-    if (!aligned_to(p, 16)) return false;
-  for (const long long* s : strides)
-    for (int i = 0; i < 3; ++i)
-      if (s[i] % per) return false;
+int self_access(int dtype, const BandArgs& a, std::initializer_list<const void*> ptrs,
+                std::initializer_list<const long long*> strides) {
+  const int access = band_access(dtype, a.head_dim, ptrs, strides);
   // a tile's rows stay within 32 bits of byte offset
   for (const long long* s : {a.ks, a.vs})
-    if (s[1] < 0 || s[1] >= (1 << 23)) return false;
-  return true;
+    if (access == 8 && (s[1] < 0 || s[1] >= (1 << 23))) return 1;
+  return access;
 }
 
 bool all_there(const recis_self_attn_desc* d, std::initializer_list<const void*> ptrs) {
@@ -702,8 +701,8 @@ recis_status recis_self_attn_fwd(const recis_self_attn_desc* desc, const void* q
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
-  const bool aln = self_aligned(desc->dtype, a, {q, k, v, out}, {a.qs, a.ks, a.vs, a.os});
-  launch_band_fwd(desc->dtype, false, aln, a, s);
+  const int access = self_access(desc->dtype, a, {q, k, v, out}, {a.qs, a.ks, a.vs, a.os});
+  launch_band_fwd(desc->dtype, false, access, a, s);
   return launch_status();
 }
 
@@ -732,12 +731,12 @@ recis_status recis_self_attn_bwd(const recis_self_attn_desc* desc, const void* g
   a.stats = static_cast<f32x2*>(workspace);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.dq_at);
   a.part_kv = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.kv_at);
-  const bool aln = self_aligned(desc->dtype, a, {q, k, v, out, grad_out, grad_q, grad_k, grad_v},
-                                {a.qs, a.ks, a.vs, a.os, a.dos, a.dqs, a.dks, a.dvs});
+  const int access = self_access(desc->dtype, a, {q, k, v, out, grad_out, grad_q, grad_k, grad_v},
+                                 {a.qs, a.ks, a.vs, a.os, a.dos, a.dqs, a.dks, a.dvs});
   if (desc->dtype == RECIS_DTYPE_BF16)
-    launch_bwd_dp<__bf16>(aln, a, s);
+    launch_bwd_dp<__bf16>(access, a, s);
   else
-    launch_bwd_dp<float>(aln, a, s);
+    launch_bwd_dp<float>(access, a, s);
   return launch_status();
 }
 

@@ -41,7 +41,7 @@ namespace {
 template <typename T, int DP>
 constexpr int kForwardWaves = DP > 64 ? 2 : sizeof(T) == 2 ? 4 : DP > 32 ? 2 : 3;
 
-template <typename T, int DP, bool PAGED, bool ALN>
+template <typename T, int DP, bool PAGED, int W>
 __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(BandArgs a) {
   constexpr int KK = DP / 16, DB = DP / 32, K = kBandKeys<T, DP>, KB = K / 32;
   constexpr int kTile = K * kLd<T, DP>;
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   // score may go before both are raised, sum
   float m = -INFINITY, ref = 0.f, most = -INFINITY, l = 0.f;
   const float c2 = a.scale * kLog2e;
-  KeyStage<T, DP, K, PAGED, ALN> st;
+  KeyStage<T, DP, K, PAGED, W> st;
   st.start(a, block_reach.low - a.window + 1);  // (below 0: all of them)
   unsigned long long bits = 0;
   if (i0 < i1) {
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i0 + 1, i1 - 1)) * K, e.len);
   }
   Frag<T> q[KK];  // (after the first keys' loads, which take longer)
-  load_row16<T, KK, ALN>(q, static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, std::min(r, rows - 1)), lane,
+  load_row16<T, KK, W>(q, static_cast<const T*>(a.q) + query_at(a, a.qs, e, b, h, std::min(r, rows - 1)), lane,
                          a.head_dim);
   int buffer = 0;
   for (int i = i0; i < i1; ++i, buffer ^= 1) {
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     const long long at = (((long long)b * a.kv_heads + h) * a.splits + split) * a.rows + r;
     float* po = a.part_o + at * a.head_dim;
 #pragma unroll
-    for (int d = 0; d < DB; ++d) store_result<float, false>(po, d, lane, a.head_dim, o[d], 1.f);
+    for (int d = 0; d < DB; ++d) store_result<float, 1>(po, d, lane, a.head_dim, o[d], 1.f);
     if (lane < 32) {
       a.part_ml[2 * at] = m * c2;
       a.part_ml[2 * at + 1] = l;
@@ -202,38 +202,40 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* out = static_cast<T*>(a.out) + query_at(a, a.os, e, b, h, r);
 #pragma unroll
-  for (int d = 0; d < DB; ++d) store_result<T, ALN>(out, d, lane, a.head_dim, o[d], inv);
+  for (int d = 0; d < DB; ++d) store_result<T, W>(out, d, lane, a.head_dim, o[d], inv);
   if (a.lse && lane < 32) a.lse[lse_at(a, e, b, h, r)] = l == 0.f ? -INFINITY : m * a.scale + __logf(l);
 }
 
 template <typename T, int DP, bool PAGED>
-void launch_fwd(bool aln, BandArgs a, hipStream_t s) {
+void launch_fwd(int access, BandArgs a, hipStream_t s) {
   const dim3 grid = band_grid(&a, a.row_tiles, a.splits);
-  if (aln)
-    hipLaunchKernelGGL((k_band_fwd<T, DP, PAGED, true>), grid, dim3(kThreads), 0, s, a);
+  if (access == 8)
+    hipLaunchKernelGGL((k_band_fwd<T, DP, PAGED, 8>), grid, dim3(kThreads), 0, s, a);
+  else if (access == 2)
+    hipLaunchKernelGGL((k_band_fwd<T, DP, PAGED, 2>), grid, dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((k_band_fwd<T, DP, PAGED, false>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_band_fwd<T, DP, PAGED, 1>), grid, dim3(kThreads), 0, s, a);
   if (a.splits <= 1) return;
   launch_join<T, PAGED, kBandKeys<T, DP>, kBandRows, kLeastTiles>(a, s);
 }
 
 template <typename T, bool PAGED>
-void launch_fwd_dp(bool aln, const BandArgs& a, hipStream_t s) {
+void launch_fwd_dp(int access, const BandArgs& a, hipStream_t s) {
   switch (band_dp(a.head_dim)) {
-    case 32: return launch_fwd<T, 32, PAGED>(aln, a, s);
-    case 64: return launch_fwd<T, 64, PAGED>(aln, a, s);
-    case 96: return launch_fwd<T, 96, PAGED>(aln, a, s);
-    default: return launch_fwd<T, 128, PAGED>(aln, a, s);
+    case 32: return launch_fwd<T, 32, PAGED>(access, a, s);
+    case 64: return launch_fwd<T, 64, PAGED>(access, a, s);
+    case 96: return launch_fwd<T, 96, PAGED>(access, a, s);
+    default: return launch_fwd<T, 128, PAGED>(access, a, s);
   }
 }
 
 }  // namespace
 
-void launch_band_fwd(int dtype, bool paged, bool aln, const BandArgs& a, hipStream_t s) {
+void launch_band_fwd(int dtype, bool paged, int access, const BandArgs& a, hipStream_t s) {
   if (dtype == RECIS_DTYPE_BF16)
-    paged ? launch_fwd_dp<__bf16, true>(aln, a, s) : launch_fwd_dp<__bf16, false>(aln, a, s);
+    paged ? launch_fwd_dp<__bf16, true>(access, a, s) : launch_fwd_dp<__bf16, false>(access, a, s);
   else
-    paged ? launch_fwd_dp<float, true>(aln, a, s) : launch_fwd_dp<float, false>(aln, a, s);
+    paged ? launch_fwd_dp<float, true>(access, a, s) : launch_fwd_dp<float, false>(access, a, s);
 }
 
 }  // namespace recis

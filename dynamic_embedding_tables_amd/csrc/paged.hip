@@ -330,19 +330,12 @@ bool paged_grid_fits(const recis_paged_attn_desc* d, const PagedPlan& p) {
   return round_up((int64_t)d->batch * d->kv_heads, (int64_t)kDies * d->kv_heads) * p.row_tiles * p.splits <= kMaxBlocks;
 }
 
-// Rows can be moved 16 bytes at a time.
-bool paged_aligned(int dtype, const BandArgs& a, std::initializer_list<const void*> ptrs) {
-  const int per = 16 / dtype_size(dtype);
-  if (a.head_dim % 8) return false;
-  for (const void* p : ptrs)
-    if (!aligned_to(p, 16)) return false;
-  for (const long long* s : {a.qs, a.os, a.ks, a.vs})
-    for (int i = 0; i < 3; ++i)
-      if (s[i] % per) return false;
+int paged_access(int dtype, const BandArgs& a, std::initializer_list<const void*> ptrs) {
+  const int access = band_access(dtype, a.head_dim, ptrs, {a.qs, a.os, a.ks, a.vs});
   // a wave's slots stay within 32 bits of byte offset
   for (const long long* s : {a.ks, a.vs})
-    if (s[1] < 0 || s[1] >= (1 << 23) || s[0] < 0 || s[0] >= (1ll << 31)) return false;
-  return true;
+    if (access == 8 && (s[1] < 0 || s[1] >= (1 << 23) || s[0] < 0 || s[0] >= (1ll << 31))) return 1;
+  return access;
 }
 
 }  // namespace
@@ -414,13 +407,13 @@ recis_status recis_paged_attn_fwd(const recis_paged_attn_desc* d, const void* q,
   a.scale = d->scale;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_at);
-  const bool aln = paged_aligned(d->dtype, a, {q, out, k_cache, v_cache});
+  const int access = paged_access(d->dtype, a, {q, out, k_cache, v_cache});
   if (!p.few)
-    launch_band_fwd(d->dtype, true, aln, a, s);
+    launch_band_fwd(d->dtype, true, access, a, s);
   else if (d->dtype == RECIS_DTYPE_BF16)
-    launch_few_dp<__bf16>(aln, a, s);
+    launch_few_dp<__bf16>(access == 8, a, s);
   else
-    launch_few_dp<float>(aln, a, s);
+    launch_few_dp<float>(access == 8, a, s);
   return launch_status();
 }
 

@@ -549,6 +549,31 @@ def test_self_attention_strides(seq, dim, dtype):
         assert torch.equal(a, b)
 
 
+def shifted(t, by):
+    """The same values on the GPU in rows two elements apart, beginning `by` elements into an allocation."""
+    wide = torch.zeros(t.numel() // t.shape[-1] * (t.shape[-1] + 2) + by, dtype=t.dtype, device="cuda")
+    return wide[by:].view(*t.shape[:-1], t.shape[-1] + 2)[..., :t.shape[-1]].copy_(t)
+
+
+@pytest.mark.parametrize("by", [0, 1, 2])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [2, 10, 38, 74, 126])
+def test_attention_of_even_heads_that_are_not_eights(seq, dim, dtype, by):
+    """Rows of pairs, and the same from an address that is not one of a pair."""
+    gen = generator(dim, by, 48)
+    for kind, band in (("all", (40, 3)), ("packed mask", None)):
+        check_self(seq, *self_case(gen, (3, 210, 4, 2, dim), dtype, kind), band, (kind, band), lambda t: shifted(t, by))
+    lens, new = [300, 41], 40
+    kc, vc, table = cache_case(gen, 2, lens, 24, 2, dim, dtype)
+    q = normal(gen, 2, new, 4, dim, dtype=dtype)
+    clean = [torch.nan_to_num(t.float()).to(dtype) for t in (kc, vc)]
+    for rows in (new, 1):
+        got = seq.paged_attention(shifted(q[:, :rows], by), shifted(kc, by), shifted(vc, by), table.cuda(), ints(*lens).cuda(),
+                                  window=70, sinks=2)
+        want = plain.paged_attention(q[:, :rows], *clean, table, lens, dim**-0.5, window=70, sinks=2)
+        within(got, *want["o"], what=rows)
+
+
 @pytest.mark.parametrize("factor,scale", [(30.0, None), (1e-3, 1e3), (1.0, 1e-6)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_self_attention_large_and_small_scores(seq, dtype, factor, scale):
