@@ -469,7 +469,7 @@ struct KeyStage {
   static constexpr int kAcross = kCols<DP> / 8, kStep = kThreads / kAcross, kPer = K / kStep;
   static_assert(K % kStep == 0, "every thread has the same number of chunks");
   Frag<T> fk[kPer], fv[kPer];
-  int page[kPer];  // of the tile that comes next
+  int page;        // paged: of key `lane` of the tile that comes next
   int row, d0, window_lo;
   unsigned at_d;   // bytes into the head
   bool bad;
@@ -481,9 +481,15 @@ struct KeyStage {
     bad = false;
   }
   __device__ __forceinline__ void ask_pages(const BandArgs& a, const int* table, int first, int len) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      page[i] = table[page_of(a, in_reach(a, std::min(first + row + i * kStep, len - 1), window_lo))];
+    page = table[page_of(a, in_reach(a, std::min(first + ((int)threadIdx.x & (K - 1)), len - 1), window_lo))];
+  }
+  // Bit i: key first + i of the tile that comes next is there, its page's number one of the
+  // cache's.  (Asked once a tile by each wave, a key a lane, and passed on by exchange.)  A page
+  // out of range is read as page 0, which is there.
+  __device__ __forceinline__ unsigned long long paged_bits(const BandArgs& a, int first, int len) {
+    const bool in = (unsigned)page < (unsigned long long)a.pages;
+    if (!in) page = 0, bad = true;
+    return __ballot(in && first + ((int)threadIdx.x & (K - 1)) < len);
   }
   static __device__ __forceinline__ Frag<T> at_bytes(const T* base, unsigned bytes) {
     return *reinterpret_cast<const Frag<T>*>(reinterpret_cast<const char*>(base) + bytes);
@@ -498,8 +504,7 @@ struct KeyStage {
       if constexpr (PAGED) {
         const int key = in_reach(a, std::min(first + in_tile, len - 1), window_lo);
         const int slot = key - page_of(a, key) * a.by_page.d;
-        int p = page[i];
-        if ((unsigned)p >= (unsigned long long)a.pages) p = 0, bad = true;
+        const int p = __shfl(page, in_tile);
         if constexpr (W == 8) {  // (strides are below 2^31)
           fk[i] = at_bytes(kb + ((unsigned long long)(unsigned)p * (unsigned)a.ks[0] +
                                  (unsigned long long)(unsigned)slot * (unsigned)a.ks[1]), at_d);
@@ -537,7 +542,6 @@ struct KeyStage {
       *reinterpret_cast<Frag<T>*>(tv + at) = fv[i];
     }
   }
-  // (a page out of range is read as page 0, which is there)
   __device__ __forceinline__ void tell(const BandArgs& a) const {
     if (PAGED && bad && a.error) atomicOr(a.error, kErrInvalid);
   }

@@ -83,11 +83,17 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
   const float c2 = a.scale * kLog2e;
   KeyStage<T, DP, K, PAGED, W> st;
   st.start(a, block_reach.low - a.window + 1);  // (below 0: all of them)
+  auto keys_there = [&](int first) {
+    if constexpr (PAGED)
+      return st.paged_bits(a, first, e.len);
+    else
+      return band_bits(a, e, b, first, lane);
+  };
   unsigned long long bits = 0;
   if (i0 < i1) {
     const int first = walk.tile(i0) * K;
     if constexpr (PAGED) st.ask_pages(a, table, first, e.len);
-    bits = band_bits(a, e, b, first, lane);
+    bits = keys_there(first);
     st.load(a, kb, vb, first, e.len, bits);
     if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i0 + 1, i1 - 1)) * K, e.len);
   }
@@ -104,7 +110,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     __syncthreads();
     {  // (after the last tile, that one again: a branch would have its loads waited for)
       const int next = walk.tile(std::min(i + 1, i1 - 1)) * K;
-      bits = band_bits(a, e, b, next, lane);
+      bits = keys_there(next);
       st.load(a, kb, vb, next, e.len, bits);
       if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i + 2, i1 - 1)) * K, e.len);
     }

@@ -574,7 +574,8 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
     kv_lens[b] keys.  Returns q's shape (in out, if given) and with return_lse the float32 log of the sums of
     exponentials [.., q_heads].  Rows that see no key, at negative positions or of an entry without keys, give zeros
     and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf.
-    Keys before the window that no new row sees are not read, nor their pages' numbers: such pages may be given away."""
+    Keys before the window that no new row sees are not read, nor their pages' numbers: such pages may be given away.
+    Keys of another page whose number is out of range do not count (and are recorded in error)."""
     if stream is not None:
         with _on(stream, q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, error):
             return paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal, window,

@@ -1,0 +1,86 @@
+"""What the operators of a growing history make of inputs that are out of range or laid out unusually, on the GPU against
+their definitions in 64 bits (bounds: history_plain)."""
+import pytest
+import torch
+
+import history_plain as plain
+from sequence_plain import within
+from test_history_gpu import BF16, DTYPES, F32, I32, cache_case, generator, ints, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from dynamic_embedding_tables_amd import recis
+    recis.load_library()
+
+
+@pytest.fixture
+def seq():
+    from dynamic_embedding_tables_amd import sequence
+    return sequence
+
+
+def without_bad_pages(q, kc, vc, table, lens, offsets=None, causal=True, window=None, sinks=0):
+    """{o, lse: (value, bound)}: paged attention to the keys whose page's number is one."""
+    pages, page_size = kc.shape[:2]
+    val = {"o": torch.zeros_like(q, dtype=torch.float64),
+           "lse": torch.full(q.shape[:-1], -float("inf"), dtype=torch.float64)}
+    err = {n: torch.full_like(x, 1e-30) for n, x in val.items()}
+    for b, rows in enumerate(plain.new_rows(table.shape[0], q.shape[1], offsets)):
+        at, n, total = (b, rows) if offsets is None else (rows,), len(rows), lens[b]
+        if not n or not total:
+            continue
+        keys = torch.arange(total)
+        there = (table[b] >= 0) & (table[b] < pages)
+        ok = there[keys // page_size][None].expand(n, total)
+        if causal:
+            ok = ok & plain.seen(total - n + torch.arange(n), keys, window, sinks)
+        known = torch.where(there, table[b], 0)
+        got = plain.attention(q[at], plain.keys_of(kc, known, page_size, total),
+                              plain.keys_of(vc, known, page_size, total), ok, q.shape[-1] ** -0.5)
+        for name, (x, e) in got.items():
+            val[name][at], err[name][at] = x, e
+    return {n: (val[n], err[n]) for n in val}
+
+
+@pytest.mark.parametrize("how", [{}, {"window": 70, "sinks": 9}, {"causal": False}])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new,page_size,heads", [
+    (1, 16, (4, 4, 32)), (4, 5, (8, 2, 40)), (16, 64, (1, 1, 128)), (17, 64, (1, 1, 128)), (40, 5, (8, 2, 40)),
+    (150, 16, (4, 2, 64)), (33, 24, (2, 2, 77)), (20, 1, (2, 1, 74)), (70, 128, (2, 1, 96)),
+])
+def test_keys_of_a_page_out_of_range_do_not_count(seq, new, page_size, heads, dtype, how):
+    """The same for few rows and for many, told or not: such a key has no weight, and no other entry's key takes its
+    place."""
+    from dynamic_embedding_tables_amd import recis
+    (hq, hkv, dim), lens = heads, [700, 150, 333, 260]
+    gen = generator(new, page_size, dim, len(how))
+    kc, vc, table = cache_case(gen, len(lens), lens, page_size, hkv, dim, dtype, garbage=0.0)
+    kc[0], vc[0] = 3.0, 50.0   # page 0 would be noticed
+    table[table == 0] = kc.shape[0] - 1
+    pages = kc.shape[0]
+    last = [-(-n // page_size) - 1 for n in lens]
+    table[0, last[0] // 2], table[0, 0], table[0, last[0]] = -1, pages, 1 << 30
+    table[1] = -1   # no key at all
+    table[2, last[2] - 1:] = (1 << 31) - 1
+    dev = [t.cuda() for t in (kc, vc, table, ints(*lens))]
+    for packed in (False, True):
+        if packed:
+            counts = [max(0, new - i) for i in range(len(lens))]
+            offsets = torch.tensor([sum(counts[:i]) for i in range(len(lens) + 1)], dtype=I32)
+            q, more = normal(gen, sum(counts), hq, dim, dtype=dtype), {"q_offsets": offsets.cuda(), "max_q_len": new}
+        else:
+            q, offsets, more = normal(gen, len(lens), new, hq, dim, dtype=dtype), None, {}
+        error = torch.zeros(1, dtype=I32).cuda()
+        o, lse = seq.paged_attention(q.cuda(), *dev, return_lse=True, error=error, **how, **more)
+        with pytest.raises(recis.RecisError) as e:
+            seq.check(error)
+        assert e.value.status == recis.RECIS_ERR_INVALID_ARG
+        want = without_bad_pages(q, kc, vc, table, lens, offsets, **how)
+        within(o, *want["o"], what=(packed, "o"))
+        within(lse, *want["lse"], what=(packed, "lse"))
+        assert torch.equal(seq.paged_attention(q.cuda(), *dev, **how, **more), o)
