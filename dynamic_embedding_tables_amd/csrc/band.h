@@ -290,7 +290,7 @@ constexpr int kBandKeys = sizeof(T) == 4 && DP > 32 ? 32 : 64;
 
 // Zeros for `heads` heads from h of the packed rows that no entry writes: those before
 // the first and after the last, a part of them from each of the head's blocks, and those
-// of an entry of too many, from its own `per` blocks (t of them).
+// of an entry that is taken as empty (entry_at), from its own `per` blocks (t of them).
 template <typename T>
 __device__ __forceinline__ void zero_rows(T* to, const long long (&st)[3], int h, int heads, int dim, long long lo,
                                           long long hi, long long end, int block, int blocks) {
@@ -309,7 +309,8 @@ __device__ __forceinline__ void zero_spare(const BandArgs& a, void* to, const lo
   if (first > 0 || last < a.total_rows)
     zero_rows(static_cast<T*>(to), st, h, heads, a.head_dim, first, std::max(first, last), a.total_rows, b * per + t,
               a.batch * per);
-  if (hi - lo > a.q_len) zero_rows(static_cast<T*>(to), st, h, heads, a.head_dim, 0, lo, hi, t, per);
+  if (hi - lo > a.q_len || a.offsets[b] < 0 || a.offsets[b + 1] > a.total_rows)
+    zero_rows(static_cast<T*>(to), st, h, heads, a.head_dim, 0, lo, hi, t, per);
 }
 
 // ------------------------------------------------------------ 32x32 products

@@ -754,7 +754,7 @@ int64_t recis_self_attn_workspace_bytes(const recis_self_attn_desc* desc, int32_
 /* out and lse (float32 [batch, len, q_heads] or [rows, q_heads], may be NULL) as
  * recis_cross_attn_fwd.  A row that sees no key, past its entry's length among
  * them, gives 0 and -infinity; packed rows of no entry get 0 in out and nothing in
- * lse.  What masked positions and positions past the length hold is not looked at;
+ * lse, and so do those of an entry whose offsets are out of range.  What masked positions and positions past the length hold is not looked at;
  * a value that is not finite may reach rows of its own entry that do not see it. */
 recis_status recis_self_attn_fwd(const recis_self_attn_desc* desc, const void* q, const void* k, const void* v,
                                  void* out, float* lse, void* workspace, int64_t workspace_bytes, hipStream_t s);

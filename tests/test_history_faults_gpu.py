@@ -84,3 +84,46 @@ def test_keys_of_a_page_out_of_range_do_not_count(seq, new, page_size, heads, dt
         within(o, *want["o"], what=(packed, "o"))
         within(lse, *want["lse"], what=(packed, "lse"))
         assert torch.equal(seq.paged_attention(q.cuda(), *dev, **how, **more), o)
+
+
+def leave_nan(*like):
+    """Memory that the next tensors of these shapes are likely to get, full of NaN."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full_like(t, float("nan")) for t in like for _ in range(4)]
+    del held
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim,hq,hkv", [(16, 2, 2), (77, 4, 2), (128, 3, 1)])
+@pytest.mark.parametrize("offsets,max_len", [
+    ((0, 120, 361, 361), 360), ((0, 120, 400, 500), 360), ((-3, 120, 200, 360), 360), ((0, 120, (1 << 31) - 1), 360),
+    ((-(1 << 31), 7, 300, 360), 360), ((-9, -5, 361, 400), 360), ((0, 300, 360), 299),
+])
+def test_rows_of_an_entry_out_of_range_are_zeros(seq, offsets, max_len, dim, hq, hkv, dtype):
+    """An entry whose rows are not all there, or too many, is taken as one without rows: nothing that was in memory
+    before comes back in its place."""
+    from dynamic_embedding_tables_amd import recis
+    gen = generator(dim, hq, max_len)
+    q, grad = (normal(gen, 360, hq, dim, dtype=dtype) for _ in range(2))
+    k, v = (normal(gen, 360, hkv, dim, dtype=dtype) for _ in range(2))
+    good = [(lo, hi) for lo, hi in zip(offsets, offsets[1:]) if 0 <= lo <= hi <= 360 and hi - lo <= max_len]
+    dev = [t.cuda() for t in (q, k, v)]
+    kw = {"offsets": ints(*offsets).cuda(), "max_len": max_len, "window": 50, "sinks": 3}
+    error = torch.zeros(1, dtype=I32).cuda()
+    leave_nan(*dev)
+    o, lse = seq.self_attention(*dev, return_lse=True, error=error, **kw)
+    with pytest.raises(recis.RecisError):
+        seq.check(error)
+    leave_nan(*dev)
+    grads = seq.self_attention_backward(grad.cuda(), *dev, o, lse, **kw)
+    want = {n: [torch.zeros(t.shape, dtype=torch.float64) + (-float("inf") if n == "lse" else 0.0),
+                torch.full(t.shape, 1e-30, dtype=torch.float64)]
+            for n, t in (("o", q), ("lse", q[..., 0]), ("dq", q), ("dk", k), ("dv", v))}
+    for lo, hi in good:
+        pos = torch.arange(hi - lo)
+        got = plain.attention(q[lo:hi], k[lo:hi], v[lo:hi], plain.seen(pos, pos, 50, 3), dim**-0.5, grad[lo:hi])
+        for n, (x, e) in got.items():
+            want[n][0][lo:hi], want[n][1][lo:hi] = x, e
+    for name, t in zip(want, (o, lse, *grads)):
+        within(t, *want[name], what=(offsets, name))
