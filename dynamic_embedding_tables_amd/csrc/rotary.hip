@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(AppendArgs a) {
       b = entry_of(a.offsets, ends[0], ends[1], n);
       i = n - a.offsets[b];
       count = (int64_t)a.offsets[b + 1] - a.offsets[b];
-      in = i >= 0 && i < count && a.offsets[b + 1] <= a.rows;
+      in = i >= 0 && i < count && a.offsets[b] >= 0 && a.offsets[b + 1] <= a.rows;
     } else {
       b = n / a.new_len;
       i = n - b * a.new_len;

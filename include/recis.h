@@ -637,9 +637,10 @@ recis_status recis_rotary(const recis_rotary_desc* desc, int32_t backward, const
  * padded batch, or rows q_offsets[b] .. q_offsets[b + 1] - 1 of a packed one; the
  * last of them is at position kv_lens[b] - 1, and rows that fall at negative
  * positions are padding.  On the GPU, a length, offset or page out of range
- * records RECIS_ERR_INVALID_ARG; keys of a page out of range are not stored and
- * do not count.  Limits (else UNSUPPORTED): table_width * page_size 2^30, 2^31
- * pages.
+ * records RECIS_ERR_INVALID_ARG: an entry whose offsets are out of range is taken
+ * as one without rows, one whose length is as one without keys, and keys of a page
+ * out of range are not stored and do not count.  Limits (else UNSUPPORTED):
+ * table_width * page_size 2^30, 2^31 pages.
  *
  * recis_cache_append stores the new keys (turned by their positions, where
  * rot_dim > 0: recis_rotary) and values, and, where q_heads > 0, writes the turned

@@ -127,3 +127,32 @@ def test_rows_of_an_entry_out_of_range_are_zeros(seq, offsets, max_len, dim, hq,
             want[n][0][lo:hi], want[n][1][lo:hi] = x, e
     for name, t in zip(want, (o, lse, *grads)):
         within(t, *want[name], what=(offsets, name))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("offsets", [(-3, 4, 8), (-(1 << 31), 4, 8), (0, 4, 9), (0, 5, (1 << 31) - 1), (-1, 4, 9)])
+def test_append_of_an_entry_out_of_range_stores_nothing(seq, offsets, dtype):
+    """As the attention that reads the cache: an entry whose rows are not all there is taken as one without rows."""
+    from dynamic_embedding_tables_amd import recis
+    gen, lens = generator(len(offsets), 91), [20, 17]
+    kc, vc, table = cache_case(gen, 2, lens, 8, 2, 16, dtype, garbage=7.0)
+    k, v = (normal(gen, 8, 2, 16, dtype=dtype) for _ in range(2))
+    q, freqs = normal(gen, 8, 4, 16, dtype=dtype), seq.rotary_frequencies(16)
+    dk, dv, error = kc.cuda(), vc.cuda(), torch.zeros(1, dtype=I32).cuda()
+    got = seq.cache_append(k.cuda(), v.cuda(), dk, dv, table.cuda(), ints(*lens).cuda(), q=q.cuda(),
+                           q_offsets=ints(*offsets).cuda(), freqs=freqs, error=error)
+    with pytest.raises(recis.RecisError) as e:
+        seq.check(error)
+    assert e.value.status == recis.RECIS_ERR_INVALID_ARG
+    want_k, bound_k, want_v = kc.double(), torch.zeros_like(kc, dtype=torch.float64), vc.clone()
+    want_q = [torch.zeros_like(q, dtype=torch.float64), torch.full_like(q, 1e-30, dtype=torch.float64)]
+    for b, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        if 0 <= lo and hi <= 8:
+            pos = lens[b] - (hi - lo) + torch.arange(hi - lo)
+            where = plain.slots(table[b], 8, pos)
+            want_k[where], bound_k[where] = plain.rotary(k[lo:hi], freqs.cpu(), pos, False, 1.0)
+            want_v[where] = v[lo:hi]
+            want_q[0][lo:hi], want_q[1][lo:hi] = plain.rotary(q[lo:hi], freqs.cpu(), pos, False, 1.0)
+    within(dk, want_k, bound_k)
+    assert torch.equal(dv.cpu(), want_v)
+    within(got, *want_q)
