@@ -483,7 +483,7 @@ def _paged(page_table, kv_lens, q_offsets, batch, error):
     if page_table.dtype != torch.int32 or len(width) != 2 or width[0] != batch:
         raise ValueError(f"page_table must be int32 [{batch}, pages an entry may have]")
     stride = page_table.stride()
-    if width[1] > 1 and stride[1] != 1:
+    if (width[1] > 1 and stride[1] != 1) or (batch > 1 and stride[0] < width[1]):  # (one row expanded among them)
         page_table = page_table.contiguous()
         stride = page_table.stride()
     if kv_lens.dtype != torch.int32 or tuple(kv_lens.shape) != (batch,):

@@ -156,3 +156,25 @@ def test_append_of_an_entry_out_of_range_stores_nothing(seq, offsets, dtype):
     within(dk, want_k, bound_k)
     assert torch.equal(dv.cpu(), want_v)
     within(got, *want_q)
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_page_tables_whose_rows_overlap(seq, new):
+    """One history that several entries read (candidates of one user): its row of the table expanded, not repeated."""
+    gen = generator(new, 92)
+    kc, vc, table = cache_case(gen, 1, [90], 16, 2, 32, F32, garbage=0.0)
+    q = normal(gen, 5, new, 4, 32).cuda()
+    dev = (kc.cuda(), vc.cuda())
+    lens = ints(90, 90, 17, 64, 33).cuda()
+    want = seq.paged_attention(q, *dev, table.expand(5, -1).contiguous().cuda(), lens, causal=False)
+    assert torch.equal(seq.paged_attention(q, *dev, table.cuda().expand(5, -1), lens, causal=False), want)
+    row = torch.cat([table[0], table[0]]).cuda()   # entry b's pages begin one further on
+    sliding = row.as_strided((5, table.shape[1]), (1, 1))
+    want = seq.paged_attention(q, *dev, sliding.contiguous(), lens)
+    assert torch.equal(seq.paged_attention(q, *dev, sliding, lens), want)
+    k = normal(gen, 2, 1, 2, 32).cuda()   # and the append, to slots that the entries do not share
+    two = table.cuda().expand(2, -1)
+    seq.cache_append(k, k, *dev, two, ints(3, 20).cuda())
+    for b, n in enumerate((3, 20)):
+        page, slot = plain.slots(table[0], 16, torch.tensor([n - 1]))
+        assert torch.equal(dev[0][page.cuda(), slot.cuda()], k[b]) and torch.equal(dev[1][page.cuda(), slot.cuda()], k[b])
