@@ -575,7 +575,8 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
     exponentials [.., q_heads].  Rows that see no key, at negative positions or of an entry without keys, give zeros
     and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf.
     Keys before the window that no new row sees are not read, nor their pages' numbers: such pages may be given away.
-    Keys of another page whose number is out of range do not count (and are recorded in error)."""
+    Keys of another page whose number is out of range do not count (and are recorded in error).  A cache whose heads
+    are not contiguous is copied whole first, with a warning."""
     if stream is not None:
         with _on(stream, q, k_cache, v_cache, page_table, kv_lens, q_offsets, out, error):
             return paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets, max_q_len, causal, window,
@@ -596,8 +597,12 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
     batch = q_offsets.numel() - 1 if packed else shape[0]
     width, table_st, at, keep = _paged(page_table, kv_lens, q_offsets, batch, error)
     q, q_st = _heads_st(q, head_dim)
+    given = k_cache, v_cache
     k_cache, k_st = _heads_st(k_cache, head_dim)
     v_cache, v_st = _heads_st(v_cache, head_dim)
+    if k_cache is not given[0] or v_cache is not given[1]:
+        warnings.warn("a cache whose heads are not contiguous is copied whole, in every call of paged_attention",
+                      stacklevel=2)
     if out is None:
         out = q.new_zeros(shape) if packed else _like(q)
     else:

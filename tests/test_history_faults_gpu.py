@@ -1,5 +1,7 @@
 """What the operators of a growing history make of inputs that are out of range or laid out unusually, on the GPU against
 their definitions in 64 bits (bounds: history_plain)."""
+import warnings
+
 import pytest
 import torch
 
@@ -178,3 +180,18 @@ def test_page_tables_whose_rows_overlap(seq, new):
     for b, n in enumerate((3, 20)):
         page, slot = plain.slots(table[0], 16, torch.tensor([n - 1]))
         assert torch.equal(dev[0][page.cuda(), slot.cuda()], k[b]) and torch.equal(dev[1][page.cuda(), slot.cuda()], k[b])
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_a_cache_that_is_copied_is_warned_about(seq, new):
+    """Heads whose elements are strided: the whole cache is copied, on every call, and not silently."""
+    gen = generator(new, 93)
+    kc, vc, table = cache_case(gen, 2, [90, 40], 16, 2, 32, F32, garbage=0.0)
+    q, kc, vc, table, lens = (t.cuda() for t in (normal(gen, 2, new, 4, 32), kc, vc, table, ints(90, 40)))
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        want = seq.paged_attention(q, kc, vc, table, lens)
+    apart = [t.transpose(2, 3).contiguous().transpose(2, 3) for t in (kc, vc)]
+    for caches in ((apart[0], vc), (kc, apart[1]), apart):
+        with pytest.warns(UserWarning, match="copied whole"):
+            assert torch.equal(seq.paged_attention(q, *caches, table, lens), want)
