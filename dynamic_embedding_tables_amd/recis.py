@@ -259,6 +259,15 @@ def _check(st: int, where: str):
 _raw_stream = _current_device = None
 
 
+def _forget_stream():
+    global _raw_stream, _current_device
+    _raw_stream = _current_device = None
+
+
+# (torch refuses the GPU in a process forked off one that uses it, but its functions that are kept here do not)
+os.register_at_fork(after_in_child=_forget_stream)
+
+
 def _stream(stream=None):
     """The HIP stream handle of `stream`, or of torch's current stream (asked
     for directly: building the Stream object takes 3 us, more than most calls'
