@@ -446,7 +446,7 @@ def evict_pass(torch, table, min_count=2, decay=0.5):
 
 # The sequence operators' sources: no kernel of the table's is built from them,
 # so its counter summaries stay valid when they change.
-SEQUENCE_SOURCES = ("attn.h", "attn.hip", "band.h", "band_bwd.hip", "band_fwd.hip", "embed.hip", "norm.hip",
+SEQUENCE_SOURCES = ("attn.h", "attn.hip", "band.h", "band_bwd.hip", "band_fwd.hip", "divide.h", "embed.hip", "norm.hip",
                     "paged.hip", "rotary.hip", "seq.h")
 
 

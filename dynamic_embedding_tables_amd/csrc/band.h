@@ -18,29 +18,11 @@
 #include <type_traits>
 
 #include "attn.h"
+#include "divide.h"
 
 namespace recis {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// x / d for 0 <= x < 2^31, without a division: the compiler's takes some 30 dependent
-// instructions, and a block of few tiles does a dozen before its first load.
-struct Quick {
-  int d, shift;
-  unsigned mul, one;
-  Quick() = default;
-  explicit Quick(int64_t by) : d((int)by), shift(0), mul(0), one(~0u) {
-    if (by <= 1) return;
-    int bits = 0;
-    while ((1ll << bits) < by) ++bits;
-    mul = (unsigned)((1ull << (31 + bits)) / by + 1);
-    shift = bits - 1;
-    one = 0;
-  }
-};
-__device__ __forceinline__ int divided(int x, const Quick& q) {
-  return (int)((__umulhi((unsigned)x, q.mul) + ((unsigned)x & q.one)) >> q.shift);
-}
 
 struct BandArgs {
   const void *q, *k, *v, *o, *dout;

@@ -20,6 +20,7 @@
 // last-level cache answers.  One event each for 64 users: 3 to 4 us, the launch.
 #include <algorithm>
 
+#include "divide.h"
 #include "seq.h"
 
 namespace recis {
@@ -29,13 +30,6 @@ constexpr int kMaxTurnDim = 1024;           // elements a head
 constexpr int kMaxTokenElems = 1 << 18;     // elements a token
 constexpr int kTurnTable = 1024;            // pairs of LDS a block: 8 KB
 constexpr int kMaxTokens = 64;              // tokens a block
-
-// x / d for x * d < 2^32.
-struct Div {
-  unsigned d, mul;
-};
-Div div_by(int64_t d) { return Div{(unsigned)d, d > 1 ? (unsigned)(((1ull << 32) + d - 1) / d) : 0}; }
-__device__ __forceinline__ unsigned divided(unsigned x, Div v) { return v.d == 1 ? x : __umulhi(x, v.mul); }
 
 struct Turns {
   const double* freqs;
