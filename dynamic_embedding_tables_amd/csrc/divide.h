@@ -1,5 +1,6 @@
 // divide.h -- divisions by numbers that are the same for a whole launch, as a
-// multiplication by what the host works out once.
+// multiplication by what the host works out once.  (It includes nothing of HIP's, so
+// that a host program can check it: include it after seq.h.)
 #pragma once
 
 #include <cstdint>

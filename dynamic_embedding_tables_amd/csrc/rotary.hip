@@ -20,8 +20,8 @@
 // last-level cache answers.  One event each for 64 users: 3 to 4 us, the launch.
 #include <algorithm>
 
-#include "divide.h"
 #include "seq.h"
+#include "divide.h"
 
 namespace recis {
 namespace {
