@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import history_plain as plain
-from sequence_plain import within
+from sequence_plain import U, U32, within
 from test_history_gpu import BF16, DTYPES, F32, I32, cache_case, generator, ints, normal
 
 pytestmark = pytest.mark.gpu
@@ -195,3 +195,82 @@ def test_a_cache_that_is_copied_is_warned_about(seq, new):
     for caches in ((apart[0], vc), (kc, apart[1]), apart):
         with pytest.warns(UserWarning, match="copied whole"):
             assert torch.equal(seq.paged_attention(q, *caches, table, lens), want)
+
+
+@pytest.mark.parametrize("bad", [(1 << 31) - 1, -1, -(1 << 31), 49])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_an_entry_whose_length_is_out_of_range_has_no_keys(seq, dtype, bad):
+    """The largest and the smallest number that a length can be, too: nothing is stored, zeros come back, and the other
+    entries are as they would be."""
+    gen, dim = generator(94), 32
+    kc, vc, table = cache_case(gen, 2, [48, 48], 16, 2, dim, dtype, garbage=0.0)
+    k, q = normal(gen, 2, 40, 2, dim, dtype=dtype).cuda(), normal(gen, 2, 40, 4, dim, dtype=dtype).cuda()
+    freqs, good, lens = seq.rotary_frequencies(dim), ints(48, 45).cuda(), ints(bad, 45).cuda()
+    stored = [(kc.cuda(), vc.cuda()) for _ in range(2)]
+    turned = [seq.cache_append(k, k, *c, table.cuda(), n, q=q, freqs=freqs) for c, n in zip(stored, (good, lens))]
+    assert not bool(turned[1][0].any()) and torch.equal(turned[1][1], turned[0][1])
+    for t, was, now in zip((kc, vc), *stored):
+        assert torch.equal(now[table[0].long().cuda()].cpu(), t[table[0].long()])
+        assert torch.equal(now[table[1].long().cuda()], was[table[1].long().cuda()])
+    for rows in (q, q[:, -1:]):
+        for how in ({}, {"window": 9, "sinks": 2}, {"causal": False}):
+            want = seq.paged_attention(rows, *stored[1], table.cuda(), good, return_lse=True, **how)
+            got = seq.paged_attention(rows, *stored[1], table.cuda(), lens, return_lse=True, **how)
+            assert not bool(got[0][0].any()) and bool((got[1][0] == -float("inf")).all())
+            assert torch.equal(got[0][1], want[0][1]) and torch.equal(got[1][1], want[1][1])
+    ends = [ints(40, 30).cuda(), ints(bad, 30).cuda()]
+    (want, wl), (got, gl) = (seq.self_attention(q, k, k, lens=n, window=9, sinks=2, return_lse=True) for n in ends)
+    assert not bool(got[0].any()) and bool((gl[0] == -float("inf")).all()) and torch.equal(got[1], want[1])
+    grads = [seq.self_attention_backward(q, q, k, k, o, x, lens=n, window=9, sinks=2)
+             for o, x, n in ((want, wl, ends[0]), (got, gl, ends[1]))]
+    for a, b in zip(*grads):
+        assert not bool(b[0].any()) and torch.equal(b[1], a[1])
+
+
+@pytest.mark.parametrize("length,group,dim", [(64, 1, 64), (50, 2, 64), (64, 1, 128), (33, 4, 128)])
+def test_short_histories_take_delta_from_the_weights(seq, length, group, dim):
+    """bfloat16, one key with nearly all the weight: what is left of its dP after delta is small, and delta from out
+    would bring out's rounding into it. Histories within one tile of keys have it from P and dP, all in 32 bits; the
+    bound has no rounding to bfloat16 but that of dS where it meets K or Q, and of the results.
+
+    P: its score's error, twice, and L's (history_plain). dP: d products, from -delta. delta: P's and dP's errors, and
+    a sum of as many terms as there are keys."""
+    gen = generator(length, dim, 95)
+    q = (normal(gen, length, group, dim) * 0.3 + 1).to(BF16)
+    k, v, grad = (normal(gen, length, h, dim) for h in (1, 1, group))
+    k, scale = k * 0.3, dim**-0.5
+    k[0] = 7 / (dim * scale)
+    k, v, grad = (t.to(BF16) for t in (k, v, grad))
+    dev = [t[None].cuda() for t in (q, k, v)]
+    o, lse = seq.self_attention(*dev, return_lse=True)
+    dq, dk, _ = seq.self_attention_backward(grad[None].cuda(), *dev, o, lse)
+    ok, u, n = torch.ones(length, length).tril().bool(), U[BF16], length
+    K, V = k[:, 0].double(), v[:, 0].double()
+    tells_apart, want_k, err_k = False, 0.0, 1e-30
+    for h in range(group):
+        Q, G = q[:, h].double(), grad[:, h].double()
+        S = scale * Q @ K.T
+        eS = (dim + 6) * U32 * scale * (Q.abs() @ K.abs().T) + 4 * U32 * S.abs()
+        L = torch.logsumexp(S.masked_fill(~ok, -float("inf")), -1, keepdim=True)
+        P = torch.where(ok, torch.exp(S - L), 0.0)
+        eP = 2 * eS.masked_fill(~ok, 0).amax(-1, keepdim=True) + eS + (n + 12) * U32
+        eP = (eP + eP.amax(-1, keepdim=True) + 8 * U32 * (L.abs() + S.abs() + 1)) * 1.1
+        dP, aP = G @ V.T, G.abs() @ V.abs().T
+        delta = (P * dP).sum(-1, keepdim=True)
+        edP = (dim + 2) * U32 * (aP + delta.abs())
+        edelta = (P * (eP * dP.abs() + (1 + eP) * edP + n * U32 * dP.abs())).sum(-1, keepdim=True)
+        dS = P * (dP - delta)
+        edS = dS.abs() * (eP + 2 * U32) + P * (1 + eP) * (edP + edelta)
+        edS = edS + u * (dS.abs() + edS)
+        out = (P @ V).to(BF16).double()   # what delta from out would make of it
+        wrong = P * (dP - (G * out).sum(-1, keepdim=True))
+        want = scale * dS @ K
+        bound = scale * (edS + (n + 2) * U32 * dS.abs()) @ K.abs()
+        bound = bound + u * (want.abs() + bound) + 1e-30
+        within(dq[0, :, h], want, bound, what=("dq", h))
+        tells_apart |= bool(((scale * wrong @ K - want).abs() > bound).any())
+        want_k = want_k + scale * dS.T @ Q
+        err_k = err_k + scale * (edS + (n * group + 2) * U32 * dS.abs()).T @ Q.abs()
+    err_k = err_k + u * (want_k.abs() + err_k)
+    within(dk[0, :, 0], want_k, err_k, what="dk")
+    assert tells_apart   # (dQ's bound: over dK's many rows the roundings of out may cancel)
