@@ -15,8 +15,6 @@
 // in that order.
 #pragma once
 
-#include <type_traits>
-
 #include "attn.h"
 #include "divide.h"
 
@@ -58,6 +56,7 @@ struct BandArgs {
 constexpr int kBandWaves = 4, kBandRows = 32 * kBandWaves;
 constexpr int kDies = 8, kDieBits = 3;
 constexpr int kLeastTiles = 2;      // tiles of keys a split has where there are so many
+constexpr int kMaxSplits = 256;     // parts that keys or rows are split into
 inline int band_dp(int head_dim) { return (head_dim + 31) / 32 * 32; }
 // Keys of a tile.  (float32 of more than 32 elements: 32, since its products take eight times
 // bfloat16's time and a few tiles must go round: 33 entries of up to 999 keys, 50 rows, 6 heads
@@ -101,9 +100,6 @@ inline int band_access(int dtype, int head_dim, std::initializer_list<const void
 void launch_band_fwd(int dtype, bool paged, int access, const BandArgs& a, hipStream_t s);
 
 namespace {
-
-template <int N>
-using Const = std::integral_constant<int, N>;
 
 __device__ __forceinline__ int page_of(const BandArgs& a, int key) { return divided(key, a.by_page); }
 
@@ -477,8 +473,7 @@ struct KeyStage {
   static __device__ __forceinline__ Frag<T> at_bytes(const T* base, unsigned bytes) {
     return *reinterpret_cast<const Frag<T>*>(reinterpret_cast<const char*>(base) + bytes);
   }
-  __device__ __forceinline__ void load(const BandArgs& a, const T* kb, const T* vb, int first, int len,
-                                       unsigned long long bits) {
+  __device__ __forceinline__ void load(const BandArgs& a, const T* kb, const T* vb, int first, int len) {
     const T* tile_k = kb + (long long)first * a.ks[1];
     const T* tile_v = vb + (long long)first * a.vs[1];
 #pragma unroll

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_
   if (i0 < i1) {
     const int first = walk.tile(i0) * K;
     bits = band_bits(a, e, b, first, lane);
-    st.load(a, kb, vb, first, e.len, bits);
+    st.load(a, kb, vb, first, e.len);
   }
   Frag<T> q[KK], g[KK];  // (after the first keys' loads, which take longer)
   float delta = 0.f;
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(kThreads, (kBackwardWaves<T, DP>)) void k_band_bwd_
     {  // (after the last tile, that one again: a branch would have its loads waited for)
       const int next = walk.tile(std::min(i + 1, i1 - 1)) * K;
       bits = band_bits(a, e, b, next, lane);
-      st.load(a, kb, vb, next, e.len, bits);
+      st.load(a, kb, vb, next, e.len);
     }
     if (none_seen<K>(a, reach, first)) continue;
     // delta from out carries out's rounding, which a key with nearly all the weight
@@ -535,8 +535,6 @@ void launch_bwd_dp(int access, const BandArgs& a, hipStream_t s) {
     default: return launch_bwd_by<T, 128>(access, a, s);
   }
 }
-
-constexpr int kMaxSplits = 256;
 
 recis_status check_self(const recis_self_attn_desc* d) {
   if (!d || !dtype_known(d->dtype) || d->batch < 0 || d->len < 0 || d->q_heads < 1 || d->kv_heads < 1 ||

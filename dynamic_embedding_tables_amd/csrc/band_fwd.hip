@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     const int first = walk.tile(i0) * K;
     if constexpr (PAGED) st.ask_pages(a, table, first, e.len);
     bits = keys_there(first);
-    st.load(a, kb, vb, first, e.len, bits);
+    st.load(a, kb, vb, first, e.len);
     if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i0 + 1, i1 - 1)) * K, e.len);
   }
   Frag<T> q[KK];  // (after the first keys' loads, which take longer)
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<T, DP>)) void k_band_fwd(B
     {  // (after the last tile, that one again: a branch would have its loads waited for)
       const int next = walk.tile(std::min(i + 1, i1 - 1)) * K;
       bits = keys_there(next);
-      st.load(a, kb, vb, next, e.len, bits);
+      st.load(a, kb, vb, next, e.len);
       if constexpr (PAGED) st.ask_pages(a, table, walk.tile(std::min(i + 2, i1 - 1)) * K, e.len);
     }
     if (none_seen<K>(a, reach, first)) continue;

@@ -317,8 +317,6 @@ void launch_few_dp(int access, const BandArgs& a, hipStream_t s) {
 }
 
 // ----------------------------------------------------------- sizes, launches
-constexpr int kMaxSplits = 256;
-
 struct PagedPlan {
   bool few;
   int row_tiles, splits;

@@ -95,8 +95,7 @@ struct RotaryArgs {
   Turns turns;
   int64_t tokens, seq;
   int64_t xs[3], os[3], ps[2];  // batch, position, head
-  int per_block, heads;
-  int turned, items;  // of a head: V pairs each, and with the rest's V elements each
+  int per_block, turned;  // turned: items of a head that are V pairs, the rest's being V elements
   Div by_half, by_token, by_head;
 };
 
@@ -137,8 +136,7 @@ struct AppendArgs {
   int64_t qs[3], qos[3], ks[3], vs[3];  // batch, position, head
   int64_t kcs[3], vcs[3];               // page, slot, head
   int batch, new_len, width, page_size;
-  int q_heads, kv_heads, head_dim;
-  int per_block, turned, items, copied;  // items of a head of q and k, and of one of v
+  int q_heads, per_block, turned;  // turned: as in RotaryArgs, of a head of q and k
   Div by_half, by_token, by_head, by_v_token, by_copied;  // by_token: of q and k
 };
 
@@ -359,17 +357,16 @@ recis_status recis_rotary(const recis_rotary_desc* d, int32_t backward, const vo
   }
   a.ps[0] = d->pos_strides[0];
   a.ps[1] = d->pos_strides[1];
-  a.heads = d->heads;
   const int v = turn_width(size, d->head_dim, a.turns.half, {x, out},
                            {a.xs[0], a.xs[1], a.xs[2], a.os[0], a.os[1], a.os[2]});
   a.turned = a.turns.half / v;
-  a.items = a.turned + (same ? 0 : (d->head_dim - d->rot_dim) / v);  // in place the rest is there
-  if (a.items == 0) return RECIS_OK;
-  const int64_t per_token = (int64_t)d->heads * a.items;
+  const int items = a.turned + (same ? 0 : (d->head_dim - d->rot_dim) / v);  // of a head (in place the rest is there)
+  if (items == 0) return RECIS_OK;
+  const int64_t per_token = (int64_t)d->heads * items;
   a.per_block = tokens_a_block(a.tokens, per_token, a.turns.half);
   a.by_half = div_by(std::max(1, a.turns.half));
   a.by_token = div_by(per_token);
-  a.by_head = div_by(a.items);
+  a.by_head = div_by(items);
   const int64_t blocks = (a.tokens + a.per_block - 1) / a.per_block;
   if (blocks > kMaxBlocks) return RECIS_ERR_UNSUPPORTED;
   RECIS_BY_WIDTH(launch_rotary, d->dtype, v, d->interleaved != 0, a, grid_of(blocks), s);
@@ -428,8 +425,6 @@ recis_status recis_cache_append(const recis_append_desc* d, const void* q, const
   a.width = d->table_width;
   a.page_size = d->page_size;
   a.q_heads = d->q_heads;
-  a.kv_heads = d->kv_heads;
-  a.head_dim = d->head_dim;
   int w = turn_width(size, d->head_dim, a.turns.half, {k, v, k_cache, v_cache},
                      {a.ks[0], a.ks[1], a.ks[2], a.vs[0], a.vs[1], a.vs[2], a.kcs[0], a.kcs[1], a.kcs[2], a.vcs[0],
                       a.vcs[1], a.vcs[2]});
@@ -437,15 +432,15 @@ recis_status recis_cache_append(const recis_append_desc* d, const void* q, const
     w = std::min(w, turn_width(size, d->head_dim, a.turns.half, {q, q_out},
                                {a.qs[0], a.qs[1], a.qs[2], a.qos[0], a.qos[1], a.qos[2]}));
   a.turned = a.turns.half / w;
-  a.items = a.turned + (d->head_dim - d->rot_dim) / w;
-  a.copied = d->head_dim / w;
-  const int64_t per_token = (int64_t)(d->q_heads + d->kv_heads) * a.items + (int64_t)d->kv_heads * a.copied;
+  // items of a head of q and k, and of one of v
+  const int items = a.turned + (d->head_dim - d->rot_dim) / w, copied = d->head_dim / w;
+  const int64_t per_token = (int64_t)(d->q_heads + d->kv_heads) * items + (int64_t)d->kv_heads * copied;
   a.per_block = tokens_a_block(rows, per_token, a.turns.half);
   a.by_half = div_by(std::max(1, a.turns.half));
-  a.by_token = div_by((int64_t)(d->q_heads + d->kv_heads) * a.items);
-  a.by_head = div_by(a.items);
-  a.by_v_token = div_by((int64_t)d->kv_heads * a.copied);
-  a.by_copied = div_by(a.copied);
+  a.by_token = div_by((int64_t)(d->q_heads + d->kv_heads) * items);
+  a.by_head = div_by(items);
+  a.by_v_token = div_by((int64_t)d->kv_heads * copied);
+  a.by_copied = div_by(copied);
   const int64_t blocks = (rows + a.per_block - 1) / a.per_block;
   if (blocks > kMaxBlocks) return RECIS_ERR_UNSUPPORTED;
   RECIS_BY_WIDTH(launch_append, d->dtype, w, d->interleaved != 0, a, grid_of(blocks), s);
