@@ -355,6 +355,7 @@ recis_status recis_rotary(const recis_rotary_desc* d, int32_t backward, const vo
     a.os[i] = stride_of(d->out_strides[i], axes[i]);
     same = same && a.xs[i] == a.os[i];
   }
+  if (x == out && !same) return RECIS_ERR_INVALID_ARG;
   a.ps[0] = d->pos_strides[0];
   a.ps[1] = d->pos_strides[1];
   const int v = turn_width(size, d->head_dim, a.turns.half, {x, out},
@@ -419,6 +420,7 @@ recis_status recis_cache_append(const recis_append_desc* d, const void* q, const
     a.vs[i] = stride_of(d->v_strides[i], kv_axes[i]);
     a.kcs[i] = stride_of(d->k_cache_strides[i], cache_axes[i]);
     a.vcs[i] = stride_of(d->v_cache_strides[i], cache_axes[i]);
+    if (d->q_heads && q == q_out && a.qs[i] != a.qos[i]) return RECIS_ERR_INVALID_ARG;
   }
   a.batch = d->batch;
   a.new_len = d->new_len;

@@ -457,7 +457,8 @@ def rotary(x, freqs, positions=None, interleaved: bool = False, amplitude: float
     """Rotary positions of heads x [seq, heads, head_dim] or [batch, seq, heads, head_dim]: pair i of each head turned
     by positions * freqs[i], the elements past 2 * len(freqs) copied.  Pairs are (i, i + len(freqs)), or (2i, 2i + 1)
     interleaved.  positions: int64 over x's leading axes or [seq] (default: 0 .. seq - 1); freqs: float64, as
-    ``rotary_frequencies`` makes them; amplitude multiplies what is turned.  out may be x."""
+    ``rotary_frequencies`` makes them; amplitude multiplies what is turned.  out may be x, or shares no element
+    with it."""
     if stream is not None:
         with _on(stream, x, freqs, positions, out):
             return rotary(x, freqs, positions, interleaved, amplitude, out)
@@ -467,7 +468,8 @@ def rotary(x, freqs, positions=None, interleaved: bool = False, amplitude: float
 
 def rotary_backward(grad_out, freqs, positions=None, interleaved: bool = False, amplitude: float = 1.0, out=None,
                     stream=None):
-    """The gradient of rotary's x: grad_out turned back.  Arguments as there; out may be grad_out."""
+    """The gradient of rotary's x: grad_out turned back.  Arguments as there; out may be grad_out, or shares no element
+    with it."""
     if stream is not None:
         with _on(stream, grad_out, freqs, positions, out):
             return rotary_backward(grad_out, freqs, positions, interleaved, amplitude, out)
@@ -571,9 +573,9 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_offsets=None, ma
     having more than max_q_len rows; q_heads is a multiple of the cache's kv_heads.  Causal, the last row of entry b is
     at position kv_lens[b] - 1 and each row sees the keys up to its position: with window the latest `window` of them,
     itself among them, and the first `sinks` ones.  Not causal (candidates reading a history), every row sees all
-    kv_lens[b] keys.  Returns q's shape (in out, if given) and with return_lse the float32 log of the sums of
-    exponentials [.., q_heads].  Rows that see no key, at negative positions or of an entry without keys, give zeros
-    and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf.
+    kv_lens[b] keys.  Returns q's shape (in out, if given, which shares no element with the others) and with return_lse
+    the float32 log of the sums of exponentials [.., q_heads].  Rows that see no key, at negative positions or of an
+    entry without keys, give zeros and -inf.  Packed rows of no entry are not written: in a result that the call allocates they are zeros and -inf.
     Keys before the window that no new row sees are not read, nor their pages' numbers: such pages may be given away.
     Keys of another page whose number is out of range do not count (and are recorded in error).  A cache whose heads
     are not contiguous is copied whole first, with a warning."""

@@ -627,7 +627,8 @@ typedef struct {
 } recis_rotary_desc;
 
 /* backward 0: out = the turned x.  Else x is a gradient and out that of what was
- * turned: the same with t negative.  out may be x (with equal strides). */
+ * turned: the same with t negative.  out may be x, with equal strides (else
+ * INVALID_ARG), or shares no element with it. */
 recis_status recis_rotary(const recis_rotary_desc* desc, int32_t backward, const void* x, void* out, hipStream_t s);
 
 /* A paged cache: key j of batch entry b lies in slot j % page_size of page
@@ -644,10 +645,10 @@ recis_status recis_rotary(const recis_rotary_desc* desc, int32_t backward, const
  *
  * recis_cache_append stores the new keys (turned by their positions, where
  * rot_dim > 0: recis_rotary) and values, and, where q_heads > 0, writes the turned
- * queries of the same rows to q_out (which may be q).  Padding rows, rows of no
- * entry and rows whose page is out of range are not stored; rows of no entry get
- * zeros in q_out (with batch 0 nothing is written, here and below).  Entries must
- * not share the slots that they append to. */
+ * queries of the same rows to q_out (which may be q, with equal strides).  Padding
+ * rows, rows of no entry and rows whose page is out of range are not stored; rows
+ * of no entry get zeros in q_out (with batch 0 nothing is written, here and below).
+ * Entries must not share the slots that they append to. */
 typedef struct {
   int32_t dtype;              /* of q, k, v and the caches */
   int32_t batch;
@@ -755,8 +756,9 @@ int64_t recis_self_attn_workspace_bytes(const recis_self_attn_desc* desc, int32_
 /* out and lse (float32 [batch, len, q_heads] or [rows, q_heads], may be NULL) as
  * recis_cross_attn_fwd.  A row that sees no key, past its entry's length among
  * them, gives 0 and -infinity; packed rows of no entry get 0 in out and nothing in
- * lse, and so do those of an entry whose offsets are out of range.  What masked positions and positions past the length hold is not looked at;
- * a value that is not finite may reach rows of its own entry that do not see it. */
+ * lse, and so do those of an entry whose offsets are out of range.  What masked
+ * positions hold as keys, and positions past the length, is not looked at; a value
+ * that is not finite may reach rows of its own entry that do not see it. */
 recis_status recis_self_attn_fwd(const recis_self_attn_desc* desc, const void* q, const void* k, const void* v,
                                  void* out, float* lse, void* workspace, int64_t workspace_bytes, hipStream_t s);
 

@@ -80,3 +80,22 @@ def test_divisions_by_multiplication(tmp_path):
     subprocess.check_call(["g++", "-O1", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)])
     wrong, checked = map(int, subprocess.check_output([str(exe)], text=True).split())
     assert wrong == 0 and checked > 1_000_000
+
+
+def test_in_place_with_other_strides_is_refused(lib):
+    """out may be x, q_out q: then each element is read where it is written. With other strides it is not."""
+    import ctypes as C
+
+    from test_history_cpu import APPEND, INVALID, P, ROTARY, described
+    L = lib.load_library()
+    still = dict(ROTARY, rot_dim=0, freqs=None)   # (in place, with nothing that turns, there is no work to do)
+    assert L.recis_rotary(C.byref(described(lib.recis_rotary_desc, still)), 0, P, P, None) == 0
+    one = dict(still, batch=1)
+    assert L.recis_rotary(C.byref(described(lib.recis_rotary_desc, one, out_strides=(7, 32, 8))), 0, P, P, None) == 0
+    for strides in ((160, 8, 32), (160, 32, 9), (0, 32, 8)):
+        for values in (ROTARY, still):
+            d = described(lib.recis_rotary_desc, values, out_strides=strides)
+            for backward in (0, 1):
+                assert L.recis_rotary(C.byref(d), backward, P, P, None) == INVALID, strides
+        d = described(lib.recis_append_desc, APPEND, q_out_strides=strides)
+        assert L.recis_cache_append(C.byref(d), P, P, P, P, P, P, None) == INVALID, strides
