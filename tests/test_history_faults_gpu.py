@@ -274,3 +274,53 @@ def test_short_histories_take_delta_from_the_weights(seq, length, group, dim):
     err_k = err_k + u * (want_k.abs() + err_k)
     within(dk[0, :, 0], want_k, err_k, what="dk")
     assert tells_apart   # (dQ's bound: over dK's many rows the roundings of out may cancel)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_packed_calls_captured_into_a_graph(seq, dtype):
+    """Packed histories and packed new events: the graph is replayed with other entries in the same rows."""
+    gen, dim, rows = generator(96), 32, 120
+    s = {"q": normal(gen, rows, 4, dim, dtype=dtype).cuda(), "k": normal(gen, rows, 2, dim, dtype=dtype).cuda(),
+         "g": normal(gen, rows, 4, dim, dtype=dtype).cuda(), "off": ints(0, 50, 50, 120).cuda(), "at": ints(60, 9, 200).cuda(),
+         "kc": torch.zeros(30, 16, 2, dim, dtype=dtype).cuda(), "vc": torch.zeros(30, 16, 2, dim, dtype=dtype).cuda(),
+         "table": torch.randperm(30, generator=gen)[:30].view(3, 10).to(I32).cuda()}
+    s["table"], s["kc"], s["vc"] = (t.repeat(*n).contiguous() for t, n in (
+        (s["table"], (1, 2)), (s["kc"], (2, 1, 1, 1)), (s["vc"], (2, 1, 1, 1))))
+    s["table"][:, 10:] += 30
+    freqs = seq.rotary_frequencies(dim)
+
+    def step():
+        band = {"offsets": s["off"], "max_len": 120, "window": 20, "sinks": 3}
+        o, lse = seq.self_attention(s["q"], s["k"], s["k"], return_lse=True, **band)
+        grads = seq.self_attention_backward(s["g"], s["q"], s["k"], s["k"], o, lse, **band)
+        turned = seq.cache_append(s["k"], s["k"], s["kc"], s["vc"], s["table"], s["at"], q=s["q"], q_offsets=s["off"],
+                                  freqs=freqs)
+        where = (s["kc"], s["vc"], s["table"], s["at"])
+        many = seq.paged_attention(turned, *where, q_offsets=s["off"], max_q_len=120, return_lse=True)
+        few = seq.paged_attention(turned, *where, q_offsets=s["few"], max_q_len=3, window=30, sinks=1, return_lse=True)
+        return [o, lse, *grads, turned, *many, *few]
+
+    s["few"] = ints(0, 3, 3, 5).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    ends = [(0, 50, 50, 120), (0, 1, 2, 3), (7, 60, 90, 100), (0, 0, 0, 0), (0, 120, 120, 120)]
+    for i, off in enumerate(ends):
+        for name in ("q", "k", "g"):
+            s[name].copy_(normal(gen, *s[name].shape, dtype=dtype))
+        s["off"].copy_(ints(*off)), s["few"].copy_(ints(*[(0, 3, 3, 5), (1, 2, 3, 4), (0, 0, 0, 2)][i % 3]))
+        s["at"].copy_(ints(60 + 40 * i, 70, 250))
+        kc, vc = s["kc"].clone(), s["vc"].clone()
+        want = step()
+        stored = s["kc"].clone(), s["vc"].clone()
+        s["kc"].copy_(kc), s["vc"].copy_(vc)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s["kc"], stored[0]) and torch.equal(s["vc"], stored[1])
+        for j, (a, b) in enumerate(zip(want, held)):
+            assert torch.equal(a, b), (off, j)
