@@ -58,9 +58,9 @@ constexpr int kDies = 8, kDieBits = 3;
 constexpr int kLeastTiles = 2;      // tiles of keys a split has where there are so many
 constexpr int kMaxSplits = 256;     // parts that keys or rows are split into
 inline int band_dp(int head_dim) { return (head_dim + 31) / 32 * 32; }
-// Keys of a tile.  (float32 of more than 32 elements: 32, since its products take eight times
-// bfloat16's time and a few tiles must go round: 33 entries of up to 999 keys, 50 rows, 6 heads
-// of 40: 49 us with 64, 39 with 32.)
+// Keys of a tile.  (float32 of more than 32 elements: 32, since its products hold the matrix
+// unit sixteen times as long as bfloat16's and a few tiles must go round: 33 entries of up to
+// 999 keys, 50 rows, 6 heads of 40: 49 us with 64, 39 with 32.)
 inline int band_keys(int dtype, int head_dim) { return dtype == RECIS_DTYPE_F32 && head_dim > 32 ? 32 : 64; }
 // The grid of a launch of `tiles` tiles a pair in `splits` parts each.
 inline dim3 band_grid(BandArgs* a, int64_t tiles, int64_t splits) {
@@ -300,8 +300,8 @@ __device__ __forceinline__ f32x16 mma32(f32x8 a, f32x8 b, f32x16 c) {
   for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
   return c;
 }
-// Whether chunk c of a head is worth its products: float32's take eight instructions, of
-// twice bfloat16's length, so those past the head are left out.
+// Whether chunk c of a head is worth its products: float32's take eight instructions, each of
+// twice bfloat16's cycles, so those past the head are left out.
 template <typename T>
 __device__ __forceinline__ bool chunk_counts(int c, int dim) {
   return sizeof(T) == 2 || c * 16 < dim;

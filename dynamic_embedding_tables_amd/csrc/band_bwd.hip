@@ -14,9 +14,12 @@
 // window are walked by blocks of their own (FAR), split over the rows, whose four waves
 // share 32 keys; the parts are added in order at the end.
 //
-// Bound by dependent products, exponentials and LDS reads at two or three waves a SIMD
-// (registers hold the operands of 32 rows or keys and both sums): the matrix unit is busy
-// about a quarter of the cycles.  32 entries of up to 4096 positions, 8 heads of 64, window
+// Bound by dependent products, exponentials and LDS reads at few waves a SIMD (registers hold
+// the operands of 32 rows or keys and both sums): dQ's kernel has two to four; dK and dV's two
+// to four at heads of up to 32, two up to 64, and above that one in most forms, above 96 in
+// all.  In float32 dK and dV's spills 72 to 92 bytes a lane at heads of 33 to 64, its far form
+// 168 to 196 there, and dQ's 248 to 288 at heads above 96.  The matrix unit is busy about a
+// quarter of the cycles.  32 entries of up to 4096 positions, 8 heads of 64, window
 // 512, 4 sinks, bfloat16: dQ 235 us, dK and dV 250 (at three waves, spilling, 392; tiles of
 // 32 rows 281), the sinks' far rows 38 (memory: they read Q and dO once more; in parts of
 // 2 steps instead of 8 62; in the near rows' launch no less), the parts 5.  Causal, 4096

@@ -21,9 +21,9 @@
 // exponentials it would take 1503 us, without loads and barriers 1110, with the products
 // and their LDS reads alone 960).  Short windows are bound by the tiles at a window's
 // ends, computed whole or by halves of 32 keys, and by each block's start: window 512 of
-// up to 4096, 8 heads of 64 160 us, of up to 1000 packed, window 128, 4 heads of 32 97 us.
+// up to 4096, 8 heads of 64 160 us, of up to 1000 packed, window 128, 4 heads of 32 90 us.
 // Over a cache, 32 entries of up to 512 rows and 8192 keys, 16 heads of 128 that share 4:
-// 425 to 460 us, 580 to 630 TFLOP/s.  Float32: 58 to 85 TFLOP/s of the 154 that a large
+// 406 to 436 us, 620 to 660 TFLOP/s.  Float32: 51 to 95 TFLOP/s of the 154 that a large
 // product reaches, padded head sizes and half-seen tiles counted as lost.
 //
 // Tried, for the same time: raised wave priority around the products, a fixed order of

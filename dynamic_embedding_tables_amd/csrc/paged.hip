@@ -15,10 +15,12 @@
 // The keys an entry sees are split evenly over `splits` blocks, whatever its length;
 // an entry short enough for one needs no join.
 //
-// 64 single events over up to 8192 keys, 16 heads of 128 that share 4, bfloat16: 116 us,
-// 4.6 TB/s, where a large copy reaches 4.9 (all pairs of an entry on one die: a pair's
-// blocks side by side 122 us, the pairs of a tile 127).  4 events over up to 200 keys, 4
-// heads of 32, float32: 6 us, the launch and three dependent reads.
+// 64 single events over up to 8192 keys, 16 heads of 128 that share 4, bfloat16: 120 us a
+// call, 4.5 TB/s, where a large copy reaches 4.9 (all pairs of an entry on one die, a pair's
+// blocks side by side; with the pairs of a tile side by side 127).  The same over 8192 keys
+// each in float32, 2.15 GB: 399 to 437 us, 4.9 to 5.4 TB/s, although heads above 96 leave it
+// one wave a SIMD.  4 events over up to 200 keys, 4 heads of 32, float32: 6 us, the launch
+// and three dependent reads.
 #include <algorithm>
 #include <cmath>
 
